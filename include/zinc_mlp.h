@@ -300,6 +300,132 @@ int zinc_moe_route_topk(const float* logits, int32_t M, int32_t n_experts, int32
                         int32_t* expert_ids, float* expert_weights, void* stream);
 
 /*
+ * The expert layer in FP8, beside the Q4_K one: the token permutation as calls
+ * of its own (with its gradients), a block quantiser, block-scaled products and
+ * the expert call built of them.
+ *
+ * Element types: ZINC_F16, ZINC_BF16, ZINC_F32 name the type of the activations
+ * (and of outputs) a call reads and writes; every other value -> ZINC_ERR_ARG.
+ *
+ * FP8 values are e4m3 bytes (OCP: bias 7, largest value 448, 0x7F / 0xFF NaN),
+ * with one fp32 scale per block of 128; a value stands for q * scale:
+ *   activations [rows x cols]: scales [rows x ceil(cols / 128)], one per row and
+ *     128 columns;
+ *   weights [n x k], the contraction dimension last: scales [ceil(n / 128) x
+ *     ceil(k / 128)], one per 128 x 128 tile; experts' matrices and their scales
+ *     lie back to back.
+ * The last block of a dimension may be cut short.  Scales may be any fp32 values.
+ */
+enum { ZINC_F16 = 0, ZINC_BF16 = 1, ZINC_F32 = 2 };
+
+/*
+ * Sort of routed slots by expert.  Slot i = t * top_k + s (token t's s-th expert,
+ * expert_ids int32 [M x top_k]) gets the row
+ *   slot_row[i] = #{slots of smaller experts} + #{earlier slots of its expert},
+ * a stable order, so the result is a function of the ids alone.  Written:
+ *   offsets   int32 [n_experts + 1]: expert e's rows are offsets[e] .. offsets[e + 1] - 1
+ *   slot_row  int32 [M x top_k]: a slot's row, -1 where its id is outside [0, n_experts)
+ *             (1 is then ORed into *dev_error as in zinc_moe_q4k_experts; may be NULL)
+ *   row_slot  int32 [M x top_k]: a row's slot, -1 for the rows from offsets[n_experts] on
+ * An expert may occur more than once in a token; each slot has a row.  M == 0 writes the
+ * offsets (zeros) and needs no other pointer.  1 <= n_experts <= 1024, 1 <= top_k <= 1024, M * top_k <=
+ * 2^24 (else ZINC_ERR_ARG; the size query returns 0, as it does where no workspace is needed:
+ * workspace may then be NULL).  int32 pointers are 4-byte aligned, the workspace 16.
+ */
+size_t zinc_moe_sort_workspace_size(int32_t M, int32_t top_k, int32_t n_experts);
+int zinc_moe_sort(const int32_t* expert_ids, int32_t M, int32_t top_k, int32_t n_experts, int32_t* offsets,
+                  int32_t* slot_row, int32_t* row_slot, void* workspace, size_t workspace_bytes,
+                  int32_t* dev_error, void* stream);
+
+/*
+ * Gather of token rows into expert order: xs[slot_row[t, s]] = x[t], xs [M * top_k x
+ * hidden], x [M x hidden].  Rows that no slot names are left as they were, and
+ * values of slot_row outside [0, M * top_k) are skipped.  slot_row names a row at
+ * most once (as zinc_moe_sort writes it).
+ * The gradient of x is zinc_moe_combine of the gradient of xs without weights:
+ * dx[t] = sum_s dxs[slot_row[t, s]].
+ * _fp8: the same rows quantised on the way, one scale per row and 128 columns
+ * (zinc_fp8_quantize's definition): q [M * top_k x hidden], scales [M * top_k x
+ * ceil(hidden / 128)].
+ * hidden: a multiple of 8 (_fp8: of 16) up to 65536, else ZINC_ERR_SHAPE.  M * top_k <=
+ * 2^24.  No workspace.
+ */
+int zinc_moe_gather(const void* x, int32_t type, int32_t M, int32_t top_k, int32_t hidden, const int32_t* slot_row,
+                    void* xs, void* stream);
+int zinc_moe_gather_fp8(const void* x, int32_t type, int32_t M, int32_t top_k, int32_t hidden,
+                        const int32_t* slot_row, void* q, float* scales, void* stream);
+
+/*
+ * The way back: y[t] = sum_s expert_weights[t, s] ys[slot_row[t, s]] (weights NULL:
+ * the plain sum), in fp32 in the order of s, rounded once.  Slots whose row is
+ * outside [0, M * top_k) add nothing; a token without any gets zeros.
+ * _backward: from dy [M x hidden] and ys, the gradients
+ *   dys[slot_row[t, s]] = expert_weights[t, s] dy[t]   (other rows are left as they were)
+ *   dweights[t, s]      = <dy[t], ys[slot_row[t, s]]>  (fp32 [M x top_k]; 0 for skipped slots)
+ * hidden a multiple of 8 up to 65536.  ys, y, dy and dys have the one type.
+ */
+int zinc_moe_combine(const void* ys, int32_t type, int32_t M, int32_t top_k, int32_t hidden,
+                     const int32_t* slot_row, const float* expert_weights, void* y, void* stream);
+int zinc_moe_combine_backward(const void* dy, const void* ys, int32_t type, int32_t M, int32_t top_k, int32_t hidden,
+                              const int32_t* slot_row, const float* expert_weights, void* dys, float* dweights,
+                              void* stream);
+
+/*
+ * Block quantiser: q = e4m3(x / s), to nearest, ties to even, x [rows x cols] row-major.
+ * block_rows 1 (activations: one scale per row and 128 columns) or 128 (weights: one
+ * per 128 x 128 tile).  s is the smallest power of two, at least 2^-126, with
+ * max|x| <= 448 s over the block's finite values; 1 where they are all zero.
+ * x / s is exact then, so e4m3's rounding is the only one.  Infinities and NaN
+ * become NaN and leave their block's other values alone.
+ * cols: a multiple of 16 up to 65536 (else ZINC_ERR_SHAPE); rows >= 0.
+ */
+int zinc_fp8_quantize(const void* x, int32_t type, int32_t rows, int32_t cols, int32_t block_rows, void* q,
+                      float* scales, void* stream);
+
+/*
+ * Product of FP8 matrices, c[M x N] of out_type:
+ *   c[m][n] = sum_kb a_scales[m][kb] w_scales[n / 128][kb] sum_{k in block kb} a[m][k] w[n][k]
+ * accumulated in fp32 and rounded once; a [M x K] activations, w [N x K] weights.
+ * zinc_moe_gemm_fp8: w holds n_experts matrices, and row r of a [rows x K] with
+ * offsets[e] <= r < offsets[e + 1] takes expert e's (offsets int32 [n_experts + 1] on
+ * the GPU, as zinc_moe_sort writes them; the host never reads them).  Rows outside
+ * every range are left as they were; offsets are cut to [0, rows] and have to ascend.
+ * The result is a function of the inputs alone, run after run.
+ * K a multiple of 16 up to 65536, 1 <= N <= 2^20 (else ZINC_ERR_SHAPE); 0 <= M <= 2^24,
+ * n_experts <= 1024 (else ZINC_ERR_ARG).  a, w, c and the workspace are 16-byte
+ * aligned, the others 4.  The size queries return 0 where no workspace is needed
+ * (workspace may then be NULL) and for arguments out of range.
+ */
+size_t zinc_gemm_fp8_workspace_size(int32_t M, int32_t N, int32_t K);
+int zinc_gemm_fp8(const void* a, const float* a_scales, const void* w, const float* w_scales, int32_t M, int32_t N,
+                  int32_t K, int32_t out_type, void* c, void* workspace, size_t workspace_bytes, void* stream);
+size_t zinc_moe_gemm_fp8_workspace_size(int32_t rows, int32_t n_experts, int32_t N, int32_t K);
+int zinc_moe_gemm_fp8(const void* a, const float* a_scales, const void* w, const float* w_scales,
+                      const int32_t* offsets, int32_t n_experts, int32_t rows, int32_t N, int32_t K,
+                      int32_t out_type, void* c, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Batched experts with FP8 weights, the FP8 form of zinc_moe_q4k_experts:
+ *   y[t] = sum_s p[t, s] W_down_e . hq,   hq = Q( silu(W_gate_e . xq) (*) (W_up_e . xq) ),   xq = Q(x[t])
+ * with e = ids[t, s] and Q the quantiser above with one scale per row and 128
+ * columns.  Gate and up rows and h are fp32 until Q; each expert's output row is
+ * rounded to x's type and the weighted sum is taken in fp32.  w_gate, w_up: n_experts
+ * [inter x hidden] FP8 weight matrices, w_down: n_experts [hidden x inter].
+ * x and y [M x hidden] of `type`.  Ids outside [0, n_experts) contribute nothing and set
+ * *dev_error; duplicate ids each count.  Nothing is read back by the host.
+ * Limits: hidden, inter multiples of 128, hidden <= 16384, inter <= 65536 (ZINC_ERR_SHAPE);
+ * 1 <= top_k <= n_experts <= 1024, M * top_k <= 2^24 (ZINC_ERR_ARG).  The workspace size
+ * is non-decreasing in M.
+ */
+size_t zinc_moe_fp8_experts_workspace_size(int32_t M, int32_t top_k, int32_t n_experts, int32_t hidden,
+                                           int32_t inter, int32_t type);
+int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const void* w_up, const float* up_scales,
+                         const void* w_down, const float* down_scales, int32_t n_experts, int32_t hidden,
+                         int32_t inter, const void* x, int32_t type, int32_t M, const int32_t* expert_ids,
+                         const float* expert_weights, int32_t top_k, void* y, void* workspace,
+                         size_t workspace_bytes, int32_t* dev_error, void* stream);
+
+/*
  * Kernel timing for benchmarks and profiles (off by default; not needed for
  * correct use).  After zinc_timing_enable(capacity), every prefill, decode and
  * MoE call records a HIP event pair on its stream immediately around its main

@@ -16,6 +16,18 @@ Functions carry the C entry points' names and take torch tensors:
 * ``zinc_moe_q4k_experts(w_gate, w_up, w_down, n_experts, hidden, inter, x, ids, p, ...)`` -> fp16 y
 * ``zinc_moe_route_topk(logits, top_k)`` -> (int32 ids, fp32 weights), both on the GPU
 
+The FP8 expert layer (float16, bfloat16 or float32 activations; FP8 tensors are
+``torch.float8_e4m3fn`` with float32 scales per block of 128):
+
+* ``zinc_moe_sort(expert_ids, n_experts)`` -> (offsets, slot_row, row_slot)
+* ``zinc_moe_gather(x, slot_row)`` -> rows in expert order, ``zinc_moe_gather_backward(dxs, slot_row)`` -> dx
+* ``zinc_moe_gather_fp8(x, slot_row)`` -> (q, scales)
+* ``zinc_moe_combine(ys, slot_row, expert_weights)`` -> y, ``zinc_moe_combine_backward(dy, ys, slot_row,
+  expert_weights)`` -> (dys, dweights)
+* ``zinc_fp8_quantize(x, block_rows)`` -> (q, scales)
+* ``zinc_gemm_fp8(a, a_scales, w, w_scales)``, ``zinc_moe_gemm_fp8(a, a_scales, w, w_scales, offsets)`` -> c
+* ``zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, ids, p)`` -> y
+
 Q4_K weights are uint8 tensors holding the raw 144-byte blocks ([rows,
 cols/256, 144] or flat); x is fp16 ``[M, hidden]``.
 """
@@ -55,6 +67,19 @@ EXPORTS = (
     "zinc_moe_q4k_experts",
     "zinc_moe_experts_fmt",
     "zinc_moe_route_topk",
+    "zinc_moe_sort_workspace_size",
+    "zinc_moe_sort",
+    "zinc_moe_gather",
+    "zinc_moe_gather_fp8",
+    "zinc_moe_combine",
+    "zinc_moe_combine_backward",
+    "zinc_fp8_quantize",
+    "zinc_gemm_fp8_workspace_size",
+    "zinc_gemm_fp8",
+    "zinc_moe_gemm_fp8_workspace_size",
+    "zinc_moe_gemm_fp8",
+    "zinc_moe_fp8_experts_workspace_size",
+    "zinc_moe_fp8_experts",
     "zinc_timing_enable",
     "zinc_timing_collect",
     "zinc_timing_disable",
@@ -118,6 +143,25 @@ def _load() -> ctypes.CDLL:
     lib.zinc_moe_experts_fmt.argtypes = [P, P, P, I32, I32, I32, I32, P, I32, P, P, I32, P, I32, I32, P, SZ, P, P]
     lib.zinc_moe_route_topk.restype = ctypes.c_int
     lib.zinc_moe_route_topk.argtypes = [P, I32, I32, I32, P, P, P]
+    for name, args in (
+            ("zinc_moe_sort_workspace_size", [I32, I32, I32]),
+            ("zinc_gemm_fp8_workspace_size", [I32, I32, I32]),
+            ("zinc_moe_gemm_fp8_workspace_size", [I32, I32, I32, I32]),
+            ("zinc_moe_fp8_experts_workspace_size", [I32, I32, I32, I32, I32, I32])):
+        getattr(lib, name).restype = SZ
+        getattr(lib, name).argtypes = args
+    for name, args in (
+            ("zinc_moe_sort", [P, I32, I32, I32, P, P, P, P, SZ, P, P]),
+            ("zinc_moe_gather", [P, I32, I32, I32, I32, P, P, P]),
+            ("zinc_moe_gather_fp8", [P, I32, I32, I32, I32, P, P, P, P]),
+            ("zinc_moe_combine", [P, I32, I32, I32, I32, P, P, P, P]),
+            ("zinc_moe_combine_backward", [P, P, I32, I32, I32, I32, P, P, P, P, P]),
+            ("zinc_fp8_quantize", [P, I32, I32, I32, I32, P, P, P]),
+            ("zinc_gemm_fp8", [P, P, P, P, I32, I32, I32, I32, P, P, SZ, P]),
+            ("zinc_moe_gemm_fp8", [P, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
+            ("zinc_moe_fp8_experts", [P, P, P, P, P, P, I32, I32, I32, P, I32, I32, P, P, I32, P, P, SZ, P, P])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
     lib.zinc_timing_enable.restype = ctypes.c_int
     lib.zinc_timing_enable.argtypes = [I32]
     lib.zinc_timing_collect.restype = ctypes.c_int
@@ -523,3 +567,341 @@ def zinc_moe_route_topk(logits, top_k: int, expert_ids=None, expert_weights=None
     st = lib.zinc_moe_route_topk(_ptr(logits), M, E, top_k, _ptr(expert_ids), _ptr(expert_weights), s.cuda_stream)
     _check(st, "zinc_moe_route_topk")
     return expert_ids, expert_weights
+
+
+# ---------------------------------------------------------------------------
+# the FP8 expert layer
+# ---------------------------------------------------------------------------
+_TYPE_CODES: dict = {}
+
+
+def _type_code(dtype, what: str) -> int:
+    if not _TYPE_CODES:
+        torch = _torch()
+        _TYPE_CODES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _TYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float16, bfloat16 or float32, got {dtype}")
+    return code
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _rows_of(x, unit: int, what: str):
+    """(type code, rows, columns) of a contiguous 2-D activation matrix."""
+    if x is None or x.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D tensor")
+    code = _type_code(x.dtype, what)
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    rows, cols = x.shape
+    if cols <= 0 or cols % unit or cols > 65536:
+        raise ValueError(f"{what} must have a multiple of {unit} columns, at most 65536, got {cols}")
+    return code, rows, cols
+
+
+def _slot_rows(slot_row, M: int | None):
+    """top_k of an int32 [M, top_k] slot_row tensor (any M where M is None)."""
+    torch = _torch()
+    if slot_row is None or slot_row.dim() != 2:
+        raise ValueError("slot_row must be a 2-D int32 [M, top_k] tensor")
+    tokens, top_k = slot_row.shape
+    _need(slot_row, torch.int32, (tokens if M is None else M, top_k), "slot_row")
+    _slots(tokens, top_k)
+    return tokens, top_k
+
+
+def _slots(M: int, top_k: int) -> None:
+    if top_k < 1 or top_k > 1024 or M * top_k > 1 << 24:
+        raise ValueError("top_k must be in 1..1024 and M * top_k at most 2**24")
+
+
+class _Call:
+    """The stream of a call and its allocations: outputs the caller did not
+    give and the workspace, made on that stream."""
+
+    def __init__(self, stream, device):
+        torch = _torch()
+        self.torch, self.device = torch, device
+        here = torch.cuda.current_stream(device)
+        self.stream = here if stream is None else _resolve_stream(stream, device)
+        self.same = self.stream == here
+
+    def empty(self, shape, dtype):
+        if self.same:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        return _empty_on(self.stream, shape, dtype=dtype, device=self.device)
+
+    def workspace(self, ws, need: int):
+        if ws is None and need:
+            ws = self.empty((need,), self.torch.uint8)
+        return ws
+
+    def run(self, name: str, *args) -> None:
+        if self.torch.cuda.current_device() == self.device.index:
+            _check(getattr(lib, name)(*args, self.stream.cuda_stream), name)
+        else:
+            with self.torch.cuda.device(self.device):
+                _check(getattr(lib, name)(*args, self.stream.cuda_stream), name)
+
+
+def moe_sort_workspace_size(M: int, top_k: int, n_experts: int) -> int:
+    return int(lib.zinc_moe_sort_workspace_size(M, top_k, n_experts))
+
+
+def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib.zinc_gemm_fp8_workspace_size(M, N, K))
+
+
+def moe_gemm_fp8_workspace_size(rows: int, n_experts: int, N: int, K: int) -> int:
+    return int(lib.zinc_moe_gemm_fp8_workspace_size(rows, n_experts, N, K))
+
+
+def moe_fp8_workspace_size(M: int, top_k: int, n_experts: int, hidden: int, inter: int, dtype) -> int:
+    return int(lib.zinc_moe_fp8_experts_workspace_size(M, top_k, n_experts, hidden, inter,
+                                                       _type_code(dtype, "dtype")))
+
+
+def _dev_error(dev_error) -> None:
+    if dev_error is not None and (dev_error.dtype != _torch().int32 or dev_error.numel() < 1):
+        raise ValueError("dev_error must be an int32 tensor of at least one element")
+
+
+def zinc_moe_sort(expert_ids, n_experts: int, offsets=None, slot_row=None, row_slot=None, workspace=None,
+                  dev_error=None, stream=None):
+    """Rows of the routed slots in expert order (stable): ``(offsets int32 [n_experts + 1], slot_row int32
+    [M, top_k], row_slot int32 [M * top_k])``.  A slot with an id outside ``[0, n_experts)`` has slot_row -1."""
+    torch = _torch()
+    if expert_ids is None or expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be a 2-D int32 [M, top_k] tensor")
+    M, top_k = expert_ids.shape
+    _need(expert_ids, torch.int32, (M, top_k), "expert_ids")
+    _slots(M, top_k)
+    if n_experts < 1 or n_experts > 1024:
+        raise ValueError("n_experts must be in 1..1024")
+    for t, shape, what in ((offsets, (n_experts + 1,), "offsets"), (slot_row, (M, top_k), "slot_row"),
+                           (row_slot, (M * top_k,), "row_slot")):
+        if t is not None:
+            _need(t, torch.int32, shape, what)
+    _dev_error(dev_error)
+    need = moe_sort_workspace_size(M, top_k, n_experts)
+    _workspace(workspace, need)
+    _on_gpu(expert_ids, offsets, slot_row, row_slot, workspace, dev_error)
+    c = _Call(stream, expert_ids.device)
+    offsets = c.empty((n_experts + 1,), torch.int32) if offsets is None else offsets
+    slot_row = c.empty((M, top_k), torch.int32) if slot_row is None else slot_row
+    row_slot = c.empty((M * top_k,), torch.int32) if row_slot is None else row_slot
+    workspace = c.workspace(workspace, need)
+    c.run("zinc_moe_sort", _ptr(expert_ids), M, top_k, n_experts, _ptr(offsets), _ptr(slot_row), _ptr(row_slot),
+          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _ptr(dev_error))
+    return offsets, slot_row, row_slot
+
+
+def zinc_moe_gather(x, slot_row, xs=None, stream=None):
+    """``xs[slot_row[t, s]] = x[t]``, ``[M * top_k, hidden]``; rows that no slot names are left as they were."""
+    code, M, hidden = _rows_of(x, 8, "x")
+    _, top_k = _slot_rows(slot_row, M)
+    if xs is not None:
+        _need(xs, x.dtype, (M * top_k, hidden), "xs")
+    _on_gpu(x, slot_row, xs)
+    c = _Call(stream, x.device)
+    xs = c.empty((M * top_k, hidden), x.dtype) if xs is None else xs
+    c.run("zinc_moe_gather", _ptr(x), code, M, top_k, hidden, _ptr(slot_row), _ptr(xs))
+    return xs
+
+
+def zinc_moe_gather_fp8(x, slot_row, q=None, scales=None, stream=None):
+    """The gathered rows quantised on the way: ``(q e4m3 [M * top_k, hidden], scales fp32 [M * top_k,
+    ceil(hidden / 128)])``."""
+    torch = _torch()
+    code, M, hidden = _rows_of(x, 16, "x")
+    _, top_k = _slot_rows(slot_row, M)
+    if q is not None:
+        _need(q, torch.float8_e4m3fn, (M * top_k, hidden), "q")
+    if scales is not None:
+        _need(scales, torch.float32, (M * top_k, _blocks(hidden)), "scales")
+    _on_gpu(x, slot_row, q, scales)
+    c = _Call(stream, x.device)
+    q = c.empty((M * top_k, hidden), torch.float8_e4m3fn) if q is None else q
+    scales = c.empty((M * top_k, _blocks(hidden)), torch.float32) if scales is None else scales
+    c.run("zinc_moe_gather_fp8", _ptr(x), code, M, top_k, hidden, _ptr(slot_row), _ptr(q), _ptr(scales))
+    return q, scales
+
+
+def _combine(ys, slot_row, expert_weights, y, stream, what: str):
+    torch = _torch()
+    code, rows, hidden = _rows_of(ys, 8, what)
+    M, top_k = _slot_rows(slot_row, None)
+    if rows != M * top_k:
+        raise ValueError(f"{what} must have M * top_k = {M * top_k} rows, got {rows}")
+    if expert_weights is not None:
+        _need(expert_weights, torch.float32, (M, top_k), "expert_weights")
+    if y is not None:
+        _need(y, ys.dtype, (M, hidden), "y")
+    _on_gpu(ys, slot_row, expert_weights, y)
+    c = _Call(stream, ys.device)
+    y = c.empty((M, hidden), ys.dtype) if y is None else y
+    c.run("zinc_moe_combine", _ptr(ys), code, M, top_k, hidden, _ptr(slot_row), _ptr(expert_weights), _ptr(y))
+    return y
+
+
+def zinc_moe_combine(ys, slot_row, expert_weights, y=None, stream=None):
+    """``y[t] = sum_s expert_weights[t, s] * ys[slot_row[t, s]]`` (``expert_weights`` None: the plain sum)."""
+    return _combine(ys, slot_row, expert_weights, y, stream, "ys")
+
+
+def zinc_moe_gather_backward(dxs, slot_row, dx=None, stream=None):
+    """The gradient of zinc_moe_gather's x: ``dx[t] = sum_s dxs[slot_row[t, s]]``."""
+    return _combine(dxs, slot_row, None, dx, stream, "dxs")
+
+
+def zinc_moe_combine_backward(dy, ys, slot_row, expert_weights, dys=None, dweights=None, stream=None):
+    """Gradients of zinc_moe_combine: ``(dys[slot_row[t, s]] = expert_weights[t, s] * dy[t], dweights[t, s] =
+    <dy[t], ys[slot_row[t, s]]>)``; rows of dys that no slot names are left as they were."""
+    torch = _torch()
+    code, M, hidden = _rows_of(dy, 8, "dy")
+    _, top_k = _slot_rows(slot_row, M)
+    _need(ys, dy.dtype, (M * top_k, hidden), "ys")
+    _need(expert_weights, torch.float32, (M, top_k), "expert_weights")
+    if dys is not None:
+        _need(dys, dy.dtype, (M * top_k, hidden), "dys")
+    if dweights is not None:
+        _need(dweights, torch.float32, (M, top_k), "dweights")
+    _on_gpu(dy, ys, slot_row, expert_weights, dys, dweights)
+    c = _Call(stream, dy.device)
+    dys = c.empty((M * top_k, hidden), dy.dtype) if dys is None else dys
+    dweights = c.empty((M, top_k), torch.float32) if dweights is None else dweights
+    c.run("zinc_moe_combine_backward", _ptr(dy), _ptr(ys), code, M, top_k, hidden, _ptr(slot_row),
+          _ptr(expert_weights), _ptr(dys), _ptr(dweights))
+    return dys, dweights
+
+
+def zinc_fp8_quantize(x, block_rows: int = 1, q=None, scales=None, stream=None):
+    """``(q e4m3 [rows, cols], scales fp32)`` with one power-of-two scale per ``block_rows`` x 128 block
+    (1: activations, 128: weights)."""
+    torch = _torch()
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    code, rows, cols = _rows_of(x, 16, "x")
+    blocks = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    if q is not None:
+        _need(q, torch.float8_e4m3fn, (rows, cols), "q")
+    if scales is not None:
+        _need(scales, torch.float32, blocks, "scales")
+    _on_gpu(x, q, scales)
+    c = _Call(stream, x.device)
+    q = c.empty((rows, cols), torch.float8_e4m3fn) if q is None else q
+    scales = c.empty(blocks, torch.float32) if scales is None else scales
+    c.run("zinc_fp8_quantize", _ptr(x), code, rows, cols, block_rows, _ptr(q), _ptr(scales))
+    return q, scales
+
+
+def _fp8_rows(a, a_scales):
+    torch = _torch()
+    if a is None or a.dim() != 2:
+        raise ValueError("a must be a 2-D float8_e4m3fn tensor")
+    M, K = a.shape
+    if K <= 0 or K % 16 or K > 65536:
+        raise ValueError(f"a must have a multiple of 16 columns, at most 65536, got {K}")
+    if M > 1 << 24:
+        raise ValueError("a must have at most 2**24 rows")
+    _need(a, torch.float8_e4m3fn, (M, K), "a")
+    _need(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
+    return M, K
+
+
+def _fp8_weight(w, scales, shape, what: str) -> None:
+    torch = _torch()
+    _need(w, torch.float8_e4m3fn, shape, what)
+    _need(scales, torch.float32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), f"{what}'s scales")
+
+
+def zinc_gemm_fp8(a, a_scales, w, w_scales, out_dtype=None, out=None, workspace=None, stream=None):
+    """``c [M, N]`` of ``out_dtype`` (float16 by default): block-scaled FP8 a ``[M, K]`` times w ``[N, K]``
+    transposed, summed in fp32."""
+    torch = _torch()
+    M, K = _fp8_rows(a, a_scales)
+    if w is None or w.dim() != 2:
+        raise ValueError("w must be a 2-D float8_e4m3fn [N, K] tensor")
+    N = w.shape[0]
+    if N < 1 or N > 1 << 20:
+        raise ValueError("w must have 1..2**20 rows")
+    _fp8_weight(w, w_scales, (N, K), "w")
+    dtype = out_dtype or (torch.float16 if out is None else out.dtype)
+    code = _type_code(dtype, "out_dtype")
+    if out is not None:
+        _need(out, dtype, (M, N), "out")
+    need = gemm_fp8_workspace_size(M, N, K)
+    _workspace(workspace, need)
+    _on_gpu(a, a_scales, w, w_scales, out, workspace)
+    c = _Call(stream, a.device)
+    out = c.empty((M, N), dtype) if out is None else out
+    workspace = c.workspace(workspace, need)
+    c.run("zinc_gemm_fp8", _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), M, N, K, code, _ptr(out),
+          _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+    return out
+
+
+def zinc_moe_gemm_fp8(a, a_scales, w, w_scales, offsets, out_dtype=None, out=None, workspace=None, stream=None):
+    """zinc_gemm_fp8 by expert: rows ``offsets[e]`` .. ``offsets[e + 1] - 1`` of a take ``w[e]`` (w ``[E, N, K]``);
+    rows outside every range are left as they were."""
+    torch = _torch()
+    M, K = _fp8_rows(a, a_scales)
+    if w is None or w.dim() != 3:
+        raise ValueError("w must be a 3-D float8_e4m3fn [n_experts, N, K] tensor")
+    E, N = w.shape[0], w.shape[1]
+    if E < 1 or E > 1024 or N < 1 or N > 1 << 20:
+        raise ValueError("w must hold 1..1024 experts of 1..2**20 rows")
+    _fp8_weight(w, w_scales, (E, N, K), "w")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    dtype = out_dtype or (torch.float16 if out is None else out.dtype)
+    code = _type_code(dtype, "out_dtype")
+    if out is not None:
+        _need(out, dtype, (M, N), "out")
+    need = moe_gemm_fp8_workspace_size(M, E, N, K)
+    _workspace(workspace, need)
+    _on_gpu(a, a_scales, w, w_scales, offsets, out, workspace)
+    c = _Call(stream, a.device)
+    out = c.empty((M, N), dtype) if out is None else out
+    workspace = c.workspace(workspace, need)
+    c.run("zinc_moe_gemm_fp8", _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), E, M, N, K, code,
+          _ptr(out), _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+    return out
+
+
+def zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, expert_ids, expert_weights,
+                         y=None, workspace=None, dev_error=None, stream=None):
+    """``y[t] = sum_s p[t, s] * MLP_{ids[t, s]}(x[t])`` with FP8 expert weights (gate and up ``[E, inter, hidden]``,
+    down ``[E, hidden, inter]``); x, and each SwiGLU row, are quantised per 128 columns on the way."""
+    torch = _torch()
+    code, M, hidden = _rows_of(x, 128, "x")
+    if hidden > 16384:
+        raise ValueError("hidden must be at most 16384")
+    if w_gate is None or w_gate.dim() != 3:
+        raise ValueError("w_gate must be a 3-D float8_e4m3fn [n_experts, inter, hidden] tensor")
+    E, inter = w_gate.shape[0], w_gate.shape[1]
+    if inter <= 0 or inter % 128 or inter > 65536:
+        raise ValueError("inter must be a multiple of 128, at most 65536")
+    _fp8_weight(w_gate, gate_scales, (E, inter, hidden), "w_gate")
+    _fp8_weight(w_up, up_scales, (E, inter, hidden), "w_up")
+    _fp8_weight(w_down, down_scales, (E, hidden, inter), "w_down")
+    top_k = _moe_routing(expert_ids, expert_weights, M)
+    _slots(M, top_k)
+    if E < 1 or E > 1024 or top_k > E:
+        raise ValueError("there must be 1..1024 experts and top_k must not exceed them")
+    if y is not None:
+        _need(y, x.dtype, (M, hidden), "y")
+    _dev_error(dev_error)
+    need = moe_fp8_workspace_size(M, top_k, E, hidden, inter, x.dtype)
+    _workspace(workspace, need)
+    _on_gpu(w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, expert_ids, expert_weights, y, workspace,
+            dev_error)
+    c = _Call(stream, x.device)
+    y = c.empty((M, hidden), x.dtype) if y is None else y
+    workspace = c.workspace(workspace, need)
+    c.run("zinc_moe_fp8_experts", _ptr(w_gate), _ptr(gate_scales), _ptr(w_up), _ptr(up_scales), _ptr(w_down),
+          _ptr(down_scales), E, hidden, inter, _ptr(x), code, M, _ptr(expert_ids), _ptr(expert_weights), top_k, _ptr(y),
+          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _ptr(dev_error))
+    return y

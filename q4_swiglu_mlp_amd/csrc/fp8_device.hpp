@@ -1,0 +1,118 @@
+// Device helpers shared by the expert layer's FP8 operators: 16-bit and fp32
+// rows read as eight values at a time, and the block quantiser's arithmetic.
+//
+// A block of 128 values is stored as e4m3 (OCP: largest value 448) with one
+// fp32 scale, the smallest power of two s with max|x| / s <= 448.  With a power
+// of two, x / s is exact, so e4m3's own rounding (to nearest, ties to even) is
+// the only one, and q * s is exact in fp32 and bf16.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace zinc {
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bhalf8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// Element types of activations: the ZINC_F16 / ZINC_BF16 / ZINC_F32 codes.
+struct F16 {
+  using T = _Float16;
+};
+struct BF16 {
+  using T = __bf16;
+};
+struct F32 {
+  using T = float;
+};
+
+// Eight consecutive values, 16-byte aligned, as fp32.
+__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
+  const half8_t h = *reinterpret_cast<const half8_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+}
+__device__ __forceinline__ void load8(const __bf16* p, float (&v)[8]) {
+  const bhalf8_t h = *reinterpret_cast<const bhalf8_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void store8(_Float16* p, const float (&v)[8]) {
+  half8_t h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
+  *reinterpret_cast<half8_t*>(p) = h;
+}
+__device__ __forceinline__ void store8(__bf16* p, const float (&v)[8]) {
+  bhalf8_t h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (__bf16)v[i];
+  *reinterpret_cast<bhalf8_t*>(p) = h;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
+
+// |v| as its bit pattern where finite, 0 for infinities and NaN (they take no
+// part in a block's maximum; patterns of non-negative floats order as the
+// floats do).
+__device__ __forceinline__ uint32_t finite_abs_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+
+// The scale of a block whose largest finite |x| has the bits `amax`: the
+// exponent field of 2^e, e = exponent - 8, one more where the fraction is above
+// 448's (1.75 x 2^8).  At least 2^-126 (so that 1 / s is finite too), and 1 for
+// a block of zeros.
+__device__ __forceinline__ uint32_t scale_field(uint32_t amax) {
+  if (amax == 0u) return 127u;
+  const int f = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)(f < 1 ? 1 : f);
+}
+__device__ __forceinline__ float scale_of(uint32_t field) { return __uint_as_float(field << 23); }
+__device__ __forceinline__ float inverse_scale_of(uint32_t field) { return __uint_as_float((254u - field) << 23); }
+
+// Eight values times `inv` as e4m3 bytes.  Infinities become NaN (e4m3 has none).
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float inv) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] = v[i] * inv;
+    if (__builtin_isinf(v[i])) s[i] = __builtin_nanf("");
+  }
+  uint2 q;
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+  q.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], w, true);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(s[4], s[5], 0, false);
+  q.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[6], s[7], w, true);
+  return q;
+}
+
+// Maximum over the aligned group of 16 lanes that holds one row's block.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  auto step = [&](int o) { v = (uint32_t)o > v ? (uint32_t)o : v; };
+  step(__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xF, 0xF, false));    // quad_perm [1,0,3,2]
+  step(__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xF, 0xF, false));    // quad_perm [2,3,0,1]
+  step(__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  step(__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xF, 0xF, false));   // row_mirror
+  return v;
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+}  // namespace zinc

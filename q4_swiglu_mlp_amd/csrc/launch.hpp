@@ -64,4 +64,35 @@ hipError_t launch_moe(const void* wg, const void* wu, const void* wd, int n_expe
 hipError_t launch_route_topk(const float* logits, int M, int n_experts, int top_k, int32_t* ids, float* p,
                              hipStream_t stream);
 
+// Expert-layer token permutation (k_moe_tokens.hip).  S = M * top_k slots; type
+// codes: 0 fp16, 1 bf16, 2 fp32.
+size_t moe_sort_workspace_bytes(int S, int E);
+hipError_t launch_moe_sort(const int32_t* ids, int S, int E, int32_t* offsets, int32_t* slot_row, int32_t* row_slot,
+                           void* ws, int32_t* dev_error, hipStream_t stream);
+hipError_t launch_moe_gather(const void* x, int row_bytes, int M, int top_k, const int32_t* slot_row, void* xs,
+                             hipStream_t stream);
+hipError_t launch_moe_combine(const void* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
+                              const float* p, void* y, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const void* dy, const void* ys, int type, int M, int top_k, int H,
+                                       const int32_t* slot_row, const float* p, void* dys, float* dp,
+                                       hipStream_t stream);
+
+// e4m3 with a scale per block of 128 (k_fp8_quant.hip).
+hipError_t launch_fp8_quantize(const void* x, int type, int R, int C, int block_rows, void* q, float* scales,
+                               hipStream_t stream);
+hipError_t launch_moe_gather_fp8(const void* x, int type, int M, int top_k, int C, const int32_t* slot_row, void* q,
+                                 float* scales, hipStream_t stream);
+hipError_t launch_swiglu_quant(const float* g, const float* u, int R, int C, const int32_t* n_valid, void* q,
+                               float* scales, hipStream_t stream);
+
+// Products of block-scaled e4m3 matrices and the FP8 expert layer (k_fp8_gemm.hip).
+// offsets: nullptr for one dense product (E = 1), else the experts' row ranges.
+size_t gemm_fp8_workspace_bytes(int M, int E, int N, int K);
+hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const float* sw, const int32_t* offsets,
+                           int E, int M, int N, int K, int out_type, void* c, void* ws, hipStream_t stream);
+size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I, int type);
+hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const float* su, const void* wd,
+                          const float* sd, int E, int H, int I, const void* x, int type, int M, const int32_t* ids,
+                          const float* p, int top_k, void* y, void* ws, int32_t* dev_error, hipStream_t stream);
+
 }  // namespace zinc
