@@ -18,164 +18,41 @@
 // layer's second quantisation (where 1.5e-5 moves a value in 5000 to the next
 // code, 1.2e-3 of y), take the fp16 MFMA on exactly converted operands instead:
 // half the rate, 7e-9 of the result.
-#include "fp8_device.hpp"
+#include <atomic>
+
+#include "fp8_tile.hpp"
 #include "launch.hpp"
 
 namespace zinc {
 namespace {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4_t mfma128(i32x8_t a, i32x8_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-}
-
-// Four e4m3 bytes as fp16, exactly.
-__device__ __forceinline__ void e4m3_to_f16(int w, _Float16* o) {
-  typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
-  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
-  o[0] = a[0];
-  o[1] = a[1];
-  o[2] = b[0];
-  o[3] = b[1];
-}
-
-// A lane's 32 bytes of a block of 128 as four fp16 operands.
-struct F16Block {
-  half8_t v[4];
-};
-__device__ __forceinline__ F16Block to_f16(i32x8_t q) {
-  F16Block b;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    _Float16 o[8];
-    e4m3_to_f16(q[2 * i], o);
-    e4m3_to_f16(q[2 * i + 1], o + 4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b.v[i][j] = o[j];
+template <typename KERNEL>
+hipError_t run_tiles(GemmArgs g, int TM, int cols, hipStream_t stream) {
+  g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, TM);
+  g.col_tiles = (g.N + cols - 1) / cols;
+  const long long per = ((long long)g.row_tiles * g.col_tiles + 7) / 8;
+  constexpr int bytes = (int)sizeof(typename KERNEL::Smem);
+  static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return b;
-}
-__device__ __forceinline__ f32x4_t mfma128(const F16Block& a, const F16Block& b, f32x4_t c) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], c, 0, 0, 0);
-  return c;
-}
-
-// The rows [first, first + rows) of tile `tile` (TM rows each) of the experts'
-// row ranges, and its expert; rows == 0 past the last tile.  Offsets outside
-// [0, total] or not ascending are cut to that range.
-struct RowTile {
-  int expert, first, rows;
-};
-
-template <int TM>
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int E, int total, int tile) {
-  if (!offsets) return {0, tile * TM, min(TM, total - tile * TM)};
-  const int lane = threadIdx.x & 63;
-  int seen = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = e < E ? min(max(offsets[e], 0), total) : 0;
-    const int hi = e < E ? min(max(offsets[e + 1], lo), total) : 0;
-    const int n = (hi - lo + TM - 1) / TM;
-    int scan = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(scan, d, 64);
-      if (lane >= d) scan += o;
-    }
-    const uint64_t here = __ballot(seen + scan > tile);
-    if (here) {
-      const int l = (int)__builtin_ctzll(here);
-      const int before = seen + __shfl(scan - n, l, 64);
-      const int first = __shfl(lo, l, 64) + (tile - before) * TM;
-      return {e0 + l, first, min(TM, __shfl(hi, l, 64) - first)};
-    }
-    seen += __shfl(scan, 63, 64);
-  }
-  return {0, 0, 0};
-}
-
-// Sixteen bytes of a row, or zeros where they lie outside the matrix.
-__device__ __forceinline__ uint4 row_piece(const uint8_t* p, bool in) {
-  return in ? *reinterpret_cast<const uint4*>(p) : uint4{0, 0, 0, 0};
-}
-
-// 64 x 64 outputs per workgroup of four waves, 32 x 32 each.
-template <typename T, bool EXACT>
-__global__ __launch_bounds__(256) void k_gemm_fp8(const uint8_t* __restrict__ a, const float* __restrict__ sa,
-                                                  const uint8_t* __restrict__ w, const float* __restrict__ sw,
-                                                  const int32_t* __restrict__ offsets, int E, int M, int N, int K,
-                                                  T* __restrict__ c) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quad = lane >> 4;
-  const int KB = (K + 127) / 128, NB = (N + 127) / 128;
-  const RowTile rt = find_tile<64>(offsets, E, M, blockIdx.x);
-  if (rt.rows <= 0) return;
-  const int m0 = rt.first + (wave >> 1) * 32, m_end = rt.first + rt.rows;
-  const int n0 = blockIdx.y * 64 + (wave & 1) * 32;
-  const uint8_t* we = w + (size_t)rt.expert * N * K;
-  const float* swe = sw + (size_t)rt.expert * NB * KB;
-  f32x4_t acc[2][2] = {};
-  for (int kb = 0; kb < KB; ++kb) {
-    i32x8_t fa[2], fw[2];
-    float s[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = m0 + 16 * i + l16, n = n0 + 16 * i + l16, k = kb * 128 + quad * 32;
-      union {
-        uint4 q[2];
-        i32x8_t v;
-      } u;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) u.q[h] = row_piece(a + (size_t)m * K + k + 16 * h, m < m_end && k + 16 * h < K);
-      fa[i] = u.v;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) u.q[h] = row_piece(we + (size_t)n * K + k + 16 * h, n < N && k + 16 * h < K);
-      fw[i] = u.v;
-      s[i] = m < m_end ? sa[(size_t)m * KB + kb] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = n0 + 16 * j;
-      const float t = n < N ? swe[(size_t)(n >> 7) * KB + kb] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f32x4_t d = {0, 0, 0, 0};
-        if constexpr (EXACT)
-          d = mfma128(to_f16(fw[j]), to_f16(fa[i]), d);
-        else
-          d = mfma128(fw[j], fa[i], d);
-        const float st = s[i] * t;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(st, d[r], acc[i][j][r]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = m0 + 16 * i + l16;
-    if (m >= m_end) continue;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = n0 + 16 * j + 4 * quad + r;
-        if (n < N) c[(size_t)m * N + n] = (T)acc[i][j][r];
-      }
-  }
-}
-
-template <typename T, bool EXACT = false>
-hipError_t gemm(const void* a, const float* sa, const void* w, const float* sw, const int32_t* offsets, int E, int M,
-                int N, int K, void* c, hipStream_t stream) {
-  // every expert's last tile may be partly filled
-  const int tiles = offsets ? (M + 63) / 64 + (E < M ? E : M) : (M + 63) / 64;
-  hipLaunchKernelGGL((k_gemm_fp8<T, EXACT>), dim3((unsigned)tiles, (unsigned)((N + 63) / 64)), dim3(256), 0, stream,
-                     static_cast<const uint8_t*>(a), sa, static_cast<const uint8_t*>(w), sw, offsets, E, M, N, K,
-                     static_cast<T*>(c));
+  hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)(8 * per)), dim3(KERNEL::THREADS), bytes, stream, g);
   return hipGetLastError();
+}
+
+template <bool EXACT, typename T>
+hipError_t gemm(const GemmArgs& g, hipStream_t stream) {
+  if constexpr (EXACT)
+    return run_tiles<TileKernel<128, 128, 2, 2, true, false, T>>(g, 128, 128, stream);
+  else
+    return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 256, stream);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -185,7 +62,7 @@ struct ExpertsPlan {
   int32_t *offsets, *slot_row, *row_slot;
   void* sort_ws;
   uint8_t *xq, *hq;
-  float *xs, *hs, *gate, *up;
+  float *xs, *hs;
   void* ys;
 };
 
@@ -201,8 +78,6 @@ ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, siz
   p.sort_ws = take(moe_sort_workspace_bytes((int)S, E));
   p.xq = reinterpret_cast<uint8_t*>(take(S * H));
   p.xs = reinterpret_cast<float*>(take(S * (H / 128) * 4));
-  p.gate = reinterpret_cast<float*>(take(S * I * 4));
-  p.up = reinterpret_cast<float*>(take(S * I * 4));
   p.hq = reinterpret_cast<uint8_t*>(take(S * I));
   p.hs = reinterpret_cast<float*>(take(S * (I / 128) * 4));
   p.ys = take(S * H * (type == 2 ? 4 : 2));
@@ -214,9 +89,20 @@ ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, siz
 
 hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const float* sw, const int32_t* offsets,
                            int E, int M, int N, int K, int out_type, void* c, void*, hipStream_t stream) {
-  if (out_type == 0) return gemm<_Float16>(a, sa, w, sw, offsets, E, M, N, K, c, stream);
-  if (out_type == 1) return gemm<__bf16>(a, sa, w, sw, offsets, E, M, N, K, c, stream);
-  return gemm<float, true>(a, sa, w, sw, offsets, E, M, N, K, c, stream);
+  GemmArgs g{};
+  g.a = static_cast<const uint8_t*>(a);
+  g.sa = sa;
+  g.w = static_cast<const uint8_t*>(w);
+  g.sw = sw;
+  g.offsets = offsets;
+  g.E = E;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.c = c;
+  if (out_type == 0) return gemm<false, _Float16>(g, stream);
+  if (out_type == 1) return gemm<false, __bf16>(g, stream);
+  return gemm<true, float>(g, stream);
 }
 
 size_t gemm_fp8_workspace_bytes(int, int, int, int) { return 0; }
@@ -234,14 +120,32 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   const int S = M * top_k;
   hipError_t e = launch_moe_sort(ids, S, E, pl.offsets, pl.slot_row, pl.row_slot, pl.sort_ws, dev_error, stream);
   if (e == hipSuccess) e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
+  GemmArgs g{};
+  g.a = pl.xq;
+  g.sa = pl.xs;
+  g.w = static_cast<const uint8_t*>(wg);
+  g.sw = sg;
+  g.w2 = static_cast<const uint8_t*>(wu);
+  g.sw2 = su;
+  g.offsets = pl.offsets;
+  g.E = E;
+  g.M = S;
+  g.N = I;
+  g.K = H;
+  g.c = pl.hq;
+  g.cs = pl.hs;
+  if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 128, stream);
+  g.a = pl.hq;
+  g.sa = pl.hs;
+  g.w = static_cast<const uint8_t*>(wd);
+  g.sw = sd;
+  g.N = H;
+  g.K = I;
+  g.c = pl.ys;
   if (e == hipSuccess)
-    e = type == 1 ? gemm<float>(pl.xq, pl.xs, wg, sg, pl.offsets, E, S, I, H, pl.gate, stream)
-                  : gemm<float, true>(pl.xq, pl.xs, wg, sg, pl.offsets, E, S, I, H, pl.gate, stream);
-  if (e == hipSuccess)
-    e = type == 1 ? gemm<float>(pl.xq, pl.xs, wu, su, pl.offsets, E, S, I, H, pl.up, stream)
-                  : gemm<float, true>(pl.xq, pl.xs, wu, su, pl.offsets, E, S, I, H, pl.up, stream);
-  if (e == hipSuccess) e = launch_swiglu_quant(pl.gate, pl.up, S, I, pl.offsets + E, pl.hq, pl.hs, stream);
-  if (e == hipSuccess) e = launch_gemm_fp8(pl.hq, pl.hs, wd, sd, pl.offsets, E, S, H, I, type, pl.ys, nullptr, stream);
+    e = type == 0 ? gemm<true, _Float16>(g, stream)
+        : type == 1 ? gemm<false, __bf16>(g, stream)
+                    : gemm<true, float>(g, stream);
   if (e == hipSuccess) e = launch_moe_combine(pl.ys, type, M, top_k, H, pl.slot_row, p, y, stream);
   return e;
 }
