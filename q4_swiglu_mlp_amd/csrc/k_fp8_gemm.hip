@@ -20,11 +20,27 @@
 // half the rate, 7e-9 of the result.
 #include <atomic>
 
-#include "fp8_tile.hpp"
+#include "fp8_stream.hpp"
 #include "launch.hpp"
 
 namespace zinc {
 namespace {
+
+// Raises the kernel's LDS limit, once a device.
+template <typename KERNEL>
+hipError_t allow_lds(const void* kernel, int bytes) {
+  static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+constexpr int kLds = 160 * 1024;
 
 template <typename KERNEL>
 hipError_t run_tiles(GemmArgs g, int TM, int cols, hipStream_t stream) {
@@ -32,27 +48,66 @@ hipError_t run_tiles(GemmArgs g, int TM, int cols, hipStream_t stream) {
   g.col_tiles = (g.N + cols - 1) / cols;
   const long long per = ((long long)g.row_tiles * g.col_tiles + 7) / 8;
   constexpr int bytes = (int)sizeof(typename KERNEL::Smem);
-  static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  const hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>), bytes);
   if (e != hipSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
   hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)(8 * per)), dim3(KERNEL::THREADS), bytes, stream, g);
   return hipGetLastError();
 }
 
+// Weight streams: the blocks of 128 of a that fit LDS beside the rings, two
+// workgroups a CU where all of them fit so, else one.
+template <typename KERNEL>
+hipError_t run_stream(StreamArgs s, int cols, hipStream_t stream) {
+  GemmArgs& g = s.g;
+  const int KB = (g.K + 127) / 128, all = (KB + s.ks - 1) / s.ks * s.ks;
+  s.rows = g.M < KERNEL::TM ? g.M : KERNEL::TM;
+  s.chunk = all;
+  if (KERNEL::smem_bytes(s.rows, all) > kLds / 2) {
+    while (KERNEL::smem_bytes(s.rows, s.chunk) > kLds) s.chunk -= s.ks;
+  }
+  const size_t bytes = KERNEL::smem_bytes(s.rows, s.chunk);
+  g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, KERNEL::TM);
+  g.col_tiles = (g.N + cols - 1) / cols;
+  const hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_stream<KERNEL>), kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_fp8_stream<KERNEL>, dim3((unsigned)((long long)g.row_tiles * g.col_tiles)),
+                     dim3(KERNEL::THREADS), bytes, stream, s);
+  return hipGetLastError();
+}
+
+// Rows of a stream's tile in sixteens, 0 where the tiled kernel is the better one.
+int stream_tiles(int rows, int E) {
+  const int mean = E ? (rows + E - 1) / E : rows;
+  return mean <= 16 ? 1 : mean <= 32 ? 2 : mean <= 64 ? 4 : 0;
+}
+
+template <int MT, typename T>
+hipError_t stream_product(const GemmArgs& g, hipStream_t stream) {
+  StreamArgs s{};
+  s.g = g;
+  const long long tiles = (g.N + 15) / 16 * (long long)(g.offsets ? (g.E < g.M ? g.E : g.M) : 1);
+  s.ks = tiles >= 4096 ? 1 : tiles >= 2048 ? 2 : tiles >= 512 ? 4 : 8;
+  return run_stream<StreamKernel<MT, 8, 4, 0, false, float, T>>(s, 8 / s.ks * 16, stream);
+}
+
 template <bool EXACT, typename T>
 hipError_t gemm(const GemmArgs& g, hipStream_t stream) {
+  switch (stream_tiles(g.M, g.offsets ? g.E : 0)) {
+    case 1: return stream_product<1, T>(g, stream);
+    case 2: return stream_product<2, T>(g, stream);
+    case 4: return stream_product<4, T>(g, stream);
+  }
   if constexpr (EXACT)
     return run_tiles<TileKernel<128, 128, 2, 2, true, false, T>>(g, 128, 128, stream);
   else
     return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 256, stream);
+}
+
+template <typename T_IN>
+hipError_t stream_gate_up(const StreamArgs& s, int mt, hipStream_t stream) {
+  if (mt == 1) return run_stream<StreamKernel<1, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
+  if (mt == 2) return run_stream<StreamKernel<2, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
+  return run_stream<StreamKernel<4, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -119,7 +174,6 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   const ExpertsPlan pl = carve(ws, M, top_k, E, H, I, type, nullptr);
   const int S = M * top_k;
   hipError_t e = launch_moe_sort(ids, S, E, pl.offsets, pl.slot_row, pl.row_slot, pl.sort_ws, dev_error, stream);
-  if (e == hipSuccess) e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
   GemmArgs g{};
   g.a = pl.xq;
   g.sa = pl.xs;
@@ -134,7 +188,23 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.K = H;
   g.c = pl.hq;
   g.cs = pl.hs;
-  if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 128, stream);
+  const int mt = stream_tiles(S, E);
+  if (e != hipSuccess) return e;
+  if (mt) {
+    StreamArgs s{};
+    s.g = g;
+    s.x = x;
+    s.row_slot = pl.row_slot;
+    s.top_k = top_k;
+    s.tokens = M;
+    s.ks = 1;
+    e = type == 0 ? stream_gate_up<_Float16>(s, mt, stream)
+        : type == 1 ? stream_gate_up<__bf16>(s, mt, stream)
+                    : stream_gate_up<float>(s, mt, stream);
+  } else {
+    e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
+    if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 128, stream);
+  }
   g.a = pl.hq;
   g.sa = pl.hs;
   g.w = static_cast<const uint8_t*>(wd);
