@@ -608,7 +608,7 @@ def _slot_rows(slot_row, M: int | None):
     if slot_row is None or slot_row.dim() != 2:
         raise ValueError("slot_row must be a 2-D int32 [M, top_k] tensor")
     tokens, top_k = slot_row.shape
-    _need(slot_row, torch.int32, (tokens if M is None else M, top_k), "slot_row")
+    _fits(slot_row, torch.int32, (tokens if M is None else M, top_k), "slot_row")
     _slots(tokens, top_k)
     return tokens, top_k
 
@@ -618,33 +618,54 @@ def _slots(M: int, top_k: int) -> None:
         raise ValueError("top_k must be in 1..1024 and M * top_k at most 2**24")
 
 
-class _Call:
-    """The stream of a call and its allocations: outputs the caller did not
-    give and the workspace, made on that stream."""
+def _fits(t, dtype, shape, what: str) -> None:
+    """_need, quick where the tensor is right."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, shape, what)
 
-    def __init__(self, stream, device):
-        torch = _torch()
-        self.torch, self.device = torch, device
-        here = torch.cuda.current_stream(device)
-        self.stream = here if stream is None else _resolve_stream(stream, device)
-        self.same = self.stream == here
+
+class _Call:
+    """One call's device and stream, and its allocations: outputs the caller did
+    not give and the workspace, made on that stream.  These calls take a few
+    microseconds on the GPU where rows are few, so the common one (on the
+    current stream of the current device) builds no stream object."""
+
+    __slots__ = ("device", "raw", "other")
+
+    def __init__(self, stream, first, *rest):
+        index = first.get_device()
+        if index < 0 or any(t is not None and t.get_device() != index for t in rest):
+            _on_gpu(first, *rest)
+        self.device = first.device
+        if stream is None:
+            self.other = None
+            self.raw = _torch()._C._cuda_getCurrentRawStream(index)
+        else:
+            self.other = _resolve_stream(stream, self.device)
+            self.raw = self.other.cuda_stream
 
     def empty(self, shape, dtype):
-        if self.same:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
-        return _empty_on(self.stream, shape, dtype=dtype, device=self.device)
+        if self.other is None:
+            return _torch().empty(shape, dtype=dtype, device=self.device)
+        return _empty_on(self.other, shape, dtype=dtype, device=self.device)
 
     def workspace(self, ws, need: int):
-        if ws is None and need:
-            ws = self.empty((need,), self.torch.uint8)
-        return ws
+        """(address, bytes, the tensor that owns them) of the caller's workspace or a new one."""
+        if ws is None:
+            if not need:
+                return None, 0, None
+            ws = self.empty((need,), _torch().uint8)
+        return ws.data_ptr(), _nbytes(ws), ws
 
     def run(self, name: str, *args) -> None:
-        if self.torch.cuda.current_device() == self.device.index:
-            _check(getattr(lib, name)(*args, self.stream.cuda_stream), name)
+        torch = _torch()
+        if torch.cuda.current_device() == self.device.index:
+            status = getattr(lib, name)(*args, self.raw)
         else:
-            with self.torch.cuda.device(self.device):
-                _check(getattr(lib, name)(*args, self.stream.cuda_stream), name)
+            with torch.cuda.device(self.device):
+                status = getattr(lib, name)(*args, self.raw)
+        if status:
+            _check(status, name)
 
 
 def moe_sort_workspace_size(M: int, top_k: int, n_experts: int) -> int:
@@ -677,25 +698,24 @@ def zinc_moe_sort(expert_ids, n_experts: int, offsets=None, slot_row=None, row_s
     if expert_ids is None or expert_ids.dim() != 2:
         raise ValueError("expert_ids must be a 2-D int32 [M, top_k] tensor")
     M, top_k = expert_ids.shape
-    _need(expert_ids, torch.int32, (M, top_k), "expert_ids")
+    _fits(expert_ids, torch.int32, (M, top_k), "expert_ids")
     _slots(M, top_k)
     if n_experts < 1 or n_experts > 1024:
         raise ValueError("n_experts must be in 1..1024")
     for t, shape, what in ((offsets, (n_experts + 1,), "offsets"), (slot_row, (M, top_k), "slot_row"),
                            (row_slot, (M * top_k,), "row_slot")):
         if t is not None:
-            _need(t, torch.int32, shape, what)
+            _fits(t, torch.int32, shape, what)
     _dev_error(dev_error)
     need = moe_sort_workspace_size(M, top_k, n_experts)
     _workspace(workspace, need)
-    _on_gpu(expert_ids, offsets, slot_row, row_slot, workspace, dev_error)
-    c = _Call(stream, expert_ids.device)
+    c = _Call(stream, expert_ids, offsets, slot_row, row_slot, workspace, dev_error)
     offsets = c.empty((n_experts + 1,), torch.int32) if offsets is None else offsets
     slot_row = c.empty((M, top_k), torch.int32) if slot_row is None else slot_row
     row_slot = c.empty((M * top_k,), torch.int32) if row_slot is None else row_slot
-    workspace = c.workspace(workspace, need)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
     c.run("zinc_moe_sort", _ptr(expert_ids), M, top_k, n_experts, _ptr(offsets), _ptr(slot_row), _ptr(row_slot),
-          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _ptr(dev_error))
+          ws, ws_bytes, _ptr(dev_error))
     return offsets, slot_row, row_slot
 
 
@@ -704,9 +724,8 @@ def zinc_moe_gather(x, slot_row, xs=None, stream=None):
     code, M, hidden = _rows_of(x, 8, "x")
     _, top_k = _slot_rows(slot_row, M)
     if xs is not None:
-        _need(xs, x.dtype, (M * top_k, hidden), "xs")
-    _on_gpu(x, slot_row, xs)
-    c = _Call(stream, x.device)
+        _fits(xs, x.dtype, (M * top_k, hidden), "xs")
+    c = _Call(stream, x, slot_row, xs)
     xs = c.empty((M * top_k, hidden), x.dtype) if xs is None else xs
     c.run("zinc_moe_gather", _ptr(x), code, M, top_k, hidden, _ptr(slot_row), _ptr(xs))
     return xs
@@ -719,11 +738,10 @@ def zinc_moe_gather_fp8(x, slot_row, q=None, scales=None, stream=None):
     code, M, hidden = _rows_of(x, 16, "x")
     _, top_k = _slot_rows(slot_row, M)
     if q is not None:
-        _need(q, torch.float8_e4m3fn, (M * top_k, hidden), "q")
+        _fits(q, torch.float8_e4m3fn, (M * top_k, hidden), "q")
     if scales is not None:
-        _need(scales, torch.float32, (M * top_k, _blocks(hidden)), "scales")
-    _on_gpu(x, slot_row, q, scales)
-    c = _Call(stream, x.device)
+        _fits(scales, torch.float32, (M * top_k, _blocks(hidden)), "scales")
+    c = _Call(stream, x, slot_row, q, scales)
     q = c.empty((M * top_k, hidden), torch.float8_e4m3fn) if q is None else q
     scales = c.empty((M * top_k, _blocks(hidden)), torch.float32) if scales is None else scales
     c.run("zinc_moe_gather_fp8", _ptr(x), code, M, top_k, hidden, _ptr(slot_row), _ptr(q), _ptr(scales))
@@ -737,11 +755,10 @@ def _combine(ys, slot_row, expert_weights, y, stream, what: str):
     if rows != M * top_k:
         raise ValueError(f"{what} must have M * top_k = {M * top_k} rows, got {rows}")
     if expert_weights is not None:
-        _need(expert_weights, torch.float32, (M, top_k), "expert_weights")
+        _fits(expert_weights, torch.float32, (M, top_k), "expert_weights")
     if y is not None:
-        _need(y, ys.dtype, (M, hidden), "y")
-    _on_gpu(ys, slot_row, expert_weights, y)
-    c = _Call(stream, ys.device)
+        _fits(y, ys.dtype, (M, hidden), "y")
+    c = _Call(stream, ys, slot_row, expert_weights, y)
     y = c.empty((M, hidden), ys.dtype) if y is None else y
     c.run("zinc_moe_combine", _ptr(ys), code, M, top_k, hidden, _ptr(slot_row), _ptr(expert_weights), _ptr(y))
     return y
@@ -763,14 +780,13 @@ def zinc_moe_combine_backward(dy, ys, slot_row, expert_weights, dys=None, dweigh
     torch = _torch()
     code, M, hidden = _rows_of(dy, 8, "dy")
     _, top_k = _slot_rows(slot_row, M)
-    _need(ys, dy.dtype, (M * top_k, hidden), "ys")
-    _need(expert_weights, torch.float32, (M, top_k), "expert_weights")
+    _fits(ys, dy.dtype, (M * top_k, hidden), "ys")
+    _fits(expert_weights, torch.float32, (M, top_k), "expert_weights")
     if dys is not None:
-        _need(dys, dy.dtype, (M * top_k, hidden), "dys")
+        _fits(dys, dy.dtype, (M * top_k, hidden), "dys")
     if dweights is not None:
-        _need(dweights, torch.float32, (M, top_k), "dweights")
-    _on_gpu(dy, ys, slot_row, expert_weights, dys, dweights)
-    c = _Call(stream, dy.device)
+        _fits(dweights, torch.float32, (M, top_k), "dweights")
+    c = _Call(stream, dy, ys, slot_row, expert_weights, dys, dweights)
     dys = c.empty((M * top_k, hidden), dy.dtype) if dys is None else dys
     dweights = c.empty((M, top_k), torch.float32) if dweights is None else dweights
     c.run("zinc_moe_combine_backward", _ptr(dy), _ptr(ys), code, M, top_k, hidden, _ptr(slot_row),
@@ -787,11 +803,10 @@ def zinc_fp8_quantize(x, block_rows: int = 1, q=None, scales=None, stream=None):
     code, rows, cols = _rows_of(x, 16, "x")
     blocks = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if q is not None:
-        _need(q, torch.float8_e4m3fn, (rows, cols), "q")
+        _fits(q, torch.float8_e4m3fn, (rows, cols), "q")
     if scales is not None:
-        _need(scales, torch.float32, blocks, "scales")
-    _on_gpu(x, q, scales)
-    c = _Call(stream, x.device)
+        _fits(scales, torch.float32, blocks, "scales")
+    c = _Call(stream, x, q, scales)
     q = c.empty((rows, cols), torch.float8_e4m3fn) if q is None else q
     scales = c.empty(blocks, torch.float32) if scales is None else scales
     c.run("zinc_fp8_quantize", _ptr(x), code, rows, cols, block_rows, _ptr(q), _ptr(scales))
@@ -807,15 +822,15 @@ def _fp8_rows(a, a_scales):
         raise ValueError(f"a must have a multiple of 16 columns, at most 65536, got {K}")
     if M > 1 << 24:
         raise ValueError("a must have at most 2**24 rows")
-    _need(a, torch.float8_e4m3fn, (M, K), "a")
-    _need(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
+    _fits(a, torch.float8_e4m3fn, (M, K), "a")
+    _fits(a_scales, torch.float32, (M, _blocks(K)), "a_scales")
     return M, K
 
 
 def _fp8_weight(w, scales, shape, what: str) -> None:
     torch = _torch()
-    _need(w, torch.float8_e4m3fn, shape, what)
-    _need(scales, torch.float32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), f"{what}'s scales")
+    _fits(w, torch.float8_e4m3fn, shape, what)
+    _fits(scales, torch.float32, (*shape[:-2], _blocks(shape[-2]), _blocks(shape[-1])), f"{what}'s scales")
 
 
 def zinc_gemm_fp8(a, a_scales, w, w_scales, out_dtype=None, out=None, workspace=None, stream=None):
@@ -832,15 +847,14 @@ def zinc_gemm_fp8(a, a_scales, w, w_scales, out_dtype=None, out=None, workspace=
     dtype = out_dtype or (torch.float16 if out is None else out.dtype)
     code = _type_code(dtype, "out_dtype")
     if out is not None:
-        _need(out, dtype, (M, N), "out")
+        _fits(out, dtype, (M, N), "out")
     need = gemm_fp8_workspace_size(M, N, K)
     _workspace(workspace, need)
-    _on_gpu(a, a_scales, w, w_scales, out, workspace)
-    c = _Call(stream, a.device)
+    c = _Call(stream, a, a_scales, w, w_scales, out, workspace)
     out = c.empty((M, N), dtype) if out is None else out
-    workspace = c.workspace(workspace, need)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
     c.run("zinc_gemm_fp8", _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), M, N, K, code, _ptr(out),
-          _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+          ws, ws_bytes)
     return out
 
 
@@ -855,19 +869,18 @@ def zinc_moe_gemm_fp8(a, a_scales, w, w_scales, offsets, out_dtype=None, out=Non
     if E < 1 or E > 1024 or N < 1 or N > 1 << 20:
         raise ValueError("w must hold 1..1024 experts of 1..2**20 rows")
     _fp8_weight(w, w_scales, (E, N, K), "w")
-    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _fits(offsets, torch.int32, (E + 1,), "offsets")
     dtype = out_dtype or (torch.float16 if out is None else out.dtype)
     code = _type_code(dtype, "out_dtype")
     if out is not None:
-        _need(out, dtype, (M, N), "out")
+        _fits(out, dtype, (M, N), "out")
     need = moe_gemm_fp8_workspace_size(M, E, N, K)
     _workspace(workspace, need)
-    _on_gpu(a, a_scales, w, w_scales, offsets, out, workspace)
-    c = _Call(stream, a.device)
+    c = _Call(stream, a, a_scales, w, w_scales, offsets, out, workspace)
     out = c.empty((M, N), dtype) if out is None else out
-    workspace = c.workspace(workspace, need)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
     c.run("zinc_moe_gemm_fp8", _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), E, M, N, K, code,
-          _ptr(out), _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+          _ptr(out), ws, ws_bytes)
     return out
 
 
@@ -892,16 +905,15 @@ def zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scal
     if E < 1 or E > 1024 or top_k > E:
         raise ValueError("there must be 1..1024 experts and top_k must not exceed them")
     if y is not None:
-        _need(y, x.dtype, (M, hidden), "y")
+        _fits(y, x.dtype, (M, hidden), "y")
     _dev_error(dev_error)
     need = moe_fp8_workspace_size(M, top_k, E, hidden, inter, x.dtype)
     _workspace(workspace, need)
-    _on_gpu(w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, expert_ids, expert_weights, y, workspace,
-            dev_error)
-    c = _Call(stream, x.device)
+    c = _Call(stream, w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, expert_ids, expert_weights, y,
+              workspace, dev_error)
     y = c.empty((M, hidden), x.dtype) if y is None else y
-    workspace = c.workspace(workspace, need)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
     c.run("zinc_moe_fp8_experts", _ptr(w_gate), _ptr(gate_scales), _ptr(w_up), _ptr(up_scales), _ptr(w_down),
           _ptr(down_scales), E, hidden, inter, _ptr(x), code, M, _ptr(expert_ids), _ptr(expert_weights), top_k, _ptr(y),
-          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _ptr(dev_error))
+          ws, ws_bytes, _ptr(dev_error))
     return y

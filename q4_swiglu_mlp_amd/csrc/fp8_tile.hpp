@@ -7,8 +7,8 @@
 // are copied straight to LDS (16 bytes a lane, no registers in between) into
 // one of two buffers while the waves multiply from the other; one barrier a
 // step.  An LDS row is 128 bytes, its eight 16-byte pieces stored in the order
-// piece ^ (row & 7), so that the lanes of a read, which run over rows, spread
-// over all banks.  Which k a lane's piece holds is free as long as both
+// piece ^ ((row >> 1) & 7), so that the lanes of a read, which run over rows,
+// spread over all 64 banks (two rows fill them).  Which k a lane's piece holds is free as long as both
 // operands agree: lane half h takes pieces h, h + 2, h + 4, h + 6.
 #pragma once
 
@@ -150,6 +150,11 @@ __device__ __forceinline__ i32x4_t load_piece(Buffer b, int off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
 }
 
+// The same for the whole workgroup and not written by the kernel: scalar loads.
+__device__ __forceinline__ const __attribute__((address_space(4))) float* uniform(const float* p) {
+  return (const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
+
 // DUAL: columns [0, TN / 2) of the tile are gate's rows, the others up's, and the
 // output is silu(gate) up quantised to e4m3 (one block of 128 columns a tile).
 template <int TM, int TN, int WM, int WN, bool EXACT, bool DUAL, typename T>
@@ -159,12 +164,14 @@ struct TileKernel {
   static constexpr int COLS = DUAL ? TN / 2 : TN;   // output columns of a tile
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
+  static constexpr int SB = TN / 128;               // w's scale blocks across the tile
   static_assert(TM % (8 * WAVES) == 0 && COLS % (8 * WAVES) == 0 && THREADS >= TM, "tile shape");
+  static_assert(SB >= 1 && TN / WN <= 128 && WAVES % 2 == 0, "a wave's columns share one scale");
   static_assert(!DUAL || (NT == 2 && COLS == 128), "a quantised tile is one block wide");
 
   struct Smem {
     uint8_t tile[2][ROWS * 128];
-    float sa[2][4][TM];
+    float scale[2][SB][4][TM];   // a's times w's, of four steps, two of them
   };
 
   static __device__ __forceinline__ void run(const GemmArgs& g, Smem& sm) {
@@ -179,7 +186,7 @@ struct TileKernel {
     // Copy plan: instruction i of a wave carries LDS rows 8 (i WAVES + wave) .. + 7,
     // by buffer loads whose bound is the tile's part of the matrix: rows behind
     // its last are not read (their products go nowhere).
-    const int piece = (lane & 7) ^ (lane >> 3);
+    const int piece = (lane & 7) ^ ((lane >> 4) + 4 * (wave & 1));
     const int row0 = 8 * wave + (lane >> 3);
     const uint8_t* a = g.a + (size_t)rt.first * K;
     const size_t w_at = ((size_t)rt.expert * N + n0) * K;
@@ -205,7 +212,8 @@ struct TileKernel {
         }
       }
     };
-    // a's scales, four blocks at a time: one thread a row
+    // scales of four steps at a time, a's times w's: one thread a row.  a's are
+    // loaded two steps before they are put, w's are scalar loads.
     const float* sa_row = g.sa + (size_t)(rt.first + min(tid, rt.rows - 1)) * KB;
     float s4[4];
     auto load_scales = [&](int kb) {
@@ -215,28 +223,25 @@ struct TileKernel {
       }
     };
     auto put_scales = [&](int kb) {
-      if (tid < TM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sm.sa[(kb >> 2) & 1][i][tid] = s4[i];
+      for (int b = 0; b < SB; ++b) {
+        const int blk = DUAL ? nt : min((n0 >> 7) + b, NB - 1);
+        const auto sw = uniform((DUAL && b ? g.sw2 : g.sw) + ((size_t)rt.expert * NB + blk) * KB);
+        float t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = sw[min(kb + i, KB - 1)];
+        if (tid < TM) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sm.scale[(kb >> 2) & 1][b][i][tid] = s4[i] * t[i];
+        }
       }
     };
-    // w's scales: one a wave and step (its columns lie in one block of 128)
-    const float* sw1;
-    const float* sw2 = nullptr;
-    if (DUAL) {
-      const size_t at = ((size_t)rt.expert * NB + nt) * KB;
-      sw1 = g.sw + at;
-      sw2 = g.sw2 + at;
-    } else {
-      const int blk = min((n0 + wn * (TN / WN)) >> 7, NB - 1);
-      sw1 = g.sw + ((size_t)rt.expert * NB + blk) * KB;
-    }
 
     f32x16_t acc[MT][NT] = {};
     // byte offsets of the lane's four pieces in an LDS row block
     int at[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) at[j] = l32 * 128 + (((half + 2 * j) ^ (lane & 7)) << 4);
+    for (int j = 0; j < 4; ++j) at[j] = l32 * 128 + (((half + 2 * j) ^ ((lane >> 1) & 7)) << 4);
 
     load_scales(0);
     put_scales(0);
@@ -246,13 +251,11 @@ struct TileKernel {
     asm volatile("" ::: "memory");
     for (int kb = 0; kb < KB; ++kb) {
       const int buf = kb & 1;
-      const bool scales = (kb & 3) == 0 && kb + 4 < KB;
+      if ((kb & 3) == 0 && kb + 4 < KB) load_scales(kb + 4);
       if (kb + 1 < KB) stage(buf ^ 1, kb + 1);
-      if (scales) load_scales(kb + 4);
-      const float t1 = sw1[kb], t2 = DUAL ? sw2[kb] : 0.0f;
       const uint8_t* ta = sm.tile[buf] + wm * (TM / WM) * 128;
       const uint8_t* tw = sm.tile[buf] + TM * 128 + (DUAL ? wn * 32 : wn * (TN / WN)) * 128;
-      const float* tsa = sm.sa[(kb >> 2) & 1][kb & 3] + wm * (TM / WM) + l32;
+      const float* ts = sm.scale[(kb >> 2) & 1][DUAL ? 0 : wn * (TN / WN) / 128][kb & 3] + wm * (TM / WM) + l32;
       Frag<EXACT> fw[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -271,7 +274,11 @@ struct TileKernel {
       };
       Frag<EXACT> fa;
       f32x16_t d[2];
-      float st[2];
+      float st[MT][DUAL ? NT : 1];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < (DUAL ? NT : 1); ++j) st[i][j] = ts[j * 4 * TM + i * 32];
       read_a(0);
 #pragma unroll
       for (int t = 0; t <= MT * NT; ++t) {
@@ -281,19 +288,18 @@ struct TileKernel {
             fa.set(p);
             if (i + 1 < MT) read_a(i + 1);
           }
-          st[t & 1] = tsa[i * 32] * (DUAL && j == 1 ? t2 : t1);
           d[t & 1] = mfma_block(fw[j], fa);
         }
         if (t > 0) {
           const int u = t - 1;
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            acc[u / NT][u % NT][r] = fmaf(st[u & 1], d[u & 1][r], acc[u / NT][u % NT][r]);
+            acc[u / NT][u % NT][r] = fmaf(st[u / NT][DUAL ? u % NT : 0], d[u & 1][r], acc[u / NT][u % NT][r]);
           asm volatile("" : "+v"(acc[u / NT][u % NT]));   // here, not behind the loop's branches
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (scales) put_scales(kb + 4);
+      if ((kb & 3) == 2 && kb + 2 < KB) put_scales(kb + 2);
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
