@@ -9,8 +9,8 @@
 // are copied straight to LDS (16 bytes a lane, no registers in between) into
 // one of two buffers while the waves multiply from the other; one barrier a
 // step.  An LDS row is 128 bytes, its eight 16-byte pieces stored in the order
-// piece ^ ((row >> 1) & 7), so that the lanes of a read, which run over rows,
-// spread over all 64 banks (two rows fill them).  Which k a lane's piece holds is free as long as both
+// piece ^ ((row >> 1) & 7) (w's: piece ^ w_turn(row)), so that the lanes of a read,
+// which run over rows, spread over all 64 banks (two rows fill them).  Which k a lane's piece holds is free as long as both
 // operands agree: lane quarter q takes pieces q and q + 4.
 #pragma once
 
@@ -111,26 +111,11 @@ struct GemmArgs {
   const float* sw2;
   const int32_t* offsets;
   int E, M, N, K;
-  int row_tiles, col_tiles;
+  int row_tiles, col_tiles;   // an upper bound of the row tiles, where experts are grouped
+  int splits;           // parts of K, each with its own output [M x N] behind the last one's
   void* c;
   float* cs;            // scales of a quantised output
 };
-
-// Order of the workgroups: consecutive ids go to the eight XCDs in turn, so each
-// XCD takes a contiguous run of tiles; within it eight row tiles are walked per
-// column, which keeps both operands' tiles in its L2.
-__device__ __forceinline__ bool tile_of_block(const GemmArgs& g, int& mt, int& nt) {
-  constexpr int kBand = 8;
-  const long long total = (long long)g.row_tiles * g.col_tiles, per = (total + 7) / 8;
-  const long long t = (long long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || t >= total) return false;
-  const long long band = t / ((long long)kBand * g.col_tiles);
-  const int in = (int)(t - band * kBand * g.col_tiles);
-  const int size = min(kBand, g.row_tiles - (int)band * kBand);
-  nt = in / size;
-  mt = (int)band * kBand + in - nt * size;
-  return true;
-}
 
 // Buffer loads bounded by a matrix's `bytes` from p: bytes behind them read as zero
 // and touch no memory.
@@ -153,6 +138,12 @@ __device__ __forceinline__ const __attribute__((address_space(4))) float* unifor
 
 // DUAL: columns [0, TN / 2) of the tile are gate's rows, the others up's, and the
 // output is silu(gate) up quantised to e4m3 (one block of 128 columns a tile).
+//
+// Workgroups are persistent: each walks its units (a tile, or a part of its K)
+// and copies the next unit's first blocks while it finishes the one before, so a
+// unit costs its steps and its stores.  Consecutive workgroup ids go to the
+// eight XCDs in turn, so an XCD takes a contiguous run of the units; eight row
+// tiles are walked per column, which keeps both operands' tiles in its L2.
 template <int TM, int TN, int WM, int WN, bool EXACT, bool DUAL, typename T>
 struct TileKernel {
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -161,99 +152,191 @@ struct TileKernel {
   static constexpr int COLS = DUAL ? TN / 2 : TN;   // output columns of a tile
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
-  static constexpr int SB = TN / 128;               // w's scale blocks across the tile
-  static_assert(TM % (8 * WAVES) == 0 && COLS % (8 * WAVES) == 0 && THREADS >= TM, "tile shape");
-  static_assert(SB >= 1 && TN / WN <= 128 && WAVES % 2 == 0, "a wave's columns share one scale");
+  static constexpr int BAND = 8;                    // row tiles walked per column
+  static_assert(TM % (8 * WAVES) == 0 && COLS % (8 * WAVES) == 0 && THREADS >= TM && TM % 64 == 0, "tile shape");
+  static_assert(TN / WN <= 128 && TN / WN % 32 == 0 && WAVES % 4 == 0, "a wave's columns share one scale");
   static_assert(!DUAL || (NT == 4 && COLS == 128), "a quantised tile is one block wide");
+
+  // How the pieces of w's LDS row are turned: rows are read as 8 q + r, q and r below 4.
+  static __device__ __forceinline__ int w_turn(int row) { return ((row >> 1) & 1) + 2 * ((row >> 3) & 3); }
 
   struct Smem {
     uint8_t tile[2][ROWS * 128];
-    float scale[2][SB][4][TM];   // a's times w's, of four steps, two of them
+    float sa[2][TM];                      // a's scales of the buffer's block
+    uint32_t part[DUAL ? WN * TM : 1];    // the waves' row maxima
+  };
+  // behind it, where experts are grouped: starts[E + 1], the experts' first rows,
+  // and ends[E], the row tiles up to and with each
+  static size_t smem_bytes(int experts) { return sizeof(Smem) + (experts ? 4 * (2 * (size_t)experts + 1) : 0); }
+
+  struct Unit {
+    int expert, first, rows;   // the tile's rows of a
+    int nt, split, kb0, kbs;   // its column tile and blocks of K
   };
 
+  // Row tiles of all experts, and the tables; offsets are cut to [0, M] and, where
+  // they do not ascend, the range is empty.
+  static __device__ __forceinline__ int make_tables(const GemmArgs& g, int32_t* starts, int32_t* ends) {
+    const int lane = threadIdx.x & 63;
+    int seen = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int lo = e < g.E ? min(max(g.offsets[e], 0), g.M) : 0;
+      const int hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.M) : 0;
+      const int n = (hi - lo + TM - 1) / TM;
+      int scan = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(scan, d, 64);
+        if (lane >= d) scan += o;
+      }
+      if (threadIdx.x < 64 && e < g.E) {
+        starts[e] = lo;
+        if (e == g.E - 1) starts[g.E] = hi;
+        ends[e] = seen + scan;
+      }
+      seen += __builtin_amdgcn_readlane(scan, 63);
+    }
+    return seen;
+  }
+
+  static __device__ __forceinline__ Unit unit_at(const GemmArgs& g, const int32_t* starts, const int32_t* ends,
+                                                 int row_tiles, int KB, long long u) {
+    Unit r;
+    const int per_row = g.col_tiles * g.splits;
+    const int band = (int)(u / ((long long)BAND * per_row));
+    const int in = (int)(u - (long long)band * BAND * per_row);
+    const int size = min(BAND, row_tiles - band * BAND);
+    const int col = in / size, mt = band * BAND + in - col * size;
+    r.split = col / g.col_tiles;
+    r.nt = col - r.split * g.col_tiles;
+    const int each = (KB + g.splits - 1) / g.splits;
+    r.kb0 = r.split * each;
+    r.kbs = min(each, KB - r.kb0);
+    if (!g.offsets) {
+      r.expert = 0;
+      r.first = mt * TM;
+      r.rows = min(TM, g.M - r.first);
+      return r;
+    }
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int end = e < g.E ? ends[e] : 0x7FFFFFFF;
+      const uint64_t here = __ballot(end > mt);
+      if (here) {
+        r.expert = e0 + (int)__builtin_ctzll(here);
+        break;
+      }
+    }
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+    const int before = r.expert ? ends[r.expert - 1] : 0, lo = starts[r.expert];
+    r.first = __builtin_amdgcn_readfirstlane(lo + (mt - before) * TM);
+    r.rows = __builtin_amdgcn_readfirstlane(min(TM, max(lo, starts[r.expert + 1]) - r.first));
+    return r;
+  }
+
   static __device__ __forceinline__ void run(const GemmArgs& g, Smem& sm) {
-    int mt, nt;
-    if (!tile_of_block(g, mt, nt)) return;
-    const RowTile rt = find_tile<TM>(g.offsets, g.E, g.M, mt);
-    if (rt.rows <= 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, l16 = lane & 15, quad = lane >> 4;
     const int K = g.K, N = g.N, KB = (K + 127) / 128, NB = (N + 127) / 128;
-    const int n0 = nt * COLS;
-    // Copy plan: instruction i of a wave carries LDS rows 8 (i WAVES + wave) .. + 7,
-    // by buffer loads whose bound is the tile's part of the matrix: rows behind
-    // its last are not read (their products go nowhere).
-    const int piece = (lane & 7) ^ ((lane >> 4) + 4 * (wave & 1));
-    const int row0 = 8 * wave + (lane >> 3);
-    const uint8_t* a = g.a + (size_t)rt.first * K;
-    const size_t w_at = ((size_t)rt.expert * N + n0) * K;
-    const int cols = min(COLS, N - n0);
-    const auto ra = tile_buffer(a, rt.rows * K);
-    const auto rw1 = tile_buffer(g.w + w_at, cols * K);
-    const auto rw2 = tile_buffer((DUAL ? g.w2 : g.w) + w_at, cols * K);
-    const int v0 = row0 * K + piece * 16;
-    auto copy_piece = [&](int i, int buf, int kb) {
+    int32_t* starts = reinterpret_cast<int32_t*>(&sm + 1);
+    int32_t* ends = starts + g.E + 1;
+    int row_tiles = g.row_tiles;
+    if (g.offsets) {
+      row_tiles = make_tables(g, starts, ends);
+      __syncthreads();
+    }
+    // this workgroup's units: u, u + stride, ... below last
+    const long long total = (long long)row_tiles * g.col_tiles * g.splits, per = (total + 7) / 8;
+    const int stride = gridDim.x / 8;
+    const long long last = min(total, (long long)((blockIdx.x & 7) + 1) * per);
+    long long u = (long long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (u >= last) return;
+
+    // Copies run ahead of the products: unit `ld`, its block `lk`, by buffer loads whose
+    // bounds are the tile's parts of the matrices (rows behind the last are not
+    // read; their products go nowhere).  Instruction i of a wave carries LDS rows
+    // 8 (i WAVES + wave) .. + 7.
+    const int a_piece = (lane & 7) ^ ((lane >> 4) + 4 * (wave & 1));
+    const int w_piece = (lane & 7) ^ (((lane >> 4) & 1) + 2 * (wave & 3));
+    const int v0 = (8 * wave + (lane >> 3)) * K;
+    Unit ld = unit_at(g, starts, ends, row_tiles, KB, u);
+    long long lu = u;
+    int lk = 0;
+    Buffer ra, rw1, rw2, rs;
+    auto open = [&] {
+      const int n0 = ld.nt * COLS, cols = min(COLS, N - n0);
+      const size_t w_at = ((size_t)ld.expert * N + n0) * K;
+      ra = tile_buffer(g.a + (size_t)ld.first * K, ld.rows * K);
+      rw1 = tile_buffer(g.w + w_at, cols * K);
+      rw2 = tile_buffer((DUAL ? g.w2 : g.w) + w_at, cols * K);
+      rs = tile_buffer(reinterpret_cast<const uint8_t*>(g.sa + (size_t)ld.first * KB), ld.rows * KB * 4);
+    };
+    open();
+    auto copy_piece = [&](int i, int buf) {
       const int r = i * WAVES * 8;   // the instruction's first row, less the wave's
       const int in = r < TM ? r : (r - TM) % COLS;
-      const auto rs = r < TM ? ra : r < TM + COLS ? rw1 : rw2;
-      to_lds(rs, v0 + in * K + kb * 128, sm.tile[buf] + (i * WAVES + wave) * 1024);
+      to_lds(r < TM ? ra : r < TM + COLS ? rw1 : rw2,
+             v0 + in * K + (ld.kb0 + lk) * 128 + 16 * (r < TM ? a_piece : w_piece), sm.tile[buf] + (i * WAVES + wave) * 1024);
     };
-    auto cut_piece = [&](int i, int buf, int kb) {   // of the last block, cut short: zeros behind K
-      const int r = i * WAVES * 8;
-      const int in = r < TM ? r : (r - TM) % COLS;
-      const auto rs = r < TM ? ra : r < TM + COLS ? rw1 : rw2;
-      const bool is_in = kb * 128 + piece * 16 < K;
-      const i32x4_t v = load_piece(rs, is_in ? v0 + in * K + kb * 128 : 0);
-      *reinterpret_cast<i32x4_t*>(sm.tile[buf] + (i * WAVES + wave) * 1024 + lane * 16) =
-          is_in ? v : i32x4_t{0, 0, 0, 0};
+    auto copy_scales = [&](int buf) {
+      if (wave * 64 < TM)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(sm.sa[buf] + wave * 64),
+                                                 4, (tid * KB + ld.kb0 + lk) * 4, 0, 0, 0);
     };
-    auto stage = [&](int buf, int kb) {
+    auto whole = [&] { return lu < last && (ld.kb0 + lk + 1) * 128 <= K; };
+    auto copy_cut = [&](int buf) {   // the last block of K, cut short: zeros behind it
+      if (lu >= last) return;
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        if ((kb + 1) * 128 <= K)
-          copy_piece(i, buf, kb);
-        else
-          cut_piece(i, buf, kb);
+        const int r = i * WAVES * 8, kb = ld.kb0 + lk;
+        const int in = r < TM ? r : (r - TM) % COLS, piece = r < TM ? a_piece : w_piece;
+        const bool is_in = kb * 128 + piece * 16 < K;
+        const i32x4_t v = load_piece(r < TM ? ra : r < TM + COLS ? rw1 : rw2, is_in ? v0 + in * K + kb * 128 + piece * 16 : 0);
+        *reinterpret_cast<i32x4_t*>(sm.tile[buf] + (i * WAVES + wave) * 1024 + lane * 16) =
+            is_in ? v : i32x4_t{0, 0, 0, 0};
+      }
+      copy_scales(buf);
+    };
+    auto advance = [&] {
+      if (lu >= last || ++lk < ld.kbs) return;
+      lk = 0;
+      lu += stride;
+      if (lu < last) {
+        ld = unit_at(g, starts, ends, row_tiles, KB, lu);
+        open();
       }
     };
-    // scales of four steps at a time, a's times w's: one thread a row.  a's are
-    // loaded two steps before they are put, w's are scalar loads.
-    const float* sa_row = g.sa + (size_t)(rt.first + min(tid, rt.rows - 1)) * KB;
-    float s4[4];
-    auto load_scales = [&](int kb) {
-      if (tid < TM) {
+    auto copy_all = [&](int buf) {
+      if (whole()) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s4[i] = sa_row[min(kb + i, KB - 1)];
+        for (int i = 0; i < PIECES; ++i) copy_piece(i, buf);
+        copy_scales(buf);
+      } else {
+        copy_cut(buf);
       }
-    };
-    auto put_scales = [&](int kb) {
-#pragma unroll
-      for (int b = 0; b < SB; ++b) {
-        const int blk = DUAL ? nt : min((n0 >> 7) + b, NB - 1);
-        const auto sw = uniform((DUAL && b ? g.sw2 : g.sw) + ((size_t)rt.expert * NB + blk) * KB);
-        float t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = sw[min(kb + i, KB - 1)];
-        if (tid < TM) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sm.scale[(kb >> 2) & 1][b][i][tid] = s4[i] * t[i];
-        }
-      }
+      advance();
     };
 
-    f32x4_t acc[MT][NT] = {};
+    f32x4_t acc[MT][NT];
     // byte offsets of the lane's two pieces in an LDS row block
-    int at[2];
+    // MFMA row 4 q + r of column tile j is column 32 (j / 2) + 8 q + 4 (j % 2) + r of
+    // the wave's, so that a lane's sums of two column tiles are eight neighbours.
+    int at[2], wat[2];
+    const int wrow = 8 * (l16 >> 2) + (l16 & 3);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) at[j] = l16 * 128 + (((quad + 4 * j) ^ ((lane >> 1) & 7)) << 4);
-
+    for (int j = 0; j < 2; ++j) {
+      at[j] = l16 * 128 + (((quad + 4 * j) ^ ((lane >> 1) & 7)) << 4);
+      wat[j] = wrow * 128 + (((quad + 4 * j) ^ w_turn(wrow)) << 4);
+    }
     // Fragments in flight: w's of a step, read at the end of the step before; a's
     // one 16-row tile ahead, the last two together.
     i32x4_t wr[NT][2], ar[2][2];
     auto read_w = [&](int j, int buf) {
-      const int row = TM + (DUAL ? wn * 32 + (j >> 1) * COLS + (j & 1) * 16 : wn * (TN / WN) + j * 16);
+      const int row = TM + (DUAL ? wn * 32 + (j >> 1) * COLS : wn * (TN / WN) + (j >> 1) * 32) + (j & 1) * 4;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) wr[j][q] = *reinterpret_cast<const i32x4_t*>(sm.tile[buf] + row * 128 + at[q]);
+      for (int q = 0; q < 2; ++q) wr[j][q] = *reinterpret_cast<const i32x4_t*>(sm.tile[buf] + row * 128 + wat[q]);
     };
     auto read_a = [&](int i, int slot, int buf) {
       const int row = wm * (TM / WM) + i * 16;
@@ -265,116 +348,142 @@ struct TileKernel {
     // for the next step's while there is work left.  A tile's block sums lie in
     // d[t % (LAG + 1)] and are scaled and added LAG tiles later, also across steps.
     constexpr int TILES = MT * NT, PAIR = (MT - 2) * NT;
-    static_assert(MT >= 4 && TILES % (LAG + 1) == 0 && 2 * NT >= LAG && 2 * NT >= PIECES, "tile shape");
-    f32x4_t d[LAG + 1] = {};
-    float st[MT][DUAL ? 2 : 1] = {};
+    static_assert(MT >= 4 && TILES % (LAG + 1) == 0 && 2 * NT >= LAG, "tile shape");
+    constexpr int EACH = (PIECES + 2 * NT - 1) / (2 * NT);   // copies beside a tile of the last quarter
+    f32x4_t d[LAG + 1];
+    float st[MT][DUAL ? 2 : 1];
     auto row_of = [](int t) { return t < PAIR ? t / NT : MT - 2 + ((t - PAIR) & 1); };
     auto col_of = [](int t) { return t < PAIR ? t % NT : (t - PAIR) >> 1; };
-    auto add = [&](int u) {
-      const int i = row_of(u), j = col_of(u);
+    auto add = [&](int v) {
+      const int i = row_of(v), j = col_of(v);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        acc[i][j][r] = fmaf(st[i][DUAL ? j >> 1 : 0], d[u % (LAG + 1)][r], acc[i][j][r]);
+        acc[i][j][r] = fmaf(st[i][DUAL ? j >> 1 : 0], d[v % (LAG + 1)][r], acc[i][j][r]);
       asm volatile("" : "+v"(acc[i][j]));   // here, not behind the loop's branches
     };
 
-    load_scales(0);
-    put_scales(0);
-    stage(0, 0);
-    if (KB > 1) stage(1, 1);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    copy_all(0);
+    const bool two = whole();   // the second block's copies may be in flight behind the first's
+    copy_all(1);
+    if (two)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PIECES) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int j = 0; j < NT; ++j) read_w(j, 0);
     read_a(0, 0, 0);
-    for (int kb = 0; kb < KB; ++kb) {
-      const int buf = kb & 1;
-      if ((kb & 3) == 0 && kb + 4 < KB) load_scales(kb + 4);
-      const float* ts = sm.scale[(kb >> 2) & 1][DUAL ? 0 : wn * (TN / WN) / 128][kb & 3] + wm * (TM / WM) + l16;
-      float sn[MT][DUAL ? 2 : 1];
+    int buf = 0;
+    for (; u < last; u += stride) {
+      const Unit cu = unit_at(g, starts, ends, row_tiles, KB, u);
+      const int n0 = cu.nt * COLS;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < (DUAL ? 2 : 1); ++j) sn[i][j] = ts[j * 4 * TM + i * 16];
-      const bool whole = (kb + 3) * 128 <= K;   // the block after the next one is not cut short
-      Frag<EXACT> fw[NT], fa[2];
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        const int i = row_of(t), j = col_of(t);
-        if (t < PAIR && j == 0) {
-          fa[0].set(ar[0]);
-          if (i + 1 < MT - 2) {
-            read_a(i + 1, 0, buf);
+      for (int i = 0; i <= LAG; ++i) d[i] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int b = 0; b < (DUAL ? 2 : 1); ++b) st[i][b] = 0.0f;
+      // w's scales: one a wave and step (two with gate and up)
+      const size_t sw_at =
+          ((size_t)cu.expert * NB + (DUAL ? cu.nt : min((n0 + wn * (TN / WN)) >> 7, NB - 1))) * KB + cu.kb0;
+      const auto sw1 = uniform(g.sw + sw_at), sw2 = uniform((DUAL ? g.sw2 : g.sw) + sw_at);
+      for (int kb = 0; kb < cu.kbs; ++kb, buf ^= 1) {
+        const float t1 = sw1[kb], t2 = DUAL ? sw2[kb] : 0.0f;
+        float sn[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sn[i] = sm.sa[buf][wm * (TM / WM) + i * 16 + l16];
+        const bool fast = whole();
+        Frag<EXACT> fw[NT], fa[2];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const int i = row_of(t), j = col_of(t);
+          if (t < PAIR && j == 0) {
+            fa[0].set(ar[0]);
+            if (i + 1 < MT - 2) {
+              read_a(i + 1, 0, buf);
+            } else {
+              read_a(MT - 2, 0, buf);
+              read_a(MT - 1, 1, buf);
+            }
+          }
+          if (t < NT) fw[t].set(wr[t]);
+          if (t == PAIR) {
+            fa[0].set(ar[0]);
+            fa[1].set(ar[1]);
+            // the next block has landed, and every wave has read what it needs of this one
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (!fast) copy_cut(buf);
+          }
+          d[t % (LAG + 1)] = mfma_block(fw[j], fa[t < PAIR ? 0 : i - (MT - 2)]);
+          if (t >= PAIR) {
+            const int v = t - PAIR;
+            if (fast) {
+#pragma unroll
+              for (int c = v * EACH; c < (v + 1) * EACH; ++c)
+                if (c < PIECES) copy_piece(c, buf);
+              if (t == TILES - 1) copy_scales(buf);
+            }
+            if (v & 1) read_w(j, buf ^ 1);
+            if (t == TILES - 1) read_a(0, 0, buf ^ 1);
+          }
+          if (t < LAG) {
+            add(TILES - LAG + t);
+            if (t == LAG - 1) {
+#pragma unroll
+              for (int r = 0; r < MT; ++r) {
+                st[r][0] = sn[r] * t1;
+                if (DUAL) st[r][DUAL ? 1 : 0] = sn[r] * t2;
+              }
+            }
           } else {
-            read_a(MT - 2, 0, buf);
-            read_a(MT - 1, 1, buf);
+            add(t - LAG);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (t < NT) fw[t].set(wr[t]);
-        if (t == PAIR) {
-          fa[0].set(ar[0]);
-          fa[1].set(ar[1]);
-          if ((kb & 3) == 2 && kb + 2 < KB) put_scales(kb + 2);
-          // the next block has landed, and every wave has read what it needs of this one
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-          if (!whole && kb + 2 < KB) stage(buf, kb + 2);
-        }
-        d[t % (LAG + 1)] = mfma_block(fw[j], fa[t < PAIR ? 0 : i - (MT - 2)]);
-        if (t >= PAIR) {
-          const int v = t - PAIR;
-          if (v < PIECES && whole) copy_piece(v, buf, kb + 2);
-          if (v & 1) read_w(j, buf ^ 1);
-          if (t == TILES - 1) read_a(0, 0, buf ^ 1);
-        }
-        if (t < LAG) {
-          add(TILES - LAG + t);
-          if (t == LAG - 1) {
-#pragma unroll
-            for (int r = 0; r < MT; ++r)
-#pragma unroll
-              for (int b = 0; b < (DUAL ? 2 : 1); ++b) st[r][b] = sn[r][b];
-          }
-        } else {
-          add(t - LAG);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        advance();
       }
-    }
 #pragma unroll
-    for (int t = 0; t < LAG; ++t) add(TILES - LAG + t);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      for (int t = 0; t < LAG; ++t) add(TILES - LAG + t);
+      store(g, sm, cu, n0, N, NB, wm, wn, l16, quad, acc);
+    }
+  }
 
+  static __device__ __forceinline__ void store(const GemmArgs& g, Smem& sm, const Unit& cu, int n0, int N, int NB,
+                                               int wm, int wn, int l16, int quad, f32x4_t (&acc)[MT][NT]) {
     if constexpr (!DUAL) {
-      T* c = static_cast<T*>(g.c);
-      const bool wide = N % 4 == 0;   // rows' outputs stay aligned to four
+      T* c = static_cast<T*>(g.c) + (size_t)cu.split * g.M * N;
+      const bool wide = N % 8 == 0;   // rows' outputs stay aligned to eight
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int m = wm * (TM / WM) + i * 16 + l16;
-        if (m >= rt.rows) continue;
-        T* row = c + (size_t)(rt.first + m) * N;
+        if (m >= cu.rows) continue;
+        T* row = c + (size_t)(cu.first + m) * N;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int n = n0 + wn * (TN / WN) + j * 16 + 4 * quad;
+        for (int j = 0; j < NT; j += 2) {
+          const int n = n0 + wn * (TN / WN) + j * 16 + 8 * quad;
+          float v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
           if (wide) {
-            typedef T T4 __attribute__((ext_vector_type(4)));
-            T4 o;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = (T)acc[i][j][r];
-            if (n < N) *reinterpret_cast<T4*>(row + n) = o;
+            if (n < N) store8(row + n, v);
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (n + r < N) row[n + r] = (T)acc[i][j][r];
+            for (int r = 0; r < 8; ++r)
+              if (n + r < N) row[n + r] = (T)v[r];
           }
         }
       }
     } else {
       // h = silu(gate) up; a row's maximum over the 128 columns: in the lane, over
       // the four lanes of the row, over the WN waves
-      uint32_t* part = reinterpret_cast<uint32_t*>(&sm.tile[0][0]);   // [WN][TM]
+      uint32_t* part = sm.part;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         uint32_t m = 0;
@@ -398,16 +507,15 @@ struct TileKernel {
 #pragma unroll
         for (int v = 0; v < WN; ++v) top = max(top, part[v * TM + m]);
         const uint32_t f = scale_field(top);
-        if (m >= rt.rows) continue;
-        uint8_t* row = static_cast<uint8_t*>(g.c) + (size_t)(rt.first + m) * N + n0 + wn * 32 + 4 * quad;
+        if (m >= cu.rows) continue;
+        uint8_t* row = static_cast<uint8_t*>(g.c) + (size_t)(cu.first + m) * N + n0 + wn * 32 + 8 * quad;
         float v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) v[r] = acc[i][r >> 2][r & 3];
-        const uint2 o = to_e4m3(v, inverse_scale_of(f));
-        *reinterpret_cast<uint32_t*>(row) = o.x;
-        *reinterpret_cast<uint32_t*>(row + 16) = o.y;
-        if (wn == 0 && quad == 0) g.cs[(size_t)(rt.first + m) * NB + nt] = scale_of(f);
+        *reinterpret_cast<uint2*>(row) = to_e4m3(v, inverse_scale_of(f));
+        if (wn == 0 && quad == 0) g.cs[(size_t)(cu.first + m) * NB + cu.nt] = scale_of(f);
       }
+      __syncthreads();   // the maxima are read
     }
   }
 };

@@ -42,15 +42,36 @@ hipError_t allow_lds(const void* kernel, int bytes) {
 
 constexpr int kLds = 160 * 1024;
 
-template <typename KERNEL>
-hipError_t run_tiles(GemmArgs g, int TM, int cols, hipStream_t stream) {
-  g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, TM);
-  g.col_tiles = (g.N + cols - 1) / cols;
-  const long long per = ((long long)g.row_tiles * g.col_tiles + 7) / 8;
-  constexpr int bytes = (int)sizeof(typename KERNEL::Smem);
-  const hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>), bytes);
+// Compute units of the current device (looked up once a device).
+hipError_t compute_units(int* n) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)(8 * per)), dim3(KERNEL::THREADS), bytes, stream, g);
+  *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*n) return hipSuccess;
+  e = hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e == hipSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+// As many persistent workgroups as the CUs hold by LDS and waves (two 256-register
+// waves a SIMD), a multiple of the eight XCDs.
+template <typename KERNEL>
+hipError_t run_tiles(GemmArgs g, int TM, int splits, hipStream_t stream) {
+  g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, TM);
+  g.col_tiles = (g.N + KERNEL::COLS - 1) / KERNEL::COLS;
+  g.splits = splits;
+  const int bytes = (int)KERNEL::smem_bytes(g.offsets ? g.E : 0);
+  hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>), kLds);
+  int cus = 0;
+  if (e == hipSuccess) e = compute_units(&cus);
+  if (e != hipSuccess) return e;
+  const int held = kLds / bytes < 8 / KERNEL::WAVES ? kLds / bytes : 8 / KERNEL::WAVES;
+  const long long units = (long long)g.row_tiles * g.col_tiles * splits, room = (long long)cus * held;
+  const long long blocks = units < room ? units : room;
+  hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)((blocks + 7) / 8 * 8)), dim3(KERNEL::THREADS), bytes, stream,
+                     g);
   return hipGetLastError();
 }
 
@@ -98,9 +119,9 @@ hipError_t gemm(const GemmArgs& g, hipStream_t stream) {
     case 4: return stream_product<4, T>(g, stream);
   }
   if constexpr (EXACT)
-    return run_tiles<TileKernel<128, 128, 2, 2, true, false, T>>(g, 128, 128, stream);
+    return run_tiles<TileKernel<128, 128, 2, 2, true, false, T>>(g, 128, 1, stream);
   else
-    return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 256, stream);
+    return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 1, stream);
 }
 
 template <typename T_IN>
@@ -203,7 +224,7 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
                     : stream_gate_up<float>(s, mt, stream);
   } else {
     e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
-    if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 128, stream);
+    if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 1, stream);
   }
   g.a = pl.hq;
   g.sa = pl.hs;
