@@ -112,7 +112,8 @@ struct GemmArgs {
   const int32_t* offsets;
   int E, M, N, K;
   int row_tiles, col_tiles;   // an upper bound of the row tiles, where experts are grouped
-  int splits;           // parts of K, each with its own output [M x N] behind the last one's
+  int splits;           // parts of K, each with its own output,
+  size_t part;          // this many values after the one before
   void* c;
   float* cs;            // scales of a quantised output
 };
@@ -153,6 +154,8 @@ struct TileKernel {
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
   static constexpr int BAND = 8;                    // row tiles walked per column
+  // workgroups a CU holds by registers: three waves a SIMD where a wave has 32 sums, else two
+  static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
   static_assert(TM % (8 * WAVES) == 0 && COLS % (8 * WAVES) == 0 && THREADS >= TM && TM % 64 == 0, "tile shape");
   static_assert(TN / WN <= 128 && TN / WN % 32 == 0 && WAVES % 4 == 0, "a wave's columns share one scale");
   static_assert(!DUAL || (NT == 4 && COLS == 128), "a quantised tile is one block wide");
@@ -458,7 +461,7 @@ struct TileKernel {
   static __device__ __forceinline__ void store(const GemmArgs& g, Smem& sm, const Unit& cu, int n0, int N, int NB,
                                                int wm, int wn, int l16, int quad, f32x4_t (&acc)[MT][NT]) {
     if constexpr (!DUAL) {
-      T* c = static_cast<T*>(g.c) + (size_t)cu.split * g.M * N;
+      T* c = static_cast<T*>(g.c) + (size_t)cu.split * g.part;
       const bool wide = N % 8 == 0;   // rows' outputs stay aligned to eight
 #pragma unroll
       for (int i = 0; i < MT; ++i) {

@@ -55,8 +55,7 @@ hipError_t compute_units(int* n) {
   return e;
 }
 
-// As many persistent workgroups as the CUs hold by LDS and waves (two 256-register
-// waves a SIMD), a multiple of the eight XCDs.
+// As many persistent workgroups as the CUs hold, a multiple of the eight XCDs.
 template <typename KERNEL>
 hipError_t run_tiles(GemmArgs g, int TM, int splits, hipStream_t stream) {
   g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, TM);
@@ -67,7 +66,7 @@ hipError_t run_tiles(GemmArgs g, int TM, int splits, hipStream_t stream) {
   int cus = 0;
   if (e == hipSuccess) e = compute_units(&cus);
   if (e != hipSuccess) return e;
-  const int held = kLds / bytes < 8 / KERNEL::WAVES ? kLds / bytes : 8 / KERNEL::WAVES;
+  const int held = kLds / bytes < KERNEL::HELD ? kLds / bytes : KERNEL::HELD;
   const long long units = (long long)g.row_tiles * g.col_tiles * splits, room = (long long)cus * held;
   const long long blocks = units < room ? units : room;
   hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)((blocks + 7) / 8 * 8)), dim3(KERNEL::THREADS), bytes, stream,
@@ -96,39 +95,123 @@ hipError_t run_stream(StreamArgs s, int cols, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows of a stream's tile in sixteens, 0 where the tiled kernel is the better one.
-int stream_tiles(int rows, int E) {
-  const int mean = E ? (rows + E - 1) / E : rows;
-  return mean <= 16 ? 1 : mean <= 32 ? 2 : mean <= 64 ? 4 : 0;
+// c = sum of the parts of K in their order; rows outside the experts' ranges are
+// left alone.
+template <typename T>
+__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ parts, size_t part, int splits, int M,
+                                                    int N, const int32_t* __restrict__ offsets, int E,
+                                                    T* __restrict__ c) {
+  const size_t total = (size_t)M * N;
+  size_t from = 0, to = total;
+  if (offsets) {
+    from = (size_t)min(max(offsets[0], 0), M) * N;
+    to = (size_t)min(max(offsets[E], 0), M) * N;
+  }
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < to; i += (size_t)gridDim.x * 1024) {
+    if (i + 4 <= from) continue;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(parts + i);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(parts + s * part + i);
+    if (i >= from && i + 4 <= to) {
+      typedef T T4 __attribute__((ext_vector_type(4)));
+      T4 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = (T)v[r];
+      *reinterpret_cast<T4*>(c + i) = o;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (i + r >= from && i + r < to) c[i + r] = (T)v[r];
+    }
+  }
 }
 
-template <int MT, typename T>
-hipError_t stream_product(const GemmArgs& g, hipStream_t stream) {
-  StreamArgs s{};
-  s.g = g;
-  const long long tiles = (g.N + 15) / 16 * (long long)(g.offsets ? (g.E < g.M ? g.E : g.M) : 1);
-  s.ks = tiles >= 4096 ? 1 : tiles >= 2048 ? 2 : tiles >= 512 ? 4 : 8;
-  return run_stream<StreamKernel<MT, 8, 4, 0, false, float, T>>(s, 8 / s.ks * 16, stream);
+// How a product is cut, by its sizes alone.  Times: us, 256 CUs, bf16 output.
+enum Shape { kStream, kSmall, kMiddle, kLarge, kLargest };
+struct Cut {
+  Shape shape;
+  int splits;
+};
+
+// Dense.
+// - Up to 16 rows the weight's stream: 1 x 11008 x 4096 11.8 against 15 for small
+//   tiles in four parts of K with their join.
+// - Else the largest tile (256 x 256, 128 x 256) with 160 units, five eighths of the CUs:
+//   1024 x 11008 x 4096 66 with the first (172 units) against 81 with small tiles, 512 rows
+//   43 with the second against 45 and 63, 2048 x 4096 x 11008 (128 and 256 units) 119 with
+//   the second against 163 with the first.
+// - Else small tiles (64 x 128), and where they are no more than the CUs, parts of K
+//   of eight blocks or more, up to 400 units: 64 x 11008 x 4096 17 in four parts against
+//   30 in one, 64 x 4096 x 11008 15 in eight against 58; their join costs 3 and more.
+Cut cut_dense(int M, int N, int K) {
+  if (M <= 16) return {kStream, 1};
+  const long long rows256 = (M + 255) / 256, cols256 = (N + 255) / 256, rows128 = (M + 127) / 128;
+  if (rows256 * cols256 >= 160) return {kLargest, 1};
+  if (rows128 * cols256 >= 160) return {kLarge, 1};
+  const long long units = (long long)((M + 63) / 64) * ((N + 127) / 128);
+  const int KB = (K + 127) / 128;
+  int splits = units <= 256 ? (int)((400 + units - 1) / units) : 1;
+  if (splits > KB / 8) splits = KB / 8 < 1 ? 1 : KB / 8;
+  const int each = (KB + splits - 1) / splits;
+  return {kSmall, (KB + each - 1) / each};   // no part is empty
+}
+
+// Grouped, by the mean rows of an expert (64 experts, 768 x 2048): 128 rows 41 with
+// small tiles, 43 with 128 x 128, 42 with 256 x 256; 256 rows 63, 55 and 69; 512
+// rows 97, 91 and 82.
+Cut cut_grouped(int rows, int E) {
+  const int mean = rows / E;
+  return {mean <= 128 ? kSmall : mean <= 384 ? kMiddle : kLargest, 1};
+}
+
+Cut cut(int M, int E, int N, int K) { return E ? cut_grouped(M, E) : cut_dense(M, N, K); }
+
+// Values from one part of K to the next, a multiple of eight.
+size_t part_values(int M, int N) { return ((size_t)M * N + 7) / 8 * 8; }
+
+template <bool EXACT, typename T>
+hipError_t small_tiles(const GemmArgs& g, int splits, hipStream_t stream) {
+  return run_tiles<TileKernel<64, 128, 1, 4, EXACT, false, T>>(g, 64, splits, stream);
 }
 
 template <bool EXACT, typename T>
-hipError_t gemm(const GemmArgs& g, hipStream_t stream) {
-  switch (stream_tiles(g.M, g.offsets ? g.E : 0)) {
-    case 1: return stream_product<1, T>(g, stream);
-    case 2: return stream_product<2, T>(g, stream);
-    case 4: return stream_product<4, T>(g, stream);
+hipError_t gemm(GemmArgs g, void* ws, hipStream_t stream) {
+  const Cut how = cut(g.M, g.offsets ? g.E : 0, g.N, g.K);
+  switch (how.shape) {
+    case kStream: {
+      // waves that share 16 columns, until there are 2048 of them or eight share
+      StreamArgs s{};
+      s.g = g;
+      const int tiles = (g.N + 15) / 16;
+      s.ks = tiles >= 2048 ? 1 : tiles >= 640 ? 2 : tiles >= 320 ? 4 : 8;
+      return run_stream<StreamKernel<1, 8, 4, 0, false, float, T>>(s, 8 / s.ks * 16, stream);
+    }
+    case kSmall: {
+      if (how.splits == 1) return small_tiles<EXACT, T>(g, 1, stream);
+      T* c = static_cast<T*>(g.c);
+      g.c = ws;
+      g.part = part_values(g.M, g.N);
+      const hipError_t e = small_tiles<EXACT, float>(g, how.splits, stream);
+      if (e != hipSuccess) return e;
+      const size_t quads = ((size_t)g.M * g.N + 1023) / 1024;
+      hipLaunchKernelGGL(k_join_parts<T>, dim3((unsigned)(quads < 2048 ? quads : 2048)), dim3(256), 0, stream,
+                         static_cast<const float*>(ws), g.part, how.splits, g.M, g.N, g.offsets, g.E, c);
+      return hipGetLastError();
+    }
+    case kMiddle: return run_tiles<TileKernel<128, 128, 2, 2, EXACT, false, T>>(g, 128, 1, stream);
+    case kLarge: return run_tiles<TileKernel<128, 256, 2, 4, EXACT, false, T>>(g, 128, 1, stream);
+    case kLargest:
+      // twice the operand registers leave the fp16 MFMAs the 128 x 256 tile
+      if constexpr (EXACT)
+        return run_tiles<TileKernel<128, 256, 2, 4, true, false, T>>(g, 128, 1, stream);
+      else
+        return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 1, stream);
   }
-  if constexpr (EXACT)
-    return run_tiles<TileKernel<128, 128, 2, 2, true, false, T>>(g, 128, 1, stream);
-  else
-    return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 1, stream);
+  return hipErrorUnknown;
 }
 
 template <typename T_IN>
-hipError_t stream_gate_up(const StreamArgs& s, int mt, hipStream_t stream) {
-  if (mt == 1) return run_stream<StreamKernel<1, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
-  if (mt == 2) return run_stream<StreamKernel<2, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
-  return run_stream<StreamKernel<4, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
+hipError_t stream_gate_up(const StreamArgs& s, hipStream_t stream) {
+  return run_stream<StreamKernel<1, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -164,7 +247,7 @@ ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, siz
 }  // namespace
 
 hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const float* sw, const int32_t* offsets,
-                           int E, int M, int N, int K, int out_type, void* c, void*, hipStream_t stream) {
+                           int E, int M, int N, int K, int out_type, void* c, void* ws, hipStream_t stream) {
   GemmArgs g{};
   g.a = static_cast<const uint8_t*>(a);
   g.sa = sa;
@@ -176,12 +259,16 @@ hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const 
   g.N = N;
   g.K = K;
   g.c = c;
-  if (out_type == 0) return gemm<false, _Float16>(g, stream);
-  if (out_type == 1) return gemm<false, __bf16>(g, stream);
-  return gemm<true, float>(g, stream);
+  if (out_type == 0) return gemm<false, _Float16>(g, ws, stream);
+  if (out_type == 1) return gemm<false, __bf16>(g, ws, stream);
+  return gemm<true, float>(g, ws, stream);
 }
 
-size_t gemm_fp8_workspace_bytes(int, int, int, int) { return 0; }
+size_t gemm_fp8_workspace_bytes(int M, int E, int N, int K) {
+  if (M == 0) return 0;
+  const Cut how = cut(M, E, N, K);
+  return how.splits > 1 ? (size_t)how.splits * part_values(M, N) * sizeof(float) : 0;
+}
 
 size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I, int type) {
   size_t total = 0;
@@ -209,9 +296,9 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.K = H;
   g.c = pl.hq;
   g.cs = pl.hs;
-  const int mt = stream_tiles(S, E);
   if (e != hipSuccess) return e;
-  if (mt) {
+  const int mean = S / E;
+  if (mean <= 16) {
     StreamArgs s{};
     s.g = g;
     s.x = x;
@@ -219,12 +306,14 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
     s.top_k = top_k;
     s.tokens = M;
     s.ks = 1;
-    e = type == 0 ? stream_gate_up<_Float16>(s, mt, stream)
-        : type == 1 ? stream_gate_up<__bf16>(s, mt, stream)
-                    : stream_gate_up<float>(s, mt, stream);
+    e = type == 0 ? stream_gate_up<_Float16>(s, stream)
+        : type == 1 ? stream_gate_up<__bf16>(s, stream)
+                    : stream_gate_up<float>(s, stream);
   } else {
     e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
-    if (e == hipSuccess) e = run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 1, stream);
+    if (e == hipSuccess)
+      e = mean <= 96 ? run_tiles<TileKernel<64, 256, 1, 4, true, true, float>>(g, 64, 1, stream)
+                     : run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 1, stream);
   }
   g.a = pl.hq;
   g.sa = pl.hs;
@@ -234,9 +323,9 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.K = I;
   g.c = pl.ys;
   if (e == hipSuccess)
-    e = type == 0 ? gemm<true, _Float16>(g, stream)
-        : type == 1 ? gemm<false, __bf16>(g, stream)
-                    : gemm<true, float>(g, stream);
+    e = type == 0 ? gemm<true, _Float16>(g, nullptr, stream)
+        : type == 1 ? gemm<false, __bf16>(g, nullptr, stream)
+                    : gemm<true, float>(g, nullptr, stream);
   if (e == hipSuccess) e = launch_moe_combine(pl.ys, type, M, top_k, H, pl.slot_row, p, y, stream);
   return e;
 }

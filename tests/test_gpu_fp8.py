@@ -258,7 +258,8 @@ def product_slack(a, sa, w, sw, kind="f32"):
 
 SIZES = [(1, 1, 16), (1, 256, 256), (2, 130, 144), (4, 512, 4096), (8, 300, 2048), (15, 129, 272), (16, 128, 128),
          (17, 64, 400), (33, 1000, 512), (64, 96, 1040), (100, 777, 528), (129, 257, 384), (200, 512, 2048),
-         (256, 384, 640), (300, 1100, 304), (513, 260, 1296), (1025, 520, 256)]
+         (256, 384, 640), (300, 1100, 304), (513, 260, 1296), (1025, 520, 256), (40, 200, 4112), (70, 1000, 8192),
+         (1600, 3400, 272), (4400, 4104, 272)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -267,6 +268,7 @@ def test_gemm(kind, M, N, K):
     rng = np.random.default_rng(M + N + K)
     (a, sa), (w, sw) = fp8_rows(rng, M, K), fp8_matrix(rng, N, K)
     c = Z.zinc_gemm_fp8(e4m3(a), dev(sa), e4m3(w), dev(sw), TYPES[kind][0])
+    assert tuple(c.shape) == (M, N)
     close(c, F.gemm(a, sa, w, sw), product_slack(a, sa, w, sw, kind), kind, f"{M}x{N}x{K}")
 
 
@@ -284,7 +286,8 @@ def test_gemm_propagates_nan_to_its_row_or_column_only():
 GROUPS = [
     ([0, 0, 0], 256, 256), ([1, 0, 0, 2], 128, 128), ([0, 5, 16, 17, 0, 1], 200, 272), ([64, 63, 65, 1], 96, 512),
     ([130, 0, 300, 7], 257, 384), ([1] * 40, 64, 144), ([3] * 300, 40, 128), ([0] * 1023 + [9], 32, 128),
-    ([700, 1, 0, 260], 300, 256), ([1100], 128, 2048), ([20] * 64, 768, 512),
+    ([700, 1, 0, 260], 300, 256), ([1100], 128, 2048), ([20] * 64, 768, 512), ([100] * 63 + [0], 1500, 272), ([300] * 20, 1300, 400),
+    ([500, 600] * 8, 5000, 144),
 ]
 
 
