@@ -630,24 +630,27 @@ class _Call:
     microseconds on the GPU where rows are few, so the common one (on the
     current stream of the current device) builds no stream object."""
 
-    __slots__ = ("device", "raw", "other")
+    __slots__ = ("first", "index", "raw", "other")
 
     def __init__(self, stream, first, *rest):
         index = first.get_device()
-        if index < 0 or any(t is not None and t.get_device() != index for t in rest):
+        for t in rest:
+            if t is not None and t.get_device() != index:
+                _on_gpu(first, *rest)
+        if index < 0:
             _on_gpu(first, *rest)
-        self.device = first.device
+        self.first, self.index = first, index
         if stream is None:
             self.other = None
-            self.raw = _torch()._C._cuda_getCurrentRawStream(index)
+            self.raw = _current_raw_stream(index)
         else:
-            self.other = _resolve_stream(stream, self.device)
+            self.other = _resolve_stream(stream, first.device)
             self.raw = self.other.cuda_stream
 
     def empty(self, shape, dtype):
         if self.other is None:
-            return _torch().empty(shape, dtype=dtype, device=self.device)
-        return _empty_on(self.other, shape, dtype=dtype, device=self.device)
+            return self.first.new_empty(shape, dtype=dtype)
+        return _empty_on(self.other, shape, dtype=dtype, device=self.first.device)
 
     def workspace(self, ws, need: int):
         """(address, bytes, the tensor that owns them) of the caller's workspace or a new one."""
@@ -658,14 +661,18 @@ class _Call:
         return ws.data_ptr(), _nbytes(ws), ws
 
     def run(self, name: str, *args) -> None:
-        torch = _torch()
-        if torch.cuda.current_device() == self.device.index:
+        cuda = _torch().cuda
+        if cuda.current_device() == self.index:
             status = getattr(lib, name)(*args, self.raw)
         else:
-            with torch.cuda.device(self.device):
+            with cuda.device(self.index):
                 status = getattr(lib, name)(*args, self.raw)
         if status:
             _check(status, name)
+
+
+def _current_raw_stream(index: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def moe_sort_workspace_size(M: int, top_k: int, n_experts: int) -> int:

@@ -29,11 +29,16 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T* __restrict__ x, lon
     const uint32_t f = scale_field(max16(m));
     const uint2 w = to_e4m3(v, inverse_scale_of(f));
     if constexpr (GATHER) {
-      for (int s = 0; s < top_k; ++s) {
-        const int o = slot_row[r * top_k + s];
-        if (o < 0 || o >= n_rows) continue;
-        if (c < C) *reinterpret_cast<uint2*>(q + (long long)o * C + c) = w;
-        if (l == 0) scales[(long long)o * nblk + b] = scale_of(f);
+      for (int s0 = 0; s0 < top_k; s0 += 8) {
+        int row[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) row[s] = s0 + s < top_k ? slot_row[r * top_k + s0 + s] : -1;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          if ((unsigned)row[s] >= (unsigned)n_rows) continue;
+          if (c < C) *reinterpret_cast<uint2*>(q + (long long)row[s] * C + c) = w;
+          if (l == 0) scales[(long long)row[s] * nblk + b] = scale_of(f);
+        }
       }
     } else {
       if (c < C) *reinterpret_cast<uint2*>(q + r * C + c) = w;
@@ -78,35 +83,6 @@ __global__ __launch_bounds__(256) void k_quant_tiles(const T* __restrict__ x, in
     if (r < R && c < C) *reinterpret_cast<uint2*>(q + (long long)r * C + c) = to_e4m3(v[j], inv);
   }
   if (threadIdx.x == 0) scales[(long long)rb * nblk + cb] = scale_of(f);
-}
-
-// SwiGLU of the experts' gate and up rows and its quantisation: h = silu(g) u in
-// fp32, one scale per row and 128 columns.  Rows from *n_valid on are left alone.
-__global__ __launch_bounds__(256) void k_swiglu_quant(const float* __restrict__ g, const float* __restrict__ u,
-                                                      long long groups, int C, int nblk,
-                                                      const int32_t* __restrict__ n_valid, uint8_t* __restrict__ q,
-                                                      float* __restrict__ scales) {
-  const int l = threadIdx.x & 15, n = *n_valid;
-  for (long long i = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); i < groups; i += (long long)gridDim.x * 16) {
-  const long long r = i / nblk;
-  if (r >= n) return;
-  const int b = (int)(i - r * nblk), c = b * 128 + l * 8;
-  float v[8] = {}, w[8] = {};
-  if (c < C) {
-    load8(g + r * C + c, v);
-    load8(u + r * C + c, w);
-  }
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = v[j] / (1.0f + expf(-v[j])) * w[j];
-    m = max(m, finite_abs_bits(v[j]));
-  }
-  const uint32_t f = scale_field(max16(m));
-  const uint2 o = to_e4m3(v, inverse_scale_of(f));
-  if (c < C) *reinterpret_cast<uint2*>(q + r * C + c) = o;
-  if (l == 0) scales[r * nblk + b] = scale_of(f);
-  }
 }
 
 // Workgroups of 16 groups of lanes; groups past 2^22 workgroups are taken in
@@ -160,15 +136,6 @@ hipError_t launch_moe_gather_fp8(const void* x, int type, int M, int top_k, int 
   if (type == 0) rows<_Float16>(x, M, C, slot_row, top_k, qb, scales, stream);
   if (type == 1) rows<__bf16>(x, M, C, slot_row, top_k, qb, scales, stream);
   if (type == 2) rows<float>(x, M, C, slot_row, top_k, qb, scales, stream);
-  return hipGetLastError();
-}
-
-hipError_t launch_swiglu_quant(const float* g, const float* u, int R, int C, const int32_t* n_valid, void* q,
-                               float* scales, hipStream_t stream) {
-  const int nblk = (C + 127) / 128;
-  const long long groups = (long long)R * nblk;
-  hipLaunchKernelGGL(k_swiglu_quant, group_grid(groups), dim3(256), 0, stream, g, u, groups, C, nblk,
-                     n_valid, static_cast<uint8_t*>(q), scales);
   return hipGetLastError();
 }
 

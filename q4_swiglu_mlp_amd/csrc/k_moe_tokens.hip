@@ -13,86 +13,44 @@ namespace {
 
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
 constexpr int kMaxE = 1024;
+constexpr int kOneBlockSlots = 4096;   // sorted by one workgroup in one launch
 constexpr int kSortMaxBlocks = 256;
 
-// Slots per workgroup: at least 4096 (a smaller sort is one workgroup and one
-// launch), and at most 256 workgroups.  A multiple of 512, so that every
-// wave's share is whole steps of 64.
+// Slots per workgroup, a multiple of 512 (whole steps of 64 a wave): up to 4096
+// slots one workgroup; else 1024, which spreads 65536 slots over 64 workgroups, or
+// what 256 workgroups need.
 int sort_tile(int S) {
+  if (S <= kOneBlockSlots) return (S + kSortThreads - 1) / kSortThreads * kSortThreads;
   const int t = (S + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  return ((t < 4096 ? 4096 : t) + kSortThreads - 1) / kSortThreads * kSortThreads;
+  return ((t < 1024 ? 1024 : t) + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 int sort_blocks(int S) { return S > 0 ? (S + sort_tile(S) - 1) / sort_tile(S) : 0; }
 
-// Per-workgroup counts of each expert's slots.
-__global__ __launch_bounds__(kSortThreads) void k_sort_hist(const int32_t* __restrict__ ids, int S, int E, int tile,
-                                                            int32_t* __restrict__ hist) {
-  __shared__ int cnt[kMaxE];
-  for (int e = threadIdx.x; e < E; e += kSortThreads) cnt[e] = 0;
-  __syncthreads();
-  const int lo = blockIdx.x * tile, hi = min(S, lo + tile);
-  for (int i = lo + threadIdx.x; i < hi; i += kSortThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+// One step of a wave: 64 slots, one a lane, in order.  Returns the slot's rank among the
+// wave's slots of its expert and counts them in cnt; the lanes with the same
+// expert are found by ballots over the bits of the id.
+__device__ __forceinline__ int rank_step(int e, bool ok, int E, int lane, int* cnt) {
+  uint64_t same = __ballot(ok);
+  for (int bit = 1; bit < E; bit <<= 1) {
+    const uint64_t m = __ballot((e & bit) != 0);
+    same &= (e & bit) ? m : ~m;
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) hist[blockIdx.x * E + e] = cnt[e];
+  const int below = __popcll(same & ((1ull << lane) - 1));
+  int rank = 0;
+  if (ok) rank = cnt[e] + below;
+  __builtin_amdgcn_wave_barrier();
+  if (ok && below == 0) cnt[e] = rank + __popcll(same);
+  __builtin_amdgcn_wave_barrier();
+  return rank;
 }
 
-// Each wave counts its contiguous share of the workgroup's slots; the counts
-// become the first row of every (wave, expert); then the wave walks its share
-// 64 slots at a time, a lane's place being its expert's next row plus the
-// number of lower lanes with the same expert (ballots over the bits of the id).
-__global__ __launch_bounds__(kSortThreads) void k_sort(const int32_t* __restrict__ ids, int S, int E, int tile,
-                                                       const int32_t* __restrict__ hist, int32_t* __restrict__ offsets,
-                                                       int32_t* __restrict__ slot_row, int32_t* __restrict__ row_slot,
-                                                       int32_t* __restrict__ dev_error) {
-  __shared__ int next[kSortWaves][kMaxE];
-  __shared__ int total[kMaxE], before[kMaxE], wsum[kSortWaves];
+// Exclusive scan over the experts of count(e), two a thread; first(e, value) receives
+// each.  Returns the sum.
+template <typename COUNT, typename FIRST>
+__device__ __forceinline__ int scan_experts(int E, int* wsum, COUNT count, FIRST first) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < E; e += kSortThreads) {
-    total[e] = 0;
-    before[e] = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) next[w][e] = 0;
-  }
-  __syncthreads();
-  const int share = tile / kSortWaves;
-  const int lo = blockIdx.x * tile + wave * share, hi = min(S, lo + share);
-  bool bad = false;
-  for (int i = lo + lane; i < hi; i += 64) {
-    const int e = ids[i];
-    if (e >= 0 && e < E)
-      atomicAdd(&next[wave][e], 1);
-    else
-      bad = true;
-  }
-  if (bad && dev_error) atomicOr(dev_error, 1);
-  // all workgroups' counts, and those of the workgroups before this one
-  if (hist) {
-    for (int j = tid; j < E * (int)gridDim.x; j += kSortThreads) {
-      const int b = j / E, e = j - b * E, c = hist[j];
-      if (c) {
-        atomicAdd(&total[e], c);
-        if (b < (int)blockIdx.x) atomicAdd(&before[e], c);
-      }
-    }
-  }
-  __syncthreads();
-  // exclusive scan over the experts, two a thread
-  int t0 = 0, t1 = 0;
-  const int e0 = 2 * tid, e1 = e0 + 1;
-  auto count = [&](int e) {
-    if (e >= E) return 0;
-    if (hist) return total[e];
-    int c = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) c += next[w][e];
-    return c;
-  };
-  t0 = count(e0);
-  t1 = count(e1);
-  int scan = t0 + t1;
+  const int e0 = 2 * tid, c0 = e0 < E ? count(e0) : 0, c1 = e0 + 1 < E ? count(e0 + 1) : 0;
+  int scan = c0 + c1;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(scan, d, 64);
@@ -100,43 +58,156 @@ __global__ __launch_bounds__(kSortThreads) void k_sort(const int32_t* __restrict
   }
   if (lane == 63) wsum[wave] = scan;
   __syncthreads();
-  int base = scan - t0 - t1, valid = 0;
+  int base = scan - c0 - c1, all = 0;
 #pragma unroll
   for (int w = 0; w < kSortWaves; ++w) {
     if (w < wave) base += wsum[w];
-    valid += wsum[w];
+    all += wsum[w];
   }
-  auto place = [&](int e, int first) {
-    if (e >= E) return;
-    if (blockIdx.x == 0) offsets[e] = first;
-    int at = first + before[e];
+  if (e0 < E) first(e0, base);
+  if (e0 + 1 < E) first(e0 + 1, base + c0);
+  return all;
+}
+
+// Up to 4096 slots: ranks stay in registers while the counts become first rows.
+__global__ __launch_bounds__(kSortThreads) void k_sort_one(const int32_t* __restrict__ ids, int S, int E, int tile,
+                                                           int32_t* __restrict__ offsets,
+                                                           int32_t* __restrict__ slot_row,
+                                                           int32_t* __restrict__ row_slot,
+                                                           int32_t* __restrict__ dev_error) {
+  constexpr int STEPS = kOneBlockSlots / kSortThreads;
+  __shared__ int cnt[kSortWaves][kMaxE];
+  __shared__ int wsum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int share = tile / kSortWaves, lo = wave * share, steps = share / 64;
+  int e[STEPS], rank[STEPS];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = next[w][e];
-      next[w][e] = at;
-      at += c;
-    }
-  };
-  place(e0, base);
-  place(e1, base + t0);
-  if (blockIdx.x == 0 && tid == 0) offsets[E] = valid;
+  for (int k = 0; k < STEPS; ++k) {
+    const int i = lo + 64 * k + lane;
+    e[k] = k < steps && i < S ? ids[i] : -1;
+  }
+  for (int j = tid; j < E; j += kSortThreads)
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) cnt[w][j] = 0;
   __syncthreads();
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    if (k >= steps) continue;
+    const bool ok = e[k] >= 0 && e[k] < E;
+    bad |= !ok && lo + 64 * k + lane < S;
+    rank[k] = rank_step(e[k], ok, E, lane, cnt[wave]);
+  }
+  if (bad && dev_error) atomicOr(dev_error, 1);
+  __syncthreads();
+  const int valid = scan_experts(
+      E, wsum,
+      [&](int j) {
+        int c = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) c += cnt[w][j];
+        return c;
+      },
+      [&](int j, int first) {
+        offsets[j] = first;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+          const int c = cnt[w][j];
+          cnt[w][j] = first;
+          first += c;
+        }
+      });
+  if (tid == 0) offsets[E] = valid;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int i = lo + 64 * k + lane;
+    if (k >= steps || i >= S) continue;
+    const bool ok = e[k] >= 0 && e[k] < E;
+    const int row = ok ? cnt[wave][e[k]] + rank[k] : -1;
+    slot_row[i] = row;
+    if (ok) row_slot[row] = i;
+  }
+  for (int r = valid + tid; r < S; r += kSortThreads) row_slot[r] = -1;
+}
+
+// More slots, first launch: each slot's rank among its wave's, kept in slot_row,
+// and the counts of the workgroup, hist[block][E], and of its waves.
+__global__ __launch_bounds__(kSortThreads) void k_sort_rank(const int32_t* __restrict__ ids, int S, int E, int tile,
+                                                            int32_t* __restrict__ hist, int32_t* __restrict__ whist,
+                                                            int32_t* __restrict__ slot_row,
+                                                            int32_t* __restrict__ dev_error) {
+  __shared__ int cnt[kSortWaves][kMaxE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int j = tid; j < E; j += kSortThreads)
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) cnt[w][j] = 0;
+  const int share = tile / kSortWaves;
+  const int lo = blockIdx.x * tile + wave * share, hi = min(S, lo + share);
+  __syncthreads();
+  bool bad = false;
   for (int i0 = lo; i0 < hi; i0 += 64) {
     const int i = i0 + lane;
     const int e = i < hi ? ids[i] : -1;
     const bool ok = e >= 0 && e < E;
-    uint64_t same = __ballot(ok);
-    for (int bit = 1; bit < E; bit <<= 1) {
-      const uint64_t m = __ballot((e & bit) != 0);
-      same &= (e & bit) ? m : ~m;
+    bad |= !ok && i < hi;
+    const int rank = rank_step(e, ok, E, lane, cnt[wave]);
+    if (i < hi) slot_row[i] = rank;
+  }
+  if (bad && dev_error) atomicOr(dev_error, 1);
+  __syncthreads();
+  for (int j = tid; j < E; j += kSortThreads) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      whist[((size_t)blockIdx.x * kSortWaves + w) * E + j] = c;   // of the waves before
+      c += cnt[w][j];
     }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    int row = -1;
-    if (ok) row = next[wave][e] + rank;
-    __builtin_amdgcn_wave_barrier();
-    if (ok && rank == 0) next[wave][e] = row + __popcll(same);
-    __builtin_amdgcn_wave_barrier();
-    if (i < hi) slot_row[i] = row;
+    hist[blockIdx.x * E + j] = c;
+  }
+}
+
+// Second launch: first rows from all workgroups' counts, then each slot's row.
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* __restrict__ ids, int S, int E, int tile,
+                                                             const int32_t* __restrict__ hist,
+                                                             const int32_t* __restrict__ whist,
+                                                             int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ slot_row,
+                                                             int32_t* __restrict__ row_slot) {
+  __shared__ int total[kMaxE], before[kMaxE], wsum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int j = tid; j < E; j += kSortThreads) total[j] = before[j] = 0;
+  __syncthreads();
+  // threads side by side take neighbouring experts, groups of them every few workgroups
+  int width = 1;
+  while (width < E && width < kSortThreads) width <<= 1;
+  const int part = tid / width, parts = kSortThreads / width, blocks = gridDim.x;
+  for (int j = tid & (width - 1); j < E; j += width) {
+    int all = 0, mine = 0;
+    for (int b = part; b < blocks; b += parts) {
+      const int c = hist[(size_t)b * E + j];
+      all += c;
+      mine += b < (int)blockIdx.x ? c : 0;
+    }
+    atomicAdd(&total[j], all);
+    atomicAdd(&before[j], mine);
+  }
+  __syncthreads();
+  const int valid = scan_experts(E, wsum, [&](int j) { return total[j]; },
+                                 [&](int j, int first) {
+                                   if (blockIdx.x == 0) offsets[j] = first;
+                                   before[j] += first;
+                                 });
+  if (blockIdx.x == 0 && tid == 0) offsets[E] = valid;
+  __syncthreads();
+  const int share = tile / kSortWaves;
+  const int lo = blockIdx.x * tile + wave * share, hi = min(S, lo + share);
+  const int32_t* wh = whist + ((size_t)blockIdx.x * kSortWaves + wave) * E;
+  for (int i = lo + lane; i < hi; i += 64) {
+    const int e = ids[i];
+    const bool ok = e >= 0 && e < E;
+    const int row = ok ? before[e] + wh[e] + slot_row[i] : -1;
+    slot_row[i] = row;
     if (ok) row_slot[row] = i;
   }
   for (int r = valid + blockIdx.x * kSortThreads + tid; r < S; r += gridDim.x * kSortThreads) row_slot[r] = -1;
@@ -154,30 +225,47 @@ __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ x, int
   if (c >= pieces) return;
   for (long long t = blockIdx.x; t < M; t += gridDim.x) {
     const uint4 v = x[t * pieces + c];
-    for (int s = 0; s < top_k; ++s) {
-      const int r = slot_row[t * top_k + s];
-      if (r >= 0 && r < n_rows) xs[(long long)r * pieces + c] = v;
+    for (int s0 = 0; s0 < top_k; s0 += 8) {
+      int row[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) row[s] = s0 + s < top_k ? slot_row[t * top_k + s0 + s] : -1;
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if ((unsigned)row[s] < (unsigned)n_rows) xs[(long long)row[s] * pieces + c] = v;
     }
   }
 }
 
-// y[t] = sum_s p[t, s] ys[slot_row[t, s]] in fp32, in the order of s.
+// y[t] = sum_s p[t, s] ys[slot_row[t, s]] in fp32, in the order of s; eight slots' rows
+// are in flight at a time.
 template <typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ ys, int H, int M, int top_k,
                                                  const int32_t* __restrict__ slot_row, const float* __restrict__ p,
                                                  T* __restrict__ y) {
+  constexpr int AHEAD = 8;
   const int c = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 8, n_rows = M * top_k;
   if (c >= H) return;
   for (long long t = blockIdx.x; t < M; t += gridDim.x) {
     float a[8] = {};
-    for (int s = 0; s < top_k; ++s) {
-      const int r = slot_row[t * top_k + s];
-      if (r < 0 || r >= n_rows) continue;
-      float v[8];
-      load8(ys + (long long)r * H + c, v);
-      const float w = WEIGHTED ? p[t * top_k + s] : 1.0f;
+    for (int s0 = 0; s0 < top_k; s0 += AHEAD) {
+      int row[AHEAD];
+      float w[AHEAD], v[AHEAD][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = WEIGHTED ? fmaf(w, v[i], a[i]) : a[i] + v[i];
+      for (int s = 0; s < AHEAD; ++s) {
+        const bool in = s0 + s < top_k;
+        row[s] = in ? slot_row[t * top_k + s0 + s] : -1;
+        w[s] = WEIGHTED && in ? p[t * top_k + s0 + s] : 1.0f;
+        if ((unsigned)row[s] >= (unsigned)n_rows) row[s] = -1;
+      }
+#pragma unroll
+      for (int s = 0; s < AHEAD; ++s)
+        if (row[s] >= 0) load8(ys + (long long)row[s] * H + c, v[s]);
+#pragma unroll
+      for (int s = 0; s < AHEAD; ++s)
+        if (row[s] >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = WEIGHTED ? fmaf(w[s], v[s][i], a[i]) : a[i] + v[s][i];
+        }
     }
     store8(y + t * H + c, a);
   }
@@ -246,19 +334,25 @@ void combine_backward(const void* dy, const void* ys, int M, int top_k, int H, c
 
 size_t moe_sort_workspace_bytes(int S, int E) {
   const int b = sort_blocks(S);
-  return b > 1 ? (size_t)b * E * sizeof(int32_t) : 0;
+  return b > 1 ? (size_t)b * (1 + kSortWaves) * E * sizeof(int32_t) : 0;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int S, int E, int32_t* offsets, int32_t* slot_row, int32_t* row_slot,
                            void* ws, int32_t* dev_error, hipStream_t stream) {
   const int b = sort_blocks(S), tile = sort_tile(S);
-  int32_t* hist = b > 1 ? static_cast<int32_t*>(ws) : nullptr;
-  if (b == 0)
+  if (b == 0) {
     hipLaunchKernelGGL(k_sort_empty, dim3(1), dim3(256), 0, stream, E, offsets);
-  if (b > 1) hipLaunchKernelGGL(k_sort_hist, dim3(b), dim3(kSortThreads), 0, stream, ids, S, E, tile, hist);
-  if (b > 0)
-    hipLaunchKernelGGL(k_sort, dim3(b), dim3(kSortThreads), 0, stream, ids, S, E, tile, hist, offsets, slot_row,
+  } else if (b == 1) {
+    hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kSortThreads), 0, stream, ids, S, E, tile, offsets, slot_row,
                        row_slot, dev_error);
+  } else {
+    int32_t* hist = static_cast<int32_t*>(ws);
+    int32_t* whist = hist + (size_t)b * E;
+    hipLaunchKernelGGL(k_sort_rank, dim3(b), dim3(kSortThreads), 0, stream, ids, S, E, tile, hist, whist, slot_row,
+                       dev_error);
+    hipLaunchKernelGGL(k_sort_place, dim3(b), dim3(kSortThreads), 0, stream, ids, S, E, tile, hist, whist, offsets,
+                       slot_row, row_slot);
+  }
   return hipGetLastError();
 }
 

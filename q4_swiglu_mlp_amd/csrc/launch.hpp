@@ -82,8 +82,6 @@ hipError_t launch_fp8_quantize(const void* x, int type, int R, int C, int block_
                                hipStream_t stream);
 hipError_t launch_moe_gather_fp8(const void* x, int type, int M, int top_k, int C, const int32_t* slot_row, void* q,
                                  float* scales, hipStream_t stream);
-hipError_t launch_swiglu_quant(const float* g, const float* u, int R, int C, const int32_t* n_valid, void* q,
-                               float* scales, hipStream_t stream);
 
 // Products of block-scaled e4m3 matrices and the FP8 expert layer (k_fp8_gemm.hip).
 // offsets: nullptr for one dense product (E = 1), else the experts' row ranges.

@@ -55,7 +55,7 @@ def activations(rng, rows, cols, kind):
 
 # ---------------------------------------------------------------- sort
 @pytest.mark.parametrize("M,k,E", [(1, 1, 1), (1, 8, 64), (7, 3, 5), (64, 1, 2), (65, 8, 64), (512, 8, 64),
-                                   (513, 8, 63), (4096, 8, 128), (1111, 17, 1024), (3, 1024, 1024), (9000, 8, 1000)])
+                                   (513, 8, 63), (4096, 8, 128), (1111, 17, 1024), (3, 1024, 1024), (9000, 8, 1000), (513, 8, 64), (40000, 7, 5)])
 def test_sort(M, k, E):
     rng = np.random.default_rng(M + k + E)
     ids = rng.integers(0, E, size=(M, k)).astype(np.int32)
