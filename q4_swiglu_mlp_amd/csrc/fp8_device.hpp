@@ -46,21 +46,32 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     v[4 + i] = b[i];
   }
 }
+// Eight consecutive values rounded to the row's type.  STREAMED: past the caches.
+template <bool STREAMED = false, typename V>
+__device__ __forceinline__ void store_vector(V* p, V v) {
+  if constexpr (STREAMED)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool STREAMED = false>
 __device__ __forceinline__ void store8(_Float16* p, const float (&v)[8]) {
   half8_t h;
 #pragma unroll
   for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
-  *reinterpret_cast<half8_t*>(p) = h;
+  store_vector<STREAMED>(reinterpret_cast<half8_t*>(p), h);
 }
+template <bool STREAMED = false>
 __device__ __forceinline__ void store8(__bf16* p, const float (&v)[8]) {
   bhalf8_t h;
 #pragma unroll
   for (int i = 0; i < 8; ++i) h[i] = (__bf16)v[i];
-  *reinterpret_cast<bhalf8_t*>(p) = h;
+  store_vector<STREAMED>(reinterpret_cast<bhalf8_t*>(p), h);
 }
+template <bool STREAMED = false>
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-  *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+  store_vector<STREAMED>(reinterpret_cast<f32x4_t*>(p), f32x4_t{v[0], v[1], v[2], v[3]});
+  store_vector<STREAMED>(reinterpret_cast<f32x4_t*>(p) + 1, f32x4_t{v[4], v[5], v[6], v[7]});
 }
 
 // |v| as its bit pattern where finite, 0 for infinities and NaN (they take no

@@ -143,7 +143,7 @@ struct StreamKernel {
         for (int r = 0; r < 4; ++r) {
           const float u = __shfl_xor(acc[i][r], 32, 64);
           const float z = acc[i][r];
-          acc[i][r] = z / (1.0f + expf(-z)) * u;
+          acc[i][r] = silu_times(z, u);
           m = max(m, finite_abs_bits(acc[i][r]));
         }
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));

@@ -132,6 +132,12 @@ __device__ __forceinline__ i32x4_t load_piece(Buffer b, int off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
 }
 
+// silu(z) u.  The reciprocal is within one unit in the last place; e^-z overflows to
+// infinity below -88, where the result is -0 times u, as the limit is.
+__device__ __forceinline__ float silu_times(float z, float u) {
+  return z * __builtin_amdgcn_rcpf(1.0f + expf(-z)) * u;
+}
+
 // The same for the whole workgroup and not written by the kernel: scalar loads.
 __device__ __forceinline__ const __attribute__((address_space(4))) float* uniform(const float* p) {
   return (const __attribute__((address_space(4))) float*)(uintptr_t)p;
@@ -153,6 +159,9 @@ struct TileKernel {
   static constexpr int COLS = DUAL ? TN / 2 : TN;   // output columns of a tile
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
+  // 16-bit outputs are stored past the caches: 8192 x 11008 x 4096 328 us against 368, whose
+  // stores push the operands' tiles out of L2.  fp32 ones may be parts of K, read again soon.
+  static constexpr bool STREAMED = sizeof(T) == 2;
   static constexpr int BAND = 8;                    // row tiles walked per column
   // workgroups a CU holds by registers: three waves a SIMD where a wave has 32 sums, else two
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
@@ -475,7 +484,7 @@ struct TileKernel {
 #pragma unroll
           for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
           if (wide) {
-            if (n < N) store8(row + n, v);
+            if (n < N) store8<STREAMED>(row + n, v);
           } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r)
@@ -495,14 +504,17 @@ struct TileKernel {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float z = acc[i][j][r];
-            acc[i][j][r] = z / (1.0f + expf(-z)) * acc[i][2 + j][r];
+            acc[i][j][r] = silu_times(z, acc[i][2 + j][r]);
             m = max(m, finite_abs_bits(acc[i][j][r]));
           }
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
         if (quad == 0) part[wn * TM + wm * (TM / WM) + i * 16 + l16] = m;
       }
-      __syncthreads();
+      // (written again a unit later, behind the barriers of its steps)
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int m = wm * (TM / WM) + i * 16 + l16;
@@ -518,7 +530,6 @@ struct TileKernel {
         *reinterpret_cast<uint2*>(row) = to_e4m3(v, inverse_scale_of(f));
         if (wn == 0 && quad == 0) g.cs[(size_t)(cu.first + m) * NB + cu.nt] = scale_of(f);
       }
-      __syncthreads();   // the maxima are read
     }
   }
 };
