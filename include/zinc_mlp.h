@@ -385,7 +385,10 @@ int zinc_fp8_quantize(const void* x, int32_t type, int32_t rows, int32_t cols, i
 /*
  * Product of FP8 matrices, c[M x N] of out_type:
  *   c[m][n] = sum_kb a_scales[m][kb] w_scales[n / 128][kb] sum_{k in block kb} a[m][k] w[n][k]
- * accumulated in fp32 and rounded once; a [M x K] activations, w [N x K] weights.
+ * accumulated in fp32 and rounded once; a [M x K] activations, w [N x K] weights.  For 16-bit
+ * outputs of more than 16 rows the FP8 matrix instructions add products in groups of
+ * eight k, cut at 2^-13 of the group's largest (about 1.5e-5 of a result, where the
+ * output's rounding is 2e-4 or 1.7e-3); fp32 outputs, and up to 16 dense rows, take exact fp16 operands.
  * zinc_moe_gemm_fp8: w holds n_experts matrices, and row r of a [rows x K] with
  * offsets[e] <= r < offsets[e + 1] takes expert e's (offsets int32 [n_experts + 1] on
  * the GPU, as zinc_moe_sort writes them; the host never reads them).  Rows outside
@@ -408,8 +411,9 @@ int zinc_moe_gemm_fp8(const void* a, const float* a_scales, const void* w, const
  * Batched experts with FP8 weights, the FP8 form of zinc_moe_q4k_experts:
  *   y[t] = sum_s p[t, s] W_down_e . hq,   hq = Q( silu(W_gate_e . xq) (*) (W_up_e . xq) ),   xq = Q(x[t])
  * with e = ids[t, s] and Q the quantiser above with one scale per row and 128
- * columns.  Gate and up rows and h are fp32 until Q; each expert's output row is
- * rounded to x's type and the weighted sum is taken in fp32.  w_gate, w_up: n_experts
+ * columns.  Gate and up rows and h are fp32 until Q, their products' sums exact to fp32
+ * rounding; the experts' output rows are fp32 up to 2^22 values (M * top_k * hidden) and
+ * rounded to x's type beyond, and the weighted sum is taken in fp32.  w_gate, w_up: n_experts
  * [inter x hidden] FP8 weight matrices, w_down: n_experts [hidden x inter].
  * x and y [M x hidden] of `type`.  Ids outside [0, n_experts) contribute nothing and set
  * *dev_error; duplicate ids each count.  Nothing is read back by the host.
@@ -430,8 +434,9 @@ int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const voi
  * correct use).  After zinc_timing_enable(capacity), every prefill, decode and
  * MoE call records a HIP event pair on its stream immediately around its main
  * kernel -- the fused unit kernel for prefill and MoE; for decode, one pair
- * around the gate/up matvec and one around the down matvec -- for up to
- * `capacity` pairs.  The events are recorded without a system-scope fence
+ * around the gate/up matvec and one around the down matvec; for an FP8 product one around
+ * its main kernel, for the FP8 experts one around the gate/up and one around the down
+ * product -- for up to `capacity` pairs.  The events are recorded without a system-scope fence
  * (hipEventDisableSystemFence), so they add no cache write-back of their own
  * to the work they bracket.  zinc_timing_collect() waits for the recorded events,
  * writes each pair's elapsed milliseconds to ms[0..*n_out) in launch order and

@@ -121,7 +121,7 @@ int zinc_moe_combine(const void* ys, int32_t type, int32_t M, int32_t top_k, int
   if (!aligned(ys, 16) || !aligned(y, 16) || !aligned(slot_row, 4) || !aligned(expert_weights, 4))
     return ZINC_ERR_ALIGN;
   return zinc::status_from_hip(
-      zinc::launch_moe_combine(ys, type, M, top_k, hidden, slot_row, expert_weights, y, begin(stream)));
+      zinc::launch_moe_combine(ys, type, type, M, top_k, hidden, slot_row, expert_weights, y, begin(stream)));
 }
 
 int zinc_moe_combine_backward(const void* dy, const void* ys, int32_t type, int32_t M, int32_t top_k, int32_t hidden,

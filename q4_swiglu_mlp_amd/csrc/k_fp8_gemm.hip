@@ -69,8 +69,10 @@ hipError_t run_tiles(GemmArgs g, int TM, int splits, hipStream_t stream) {
   const int held = kLds / bytes < KERNEL::HELD ? kLds / bytes : KERNEL::HELD;
   const long long units = (long long)g.row_tiles * g.col_tiles * splits, room = (long long)cus * held;
   const long long blocks = units < room ? units : room;
+  timing_begin(stream);
   hipLaunchKernelGGL(k_fp8_tile<KERNEL>, dim3((unsigned)((blocks + 7) / 8 * 8)), dim3(KERNEL::THREADS), bytes, stream,
                      g);
+  timing_end(stream);
   return hipGetLastError();
 }
 
@@ -90,8 +92,10 @@ hipError_t run_stream(StreamArgs s, int cols, hipStream_t stream) {
   g.col_tiles = (g.N + cols - 1) / cols;
   const hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_stream<KERNEL>), kLds);
   if (e != hipSuccess) return e;
+  timing_begin(stream);
   hipLaunchKernelGGL(k_fp8_stream<KERNEL>, dim3((unsigned)((long long)g.row_tiles * g.col_tiles)),
                      dim3(KERNEL::THREADS), bytes, stream, s);
+  timing_end(stream);
   return hipGetLastError();
 }
 
@@ -216,6 +220,18 @@ hipError_t stream_gate_up(const StreamArgs& s, hipStream_t stream) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// The type of the experts' output rows before they are combined.  In x's 16-bit type their
+// rounding is as large as the output's own (1.4 times its error); as fp32 they are
+// twice the bytes, which matters where they do not stay in the caches: 131 MB of
+// bf16 at 4001 tokens, top-8, hidden 2048.
+constexpr size_t kWideRows = 4 << 20;   // values kept as fp32
+int rows_type(size_t S, int H, int type) { return S * H <= kWideRows ? 2 : type; }
+// (not less for more rows)
+size_t rows_bytes(size_t S, int H, int type) {
+  const size_t wide = (S * H < kWideRows ? S * H : kWideRows) * 4, all = S * H * (type == 2 ? 4 : 2);
+  return wide > all ? wide : all;
+}
+
 // The expert call's workspace.
 struct ExpertsPlan {
   int32_t *offsets, *slot_row, *row_slot;
@@ -239,7 +255,7 @@ ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, siz
   p.xs = reinterpret_cast<float*>(take(S * (H / 128) * 4));
   p.hq = reinterpret_cast<uint8_t*>(take(S * I));
   p.hs = reinterpret_cast<float*>(take(S * (I / 128) * 4));
-  p.ys = take(S * H * (type == 2 ? 4 : 2));
+  p.ys = take(rows_bytes(S, H, type));
   if (total) *total = off;
   return p;
 }
@@ -322,11 +338,13 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.N = H;
   g.K = I;
   g.c = pl.ys;
-  if (e == hipSuccess)
-    e = type == 0 ? gemm<true, _Float16>(g, nullptr, stream)
-        : type == 1 ? gemm<false, __bf16>(g, nullptr, stream)
-                    : gemm<true, float>(g, nullptr, stream);
-  if (e == hipSuccess) e = launch_moe_combine(pl.ys, type, M, top_k, H, pl.slot_row, p, y, stream);
+  const int ys_type = rows_type(S, H, type);
+  if (e != hipSuccess) return e;
+  if (type == 1)
+    e = ys_type == 2 ? gemm<false, float>(g, nullptr, stream) : gemm<false, __bf16>(g, nullptr, stream);
+  else
+    e = ys_type == 2 ? gemm<true, float>(g, nullptr, stream) : gemm<true, _Float16>(g, nullptr, stream);
+  if (e == hipSuccess) e = launch_moe_combine(pl.ys, ys_type, type, M, top_k, H, pl.slot_row, p, y, stream);
   return e;
 }
 

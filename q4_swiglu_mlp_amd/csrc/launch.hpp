@@ -71,8 +71,9 @@ hipError_t launch_moe_sort(const int32_t* ids, int S, int E, int32_t* offsets, i
                            void* ws, int32_t* dev_error, hipStream_t stream);
 hipError_t launch_moe_gather(const void* x, int row_bytes, int M, int top_k, const int32_t* slot_row, void* xs,
                              hipStream_t stream);
-hipError_t launch_moe_combine(const void* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
-                              const float* p, void* y, hipStream_t stream);
+// ys_type: type, or fp32.
+hipError_t launch_moe_combine(const void* ys, int ys_type, int type, int M, int top_k, int H,
+                              const int32_t* slot_row, const float* p, void* y, hipStream_t stream);
 hipError_t launch_moe_combine_backward(const void* dy, const void* ys, int type, int M, int top_k, int H,
                                        const int32_t* slot_row, const float* p, void* dys, float* dp,
                                        hipStream_t stream);

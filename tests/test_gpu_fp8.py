@@ -259,7 +259,8 @@ def product_slack(a, sa, w, sw, kind="f32"):
 SIZES = [(1, 1, 16), (1, 256, 256), (2, 130, 144), (4, 512, 4096), (8, 300, 2048), (15, 129, 272), (16, 128, 128),
          (17, 64, 400), (33, 1000, 512), (64, 96, 1040), (100, 777, 528), (129, 257, 384), (200, 512, 2048),
          (256, 384, 640), (300, 1100, 304), (513, 260, 1296), (1025, 520, 256), (40, 200, 4112), (70, 1000, 8192),
-         (1600, 3400, 272), (4400, 4104, 272)]
+         (1600, 3400, 272), (4400, 4104, 272),
+         (4400, 4104, 48)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -272,9 +273,10 @@ def test_gemm(kind, M, N, K):
     close(c, F.gemm(a, sa, w, sw), product_slack(a, sa, w, sw, kind), kind, f"{M}x{N}x{K}")
 
 
-def test_gemm_propagates_nan_to_its_row_or_column_only():
+@pytest.mark.parametrize("M", [8, 40])
+def test_gemm_propagates_nan_to_its_row_or_column_only(M):
     rng = np.random.default_rng(12)
-    M, N, K = 40, 200, 272
+    N, K = 200, 272
     (a, sa), (w, sw) = fp8_rows(rng, M, K), fp8_matrix(rng, N, K)
     a[7, 271], w[150, 3] = 0x7F, 0xFF
     c = host(Z.zinc_gemm_fp8(e4m3(a), dev(sa), e4m3(w), dev(sw), torch.float32))
@@ -287,7 +289,7 @@ GROUPS = [
     ([0, 0, 0], 256, 256), ([1, 0, 0, 2], 128, 128), ([0, 5, 16, 17, 0, 1], 200, 272), ([64, 63, 65, 1], 96, 512),
     ([130, 0, 300, 7], 257, 384), ([1] * 40, 64, 144), ([3] * 300, 40, 128), ([0] * 1023 + [9], 32, 128),
     ([700, 1, 0, 260], 300, 256), ([1100], 128, 2048), ([20] * 64, 768, 512), ([100] * 63 + [0], 1500, 272), ([300] * 20, 1300, 400),
-    ([500, 600] * 8, 5000, 144),
+    ([500, 600] * 8, 5000, 144), ([2] * 1000, 200, 128),
 ]
 
 
@@ -334,38 +336,45 @@ def test_dense_is_one_group_and_runs_repeat():
 
 
 # ---------------------------------------------------------------- experts
-def experts_tolerance(gate, up, down, slots, shape, kind):
+def experts_tolerance(gate, up, down, slots, xc, xs, shape, kind):
     """How far y may be from the oracle's.
 
-    g and u carry the products' error; h then has a relative error of about
-    d = (error of u) / |u| + (error of g)(1 + |g|) / |g| + 2^-20 (exp, the division), taken as an absolute
-    bound dh.  An e4m3 code of h can differ only where h lies within dh of a tie: one step there (two where a
-    block's maximum lies within dh of 448 times a power of two: the other scale).  What stays equal is exact,
-    so the down product adds its own slack, the expert row its type's rounding.
+    g and u are summed exactly to fp32 rounding: eg, eu.  h then is off by at most dh = |u| 1.1 eg + |silu(g)| eu +
+    1.1 eg eu + 2^-20 |h| (|silu'| <= 1.1; exp and the reciprocal).  An e4m3 code of h can differ only where h lies
+    within dh of a tie: one step there (two where a block's maximum lies within dh of 448 times a power of two: the
+    other scale).  What stays equal is exact, so the down product adds its own slack (16-bit expert rows of a bf16
+    layer: the FP8 MFMA's too), and an expert row its type's rounding.
     """
     _, half, tiny = TYPES[kind]
     y_tol = np.zeros(shape)
-    for t, p, e, h, dh in slots:
-        wd = np.abs(F.dequantize(down[0][e], down[1][e], 128))
-        q, s = F.quantize(h[None])
-        v, sc = F.dequantize(q, s, 1)[0], F.spread(s, 1, (1, h.size))[0]
+    H = shape[1]
+    xq = F.dequantize(xc, xs, 1)
+    for e in range(gate[0].shape[0]):
+        mine = [v for v in slots if v[2] == e]
+        if not mine:
+            continue
+        t = np.array([v[0] for v in mine])
+        p = np.array([v[1] for v in mine])
+        h = np.stack([v[3] for v in mine])
+        wg, wu, wd = (F.dequantize(m[0][e], m[1][e], 128) for m in (gate, up, down))
+        g, u = xq[t] @ wg.T, xq[t] @ wu.T
+        eg, eu = ((H + 16) * 2.0 ** -23 * (np.abs(xq[t]) @ np.abs(m).T) for m in (wg, wu))
+        dh = np.abs(u) * 1.1 * eg + np.abs(F.silu(g)) * eu + 1.1 * eg * eu + 2.0 ** -20 * np.abs(h)
+        q, s = F.quantize(h)
+        v, sc = F.dequantize(q, s, 1), F.spread(s, 1, h.shape)
         step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(np.abs(h / sc), 2.0 ** -60))) - 3), 2.0 ** -9) * sc
         doubt = np.abs(np.abs(h - v) - step / 2) <= dh
-        edge = np.zeros(h.size, bool)
-        for b in range(0, h.size, 128):
-            blk, top = slice(b, b + 128), np.abs(h[b:b + 128]).argmax()
-            m, d = abs(h[b + top]), dh[b + top]
-            if not m:
-                continue
-            near = 448 * 2.0 ** np.round(np.log2(m / 448))
-            edge[blk] = abs(m - near) <= d
-        off = np.where(doubt | edge, 2 * step, 0.0)
-        size = wd @ np.abs(v)
-        row = wd @ off + (h.size + 16) * 2.0 ** -23 * size
-        if kind != "f32":
-            row = row + cut(q, s, down[0][e], down[1][e])[0]
-        row += half * (size + row) + tiny
-        y_tol[t] += p * row * (1 + 2.0 ** -20)
+        blocks = np.abs(h).reshape(h.shape[0], -1, 128)
+        top = blocks.argmax(-1)[..., None]
+        m = np.take_along_axis(blocks, top, -1)
+        near = 448 * 2.0 ** np.round(np.log2(np.maximum(m, 1e-300) / 448))
+        edge = np.abs(m - near) <= np.take_along_axis(dh.reshape(blocks.shape), top, -1)
+        doubt |= np.broadcast_to(edge & (m > 0), blocks.shape).reshape(h.shape)
+        row = (np.where(doubt, 2 * step, 0.0)) @ np.abs(wd).T + (h.shape[1] + 16) * 2.0 ** -23 * (np.abs(v) @ np.abs(wd).T)
+        if kind == "bf16":
+            row = row + cut(q, s, down[0][e], down[1][e])
+        row = row + half * (np.abs(v @ wd.T) + row) + tiny
+        np.add.at(y_tol, t, p[:, None] * row * (1 + 2.0 ** -20))
     return y_tol
 
 
@@ -382,18 +391,7 @@ def run_experts(rng, E, H, I, M, k, kind, ids=None):
     xf = host(x)
     y_ref, slots = F.experts(gate, up, down, xf, ids, p)
     xc, xs = F.quantize(xf)
-    xq = F.dequantize(xc, xs, 1)
-    full = []
-    for t_, p_, e, h in slots:
-        wg, wu = (F.dequantize(m[0][e], m[1][e], 128) for m in (gate, up))
-        g, u = wg @ xq[t_], wu @ xq[t_]
-        eg, eu = ((H + 16) * 2.0 ** -23 * (np.abs(m) @ np.abs(xq[t_])) for m in (wg, wu))
-        if kind == "bf16":                                             # gate and up by the FP8 MFMA
-            eg = eg + cut(xc[t_][None], xs[t_][None], gate[0][e], gate[1][e])[0]
-            eu = eu + cut(xc[t_][None], xs[t_][None], up[0][e], up[1][e])[0]
-        slope = np.abs(u) * 1.1                                        # |silu'| <= 1.1
-        full.append((t_, p_, e, h, slope * eg + np.abs(F.silu(g)) * eu + eg * eu * 1.1 + 2.0 ** -20 * np.abs(h)))
-    tol = experts_tolerance(gate, up, down, full, y_ref.shape, kind)
+    tol = experts_tolerance(gate, up, down, slots, xc, xs, y_ref.shape, kind)
     _, half, tiny = TYPES[kind]
     tol = tol + half * (np.abs(y_ref) + tol) + tiny + 2.0 ** -22 * np.abs(y_ref)
     err = np.abs(host(y) - y_ref)
@@ -405,7 +403,8 @@ def run_experts(rng, E, H, I, M, k, kind, ids=None):
 
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("E,H,I,M,k", [(1, 128, 128, 1, 1), (4, 256, 384, 3, 2), (8, 512, 128, 70, 2),
-                                       (6, 384, 640, 130, 3), (64, 256, 256, 33, 8)])
+                                       (6, 384, 640, 130, 3), (64, 256, 256, 33, 8), (4, 256, 256, 300, 2),
+                                       (3, 1024, 128, 2100, 2)])
 def test_experts(kind, E, H, I, M, k):
     run_experts(np.random.default_rng(E + H + I + M), E, H, I, M, k, kind)
 
@@ -466,6 +465,78 @@ def test_training_step_through_dispatch_and_combine():
     assert torch.allclose(dx.double(), x64.grad, rtol=0, atol=float(8 * 2.0 ** -24 * 3 * k * dy.abs().max()))
     bound = (H + 4) * 2.0 ** -24 * 3 * float((x.abs() * dy.abs()).sum(1).max())
     assert torch.allclose(dp.double(), p64.grad, rtol=0, atol=bound)
+
+
+# ---------------------------------------------------------------- sizes
+def test_offsets_past_32_bits_products():
+    # a past 2^32 bytes, and an expert's weight behind 2^32 bytes: the last rows against the same rows alone
+    M, N, K = 135000, 64, 32768
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    a = torch.randint(0, 0x70, (M, K), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    sa = torch.rand((M, K // 128), device=DEV, generator=g)
+    w = torch.randint(0, 0x70, (N, K), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    sw = torch.rand((1, K // 128), device=DEV, generator=g)
+    assert M * K > 1 << 32
+    c = Z.zinc_gemm_fp8(a, sa, w, sw, torch.float32)
+    tail = slice(M - 300, M)
+    x = a[tail].double() * sa[tail].double().repeat_interleave(128, 1)
+    y = w.double() * sw.double().repeat_interleave(128, 1)
+    # all terms positive: the sum is its own magnitude; fp32 sums of K terms, cut
+    assert torch.allclose(c[tail].double(), x @ y.t(), rtol=(K + 16) * 2.0 ** -23, atol=0)
+    del a, sa, c
+    E, N, K, rows = 40, 8192, 16384, 90
+    w = torch.randint(0, 0x70, (E, N, K), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    assert (E - 1) * N * K > 1 << 32
+    sw = torch.rand((E, N // 128, K // 128), device=DEV, generator=g)
+    a = torch.randint(0, 0x70, (rows, K), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    sa = torch.rand((rows, K // 128), device=DEV, generator=g)
+    off = torch.full((E + 1,), 5, dtype=torch.int32, device=DEV)
+    off[0], off[E] = 0, rows
+    c = Z.zinc_moe_gemm_fp8(a, sa, w, sw, off, torch.float32)
+    alone = Z.zinc_gemm_fp8(a[5:].contiguous(), sa[5:].contiguous(), w[E - 1], sw[E - 1], torch.float32)
+    # the same sums, cut into parts of K or not
+    assert torch.allclose(c[5:], alone, rtol=(K + 16) * 2.0 ** -22, atol=0)
+
+
+def test_offsets_past_32_bits_rows():
+    M, k, H, E = 34000, 8, 8192, 16
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    x = torch.randn((M, H), device=DEV, generator=g).bfloat16()
+    ids = torch.randint(0, E, (M, k), dtype=torch.int32, device=DEV, generator=g)
+    off, slot_row, row_slot = Z.zinc_moe_sort(ids, E)
+    xs = Z.zinc_moe_gather(x, slot_row)
+    assert xs.numel() * 2 > 1 << 32
+    at = torch.arange(0, M * k, 997, device=DEV)
+    assert torch.equal(xs[at], x[(row_slot[at] // k).long()])
+    assert torch.equal(ids.reshape(-1)[row_slot.long()], torch.sort(ids.reshape(-1)).values)
+    p = torch.full((M, k), 0.125, device=DEV)
+    y = Z.zinc_moe_combine(xs, slot_row, p)                            # eight equal rows, an eighth each: exact
+    assert torch.equal(y, x)
+    q, s = Z.zinc_fp8_quantize(xs)
+    qt, st = Z.zinc_fp8_quantize(xs[-384:].contiguous())
+    assert torch.equal(q[-384:].view(torch.uint8), qt.view(torch.uint8)) and torch.equal(s[-384:], st)
+    del q, s
+    dys, dp = Z.zinc_moe_combine_backward(x, xs, slot_row, p)
+    assert torch.equal(dys[at], 0.125 * x[(row_slot[at] // k).long()])
+    want = (x[-64:].double() ** 2).sum(1, keepdim=True).expand(64, k)
+    assert torch.allclose(dp[-64:].double(), want, rtol=(H + 1) * 2.0 ** -24, atol=0)
+
+
+def test_timing_hook_brackets_the_products():
+    rng = np.random.default_rng(22)
+    (a, sa), (w, sw) = fp8_rows(rng, 20, 256), fp8_matrix(rng, 130, 256)
+    args = e4m3(a), dev(sa), e4m3(w), dev(sw)
+    wx, x, ids, p, _ = _layer(rng, 20)
+    Z.timing_enable(8)
+    try:
+        Z.zinc_gemm_fp8(*args)
+        Z.zinc_moe_fp8_experts(*wx, x, ids, p)
+        ms = Z.timing_collect(8)
+    finally:
+        Z.timing_disable()
+    assert len(ms) == 3 and all(0 < v < 100 for v in ms)
 
 
 # ---------------------------------------------------------------- graphs, streams
