@@ -55,11 +55,14 @@ struct Frag<true> {
 __device__ __forceinline__ f32x4_t mfma_block(const Frag<false>& a, const Frag<false>& b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4_t{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4_t mfma_block(const Frag<true>& a, const Frag<true>& b) {
-  f32x4_t d = {0, 0, 0, 0};
+__device__ __forceinline__ void mfma_blocks(const Frag<true>& a0, const Frag<true>& b0, f32x4_t& d0,
+                                            const Frag<true>& a1, const Frag<true>& b1, f32x4_t& d1) {
+  d0 = d1 = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-  for (int h = 0; h < 4; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[h], b.v[h], d, 0, 0, 0);
-  return d;
+  for (int h = 0; h < 4; ++h) {
+    d0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0.v[h], b0.v[h], d0, 0, 0, 0);
+    d1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1.v[h], b1.v[h], d1, 0, 0, 0);
+  }
 }
 
 // The rows [first, first + rows) of tile `tile` (TM rows each) of the experts'
@@ -155,7 +158,10 @@ template <int TM, int TN, int WM, int WN, bool EXACT, bool DUAL, typename T>
 struct TileKernel {
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
-  static constexpr int LAG = 3;                     // tiles between an MFMA and the use of its sums
+  // Tiles whose MFMAs are issued together (the fp16 MFMAs of a tile wait for one
+  // another, so those of two take turns), and tiles between an MFMA and the use of
+  // its sums, which lie in a ring.
+  static constexpr int GROUP = EXACT ? 2 : 1, LAG = EXACT ? 2 : 3, RING = 4;
   static constexpr int COLS = DUAL ? TN / 2 : TN;   // output columns of a tile
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
@@ -358,11 +364,11 @@ struct TileKernel {
     // Tile t of a step is (i, j): all columns of one row tile after the other, but
     // the last two row tiles column by column, so that w's fragments fall free
     // for the next step's while there is work left.  A tile's block sums lie in
-    // d[t % (LAG + 1)] and are scaled and added LAG tiles later, also across steps.
+    // d[t % RING] and are scaled and added LAG tiles later, also across steps.
     constexpr int TILES = MT * NT, PAIR = (MT - 2) * NT;
-    static_assert(MT >= 4 && TILES % (LAG + 1) == 0 && 2 * NT >= LAG, "tile shape");
+    static_assert(MT >= 4 && TILES % RING == 0 && NT % 2 == 0 && 2 * NT >= LAG, "tile shape");
     constexpr int EACH = (PIECES + 2 * NT - 1) / (2 * NT);   // copies beside a tile of the last quarter
-    f32x4_t d[LAG + 1];
+    f32x4_t d[RING];
     float st[MT][DUAL ? 2 : 1];
     auto row_of = [](int t) { return t < PAIR ? t / NT : MT - 2 + ((t - PAIR) & 1); };
     auto col_of = [](int t) { return t < PAIR ? t % NT : (t - PAIR) >> 1; };
@@ -370,7 +376,7 @@ struct TileKernel {
       const int i = row_of(v), j = col_of(v);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        acc[i][j][r] = fmaf(st[i][DUAL ? j >> 1 : 0], d[v % (LAG + 1)][r], acc[i][j][r]);
+        acc[i][j][r] = fmaf(st[i][DUAL ? j >> 1 : 0], d[v % RING][r], acc[i][j][r]);
       asm volatile("" : "+v"(acc[i][j]));   // here, not behind the loop's branches
     };
 
@@ -395,7 +401,7 @@ struct TileKernel {
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i <= LAG; ++i) d[i] = f32x4_t{0, 0, 0, 0};
+      for (int i = 0; i < RING; ++i) d[i] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -412,50 +418,60 @@ struct TileKernel {
         const bool fast = whole();
         Frag<EXACT> fw[NT], fa[2];
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-          const int i = row_of(t), j = col_of(t);
-          if (t < PAIR && j == 0) {
-            fa[0].set(ar[0]);
-            if (i + 1 < MT - 2) {
-              read_a(i + 1, 0, buf);
-            } else {
-              read_a(MT - 2, 0, buf);
-              read_a(MT - 1, 1, buf);
-            }
-          }
-          if (t < NT) fw[t].set(wr[t]);
-          if (t == PAIR) {
-            fa[0].set(ar[0]);
-            fa[1].set(ar[1]);
-            // the next block has landed, and every wave has read what it needs of this one
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            if (!fast) copy_cut(buf);
-          }
-          d[t % (LAG + 1)] = mfma_block(fw[j], fa[t < PAIR ? 0 : i - (MT - 2)]);
-          if (t >= PAIR) {
-            const int v = t - PAIR;
-            if (fast) {
+        for (int t0 = 0; t0 < TILES; t0 += GROUP) {
 #pragma unroll
-              for (int c = v * EACH; c < (v + 1) * EACH; ++c)
-                if (c < PIECES) copy_piece(c, buf);
-              if (t == TILES - 1) copy_scales(buf);
-            }
-            if (v & 1) read_w(j, buf ^ 1);
-            if (t == TILES - 1) read_a(0, 0, buf ^ 1);
-          }
-          if (t < LAG) {
-            add(TILES - LAG + t);
-            if (t == LAG - 1) {
-#pragma unroll
-              for (int r = 0; r < MT; ++r) {
-                st[r][0] = sn[r] * t1;
-                if (DUAL) st[r][DUAL ? 1 : 0] = sn[r] * t2;
+          for (int t = t0; t < t0 + GROUP; ++t) {
+            const int i = row_of(t), j = col_of(t);
+            if (t < PAIR && j == 0) {
+              fa[0].set(ar[0]);
+              if (i + 1 < MT - 2) {
+                read_a(i + 1, 0, buf);
+              } else {
+                read_a(MT - 2, 0, buf);
+                read_a(MT - 1, 1, buf);
               }
             }
-          } else {
-            add(t - LAG);
+            if (t < NT) fw[t].set(wr[t]);
+            if (t == PAIR) {
+              fa[0].set(ar[0]);
+              fa[1].set(ar[1]);
+              // the next block has landed, and every wave has read what it needs of this one
+              asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+              __builtin_amdgcn_s_barrier();
+              asm volatile("" ::: "memory");
+              if (!fast) copy_cut(buf);
+            }
+          }
+          auto a_of = [&](int t) -> const Frag<EXACT>& { return fa[t < PAIR ? 0 : row_of(t) - (MT - 2)]; };
+          if constexpr (EXACT)
+            mfma_blocks(fw[col_of(t0)], a_of(t0), d[t0 % RING], fw[col_of(t0 + 1)], a_of(t0 + 1), d[(t0 + 1) % RING]);
+          else
+            d[t0 % RING] = mfma_block(fw[col_of(t0)], a_of(t0));
+#pragma unroll
+          for (int t = t0; t < t0 + GROUP; ++t) {
+            if (t >= PAIR) {
+              const int v = t - PAIR;
+              if (fast) {
+#pragma unroll
+                for (int c = v * EACH; c < (v + 1) * EACH; ++c)
+                  if (c < PIECES) copy_piece(c, buf);
+                if (t == TILES - 1) copy_scales(buf);
+              }
+              if (v & 1) read_w(col_of(t), buf ^ 1);
+              if (t == TILES - 1) read_a(0, 0, buf ^ 1);
+            }
+            if (t < LAG) {
+              add(TILES - LAG + t);
+              if (t == LAG - 1) {
+#pragma unroll
+                for (int r = 0; r < MT; ++r) {
+                  st[r][0] = sn[r] * t1;
+                  if (DUAL) st[r][DUAL ? 1 : 0] = sn[r] * t2;
+                }
+              }
+            } else {
+              add(t - LAG);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
