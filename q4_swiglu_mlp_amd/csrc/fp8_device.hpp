@@ -74,12 +74,21 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   store_vector<STREAMED>(reinterpret_cast<f32x4_t*>(p) + 1, f32x4_t{v[4], v[5], v[6], v[7]});
 }
 
-// |v| as its bit pattern where finite, 0 for infinities and NaN (they take no
-// part in a block's maximum; patterns of non-negative floats order as the
-// floats do).
-__device__ __forceinline__ uint32_t finite_abs_bits(float v) {
-  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
-  return b < 0x7F800000u ? b : 0u;
+// The largest |v| of eight values as its bit pattern (patterns of non-negative
+// floats order as the floats do), infinities and NaN left out.  They are looked
+// for once, over the wave, and `whole` says that it holds none.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t max_finite(const float (&v)[8], bool& whole) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  whole = !__any(m >= 0x7F800000u);
+  if (!whole) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]) < 0x7F800000u ? abs_bits(v[i]) : 0u);
+  }
+  return m;
 }
 
 // The scale of a block whose largest finite |x| has the bits `amax`: the
@@ -95,12 +104,14 @@ __device__ __forceinline__ float scale_of(uint32_t field) { return __uint_as_flo
 __device__ __forceinline__ float inverse_scale_of(uint32_t field) { return __uint_as_float((254u - field) << 23); }
 
 // Eight values times `inv` as e4m3 bytes.  Infinities become NaN (e4m3 has none).
-__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float inv) {
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float inv, bool whole) {
   float s[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s[i] = v[i] * inv;
-    if (__builtin_isinf(v[i])) s[i] = __builtin_nanf("");
+  for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (__builtin_isinf(v[i])) s[i] = __builtin_nanf("");
   }
   uint2 q;
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);

@@ -136,16 +136,16 @@ struct StreamKernel {
       __syncthreads();
       uint32_t* part = reinterpret_cast<uint32_t*>(smem);   // [NW][TM]
       // quads 0 and 1 hold gate's columns, 2 and 3 up's of the same rows
+      float h[MT][8] = {};
+      bool whole[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        uint32_t m = 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float u = __shfl_xor(acc[i][r], 32, 64);
-          const float z = acc[i][r];
-          acc[i][r] = silu_times(z, u);
-          m = max(m, finite_abs_bits(acc[i][r]));
+          h[i][r] = silu_times(acc[i][r], u);
         }
+        uint32_t m = max_finite(h[i], whole[i]);
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
         if (quad == 0) part[wave * TM + 16 * i + l16] = m;
       }
@@ -159,9 +159,8 @@ struct StreamKernel {
         const uint32_t f = scale_field(top);
         const float inv = inverse_scale_of(f);
         if (m < rows && quad < 2) {
-          const float v[8] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3], 0, 0, 0, 0};
           *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.c) + (size_t)(rt.first + m) * N + n0 + 4 * quad) =
-              to_e4m3(v, inv).x;
+              to_e4m3(h[i], inv, whole[i]).x;
           if (wave == 0 && quad == 0) g.cs[(size_t)(rt.first + m) * NB + nt] = scale_of(f);
         }
       }
@@ -224,11 +223,9 @@ struct StreamKernel {
         const int k = (c0 + b) * 128 + l * 8;
         float v[8] = {};
         if (k < K) load8(static_cast<const T_IN*>(s.x) + (size_t)tok * K + k, v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, finite_abs_bits(v[e]));
-        const uint32_t f = scale_field(max16(top));
-        const uint2 q = to_e4m3(v, inverse_scale_of(f));
+        bool whole;
+        const uint32_t f = scale_field(max16(max_finite(v, whole)));
+        const uint2 q = to_e4m3(v, inverse_scale_of(f), whole);
         *reinterpret_cast<uint2*>(ta + ((size_t)b * s.rows + m) * 128 + (((l >> 1) ^ (m & 7)) << 4) + (l & 1) * 8) = q;
         if (l == 0) tsa[b * s.rows + m] = scale_of(f);
       }

@@ -135,10 +135,16 @@ __device__ __forceinline__ i32x4_t load_piece(Buffer b, int off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
 }
 
-// silu(z) u.  The reciprocal is within one unit in the last place; e^-z overflows to
-// infinity below -88, where the result is -0 times u, as the limit is.
+// silu(z) u = z u / (1 + e^-z).  e^-z as 2^t (1 + r ln 2) with t = -z log2(e) rounded and r what
+// the rounding left, log2(e) in two parts: within a few units in the last place.
+// t stops at 127, where the quotient is below 2^-126; the reciprocal is within one unit.
 __device__ __forceinline__ float silu_times(float z, float u) {
-  return z * __builtin_amdgcn_rcpf(1.0f + expf(-z)) * u;
+  constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float t = z * kHi;
+  const float r = fmaf(z, kLo, fmaf(z, kHi, -t));
+  const float e2 = __builtin_amdgcn_exp2f(fminf(t, 127.0f));
+  const float e = fmaf(e2, r * kLn2, e2);
+  return z * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // The same for the whole workgroup and not written by the kernel: scalar loads.
@@ -512,17 +518,13 @@ struct TileKernel {
       // h = silu(gate) up; a row's maximum over the 128 columns: in the lane, over
       // the four lanes of the row, over the WN waves
       uint32_t* part = sm.part;
+      float h[MT][8];
+      bool whole[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float z = acc[i][j][r];
-            acc[i][j][r] = silu_times(z, acc[i][2 + j][r]);
-            m = max(m, finite_abs_bits(acc[i][j][r]));
-          }
+        for (int r = 0; r < 8; ++r) h[i][r] = silu_times(acc[i][r >> 2][r & 3], acc[i][2 + (r >> 2)][r & 3]);
+        uint32_t m = max_finite(h[i], whole[i]);
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
         if (quad == 0) part[wn * TM + wm * (TM / WM) + i * 16 + l16] = m;
@@ -540,10 +542,7 @@ struct TileKernel {
         const uint32_t f = scale_field(top);
         if (m >= cu.rows) continue;
         uint8_t* row = static_cast<uint8_t*>(g.c) + (size_t)(cu.first + m) * N + n0 + wn * 32 + 8 * quad;
-        float v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = acc[i][r >> 2][r & 3];
-        *reinterpret_cast<uint2*>(row) = to_e4m3(v, inverse_scale_of(f));
+        *reinterpret_cast<uint2*>(row) = to_e4m3(h[i], inverse_scale_of(f), whole[i]);
         if (wn == 0 && quad == 0) g.cs[(size_t)(cu.first + m) * NB + cu.nt] = scale_of(f);
       }
     }

@@ -23,11 +23,9 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T* __restrict__ x, lon
     const int c = b * 128 + l * 8;
     float v[8] = {};
     if (c < C) load8(x + r * C + c, v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
-    const uint32_t f = scale_field(max16(m));
-    const uint2 w = to_e4m3(v, inverse_scale_of(f));
+    bool whole;
+    const uint32_t f = scale_field(max16(max_finite(v, whole)));
+    const uint2 w = to_e4m3(v, inverse_scale_of(f), whole);
     if constexpr (GATHER) {
       for (int s0 = 0; s0 < top_k; s0 += 8) {
         int row[8];
@@ -47,18 +45,18 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T* __restrict__ x, lon
   }
 }
 
-// One workgroup per 128 x 128 tile (row blocks past 2^20 in turn); a thread holds
-// eight columns of eight rows.
+// One workgroup per 128 x 128 tile, neighbours along a row block (tiles past 2^22 in
+// turn); a thread holds eight columns of eight rows.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quant_tiles(const T* __restrict__ x, int R, int C, int nblk,
                                                      uint8_t* __restrict__ q, float* __restrict__ scales) {
   __shared__ uint32_t part[4];
-  const int cb = blockIdx.y, rblk = (int)(((long long)R + 127) / 128);
-  const int c = cb * 128 + (int)(threadIdx.x & 15) * 8;
-  for (int rb = blockIdx.x; rb < rblk; rb += gridDim.x) {
-    const long long r0 = (long long)rb * 128 + (threadIdx.x >> 4);
+  const long long tiles = ((long long)R + 127) / 128 * nblk;
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const long long rb = tile / nblk;
+    const int c = (int)(tile - rb * nblk) * 128 + (int)(threadIdx.x & 15) * 8;
+    const long long r0 = rb * 128 + (threadIdx.x >> 4);
     float v[8][8];
-    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const long long r = r0 + 16 * j;
@@ -69,24 +67,24 @@ __global__ __launch_bounds__(256) void k_quant_tiles(const T* __restrict__ x, in
         for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
       }
     }
+    uint32_t m = 0;
+    bool whole[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[j][i]));
+    for (int j = 0; j < 8; ++j) m = max(m, max_finite(v[j], whole[j]));
     m = max16(m);
     m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
     const uint32_t f = scale_field(max(max(part[0], part[1]), max(part[2], part[3])));
-    __syncthreads();
     const float inv = inverse_scale_of(f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const long long r = r0 + 16 * j;
-      if (r < R && c < C) *reinterpret_cast<uint2*>(q + r * C + c) = to_e4m3(v[j], inv);
+      if (r < R && c < C) *reinterpret_cast<uint2*>(q + r * C + c) = to_e4m3(v[j], inv, whole[j]);
     }
-    if (threadIdx.x == 0) scales[(long long)rb * nblk + cb] = scale_of(f);
+    if (threadIdx.x == 0) scales[tile] = scale_of(f);
+    if (tile + gridDim.x < tiles) __syncthreads();   // part is read before it is written again
   }
 }
 
@@ -113,8 +111,9 @@ void rows(const void* x, int R, int C, const int32_t* slot_row, int top_k, uint8
 
 template <typename T>
 void tiles(const void* x, int R, int C, uint8_t* q, float* scales, hipStream_t stream) {
-  const int nblk = (C + 127) / 128, rblk = (int)(((long long)R + 127) / 128);
-  hipLaunchKernelGGL(k_quant_tiles<T>, dim3((unsigned)(rblk < (1 << 20) ? rblk : (1 << 20)), (unsigned)nblk), dim3(256), 0, stream,
+  const int nblk = (C + 127) / 128;
+  const long long n = ((long long)R + 127) / 128 * nblk;
+  hipLaunchKernelGGL(k_quant_tiles<T>, dim3((unsigned)(n < (1 << 22) ? n : (1 << 22))), dim3(256), 0, stream,
                      static_cast<const T*>(x), R, C, nblk, q, scales);
 }
 
