@@ -117,6 +117,7 @@ struct GemmArgs {
   int row_tiles, col_tiles;   // an upper bound of the row tiles, where experts are grouped
   int splits;           // parts of K, each with its own output,
   size_t part;          // this many values after the one before
+  bool read_soon;       // the output is read by the next launch: kept in the caches
   void* c;
   float* cs;            // scales of a quantised output
 };
@@ -505,8 +506,10 @@ struct TileKernel {
           float v[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
-          if (wide) {
+          if (wide && STREAMED && !g.read_soon) {
             if (n < N) store8<STREAMED>(row + n, v);
+          } else if (wide) {
+            if (n < N) store8(row + n, v);
           } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r)

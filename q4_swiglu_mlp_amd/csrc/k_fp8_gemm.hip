@@ -338,6 +338,7 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.N = H;
   g.K = I;
   g.c = pl.ys;
+  g.read_soon = true;
   const int ys_type = rows_type(S, H, type);
   if (e != hipSuccess) return e;
   if (type == 1)
