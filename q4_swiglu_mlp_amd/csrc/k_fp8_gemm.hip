@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ pa
   }
 }
 
-// How a product is cut, by its sizes alone.  Times: us, 256 CUs, bf16 output.
+// How a product is cut, by its sizes alone.  Times: us, 256 CUs, bf16 output, calls replayed.
 enum Shape { kStream, kSmall, kMiddle, kLarge, kLargest };
 struct Cut {
   Shape shape;
@@ -137,34 +137,38 @@ struct Cut {
 };
 
 // Dense.
-// - Up to 16 rows the weight's stream: 1 x 11008 x 4096 11.8 against 15 for small
-//   tiles in four parts of K with their join.
+// - Up to 4 rows the weight's stream: 11008 x 4096 12.1 against 12.8 for the best parts of
+//   small tiles, 4096 x 11008 14.7 and 15.2, 4096 x 4096 7.8 and 9.9; with 8 rows 13.3
+//   and 12.9, 18.2 and 15.3, 9.3 and 10.1; with 16 rows 16.1 and 13.2, 24 and 15.6.
 // - Else the largest tile (256 x 256, 128 x 256) with 160 units, five eighths of the CUs:
-//   1024 x 11008 x 4096 66 with the first (172 units) against 81 with small tiles, 512 rows
-//   43 with the second against 45 and 63, 2048 x 4096 x 11008 (128 and 256 units) 119 with
-//   the second against 163 with the first.
-// - Else small tiles (64 x 128), and where they are no more than the CUs, parts of K
-//   of eight blocks or more, up to 400 units: 64 x 11008 x 4096 17 in four parts against
-//   30 in one, 64 x 4096 x 11008 15 in eight against 58; their join costs 3 and more.
+//   1024 x 11008 x 4096 53 with the first (172 units) against 74 with small tiles, 512 rows
+//   35 with the second against 49 and 39, 2048 x 4096 x 11008 (128 and 256 units) 95 with
+//   the second against 121 with the first.
+// - Else small tiles (64 x 128), in parts of K that make one and a half units a CU, eight at
+//   most, of five blocks or more: 64 x 11008 x 4096 16.2 in four parts, 17.1 in three
+//   or five, 22 in one; 64 x 4096 x 11008 17.4 in eight, 18.2 in six, 20.3 in twelve, 52 in
+//   one; 64 x 4096 x 4096 13.3 in six, 13.2 in four, 14.6 in eight.
 Cut cut_dense(int M, int N, int K) {
-  if (M <= 16) return {kStream, 1};
+  if (M <= 4) return {kStream, 1};
   const long long rows256 = (M + 255) / 256, cols256 = (N + 255) / 256, rows128 = (M + 127) / 128;
   if (rows256 * cols256 >= 160) return {kLargest, 1};
   if (rows128 * cols256 >= 160) return {kLarge, 1};
   const long long units = (long long)((M + 63) / 64) * ((N + 127) / 128);
   const int KB = (K + 127) / 128;
-  int splits = units <= 256 ? (int)((400 + units - 1) / units) : 1;
-  if (splits > KB / 8) splits = KB / 8 < 1 ? 1 : KB / 8;
+  int splits = (int)((380 + units / 2) / units);
+  splits = splits > 8 ? 8 : splits;
+  splits = splits > KB / 5 ? KB / 5 : splits;
+  splits = splits < 1 ? 1 : splits;
   const int each = (KB + splits - 1) / splits;
   return {kSmall, (KB + each - 1) / each};   // no part is empty
 }
 
-// Grouped, by the mean rows of an expert (64 experts, 768 x 2048): 128 rows 41 with
-// small tiles, 43 with 128 x 128, 42 with 256 x 256; 256 rows 63, 55 and 69; 512
-// rows 97, 91 and 82.
+// Grouped, by the mean rows of an expert (64 experts, 768 x 2048): 128 rows 43 with
+// small tiles, 46 with 128 x 128, 44 with 256 x 256; 192 rows 54, 52 and 66; 256 rows 61, 56
+// and 70; 384 rows 85, 80 and 76; 1024 rows 190, 164 and 142.
 Cut cut_grouped(int rows, int E) {
   const int mean = rows / E;
-  return {mean <= 128 ? kSmall : mean <= 384 ? kMiddle : kLargest, 1};
+  return {mean <= 160 ? kSmall : mean <= 320 ? kMiddle : kLargest, 1};
 }
 
 Cut cut(int M, int E, int N, int K) { return E ? cut_grouped(M, E) : cut_dense(M, N, K); }
@@ -313,8 +317,14 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.c = pl.hq;
   g.cs = pl.hs;
   if (e != hipSuccess) return e;
+  // The gate and up products, by the mean rows of an expert (64 experts, top-8, 2048 to
+  // 768, ids at random; us of the whole call).  While no expert has more than 16 rows the
+  // weights stream past tokens that are quantised on the way: mean 8 84 against 96 with tiles
+  // of 64 rows, 13 93 against 100, 14 101 against 100.  Tiles of 64 rows where they
+  // hold any expert: mean 16 101 against 112 with tiles of 128 rows, 42 109 against 121,
+  // 44 123 each, 64 135 against 129.
   const int mean = S / E;
-  if (mean <= 16) {
+  if (mean <= 13) {
     StreamArgs s{};
     s.g = g;
     s.x = x;
@@ -328,7 +338,7 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   } else {
     e = launch_moe_gather_fp8(x, type, M, top_k, H, pl.slot_row, pl.xq, pl.xs, stream);
     if (e == hipSuccess)
-      e = mean <= 96 ? run_tiles<TileKernel<64, 256, 1, 4, true, true, float>>(g, 64, 1, stream)
+      e = mean <= 43 ? run_tiles<TileKernel<64, 256, 1, 4, true, true, float>>(g, 64, 1, stream)
                      : run_tiles<TileKernel<128, 256, 2, 4, true, true, float>>(g, 128, 1, stream);
   }
   g.a = pl.hq;
