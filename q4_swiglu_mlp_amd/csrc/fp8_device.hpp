@@ -16,17 +16,6 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bhalf8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// Element types of activations: the ZINC_F16 / ZINC_BF16 / ZINC_F32 codes.
-struct F16 {
-  using T = _Float16;
-};
-struct BF16 {
-  using T = __bf16;
-};
-struct F32 {
-  using T = float;
-};
-
 // Eight consecutive values, 16-byte aligned, as fp32.
 __device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
   const half8_t h = *reinterpret_cast<const half8_t*>(p);

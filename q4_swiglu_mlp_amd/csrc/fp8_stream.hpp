@@ -1,5 +1,5 @@
 // The weight-streaming kernel of the block-scaled FP8 products for few rows:
-// up to 16 MT rows of a against 16 rows of w a wave.  The work is the one pass
+// up to 16 rows of a against 16 rows of w a wave.  The work is the one pass
 // over w; everything else is arranged around keeping its loads in flight.
 //
 // - A wave copies its 16 rows x 128 k (2 KB) straight to its own LDS ring, DEPTH
@@ -19,8 +19,8 @@
 namespace zinc {
 
 struct StreamArgs {
-  GemmArgs g;               // g.a / g.sa: e4m3 rows and scales (SRC 0)
-  const void* x;            // SRC 1: rows of type T_IN, row r being x[row_slot[r] / top_k]
+  GemmArgs g;               // g.a / g.sa: e4m3 rows and scales
+  const void* x;            // DUAL in their place: rows of type T_IN, row r being x[row_slot[r] / top_k]
   const int32_t* row_slot;
   int top_k, tokens;
   int ks;                   // waves per 16 rows of w
@@ -28,9 +28,11 @@ struct StreamArgs {
   int rows;                 // rows of a held in LDS
 };
 
-template <int MT, int NW, int DEPTH, int SRC, bool DUAL, typename T_IN, typename T>
+// DUAL: the experts' gate and up products of token rows, quantised on the way in, and
+// silu(gate) up quantised on the way out; else a dense product.
+template <int NW, int DEPTH, bool DUAL, typename T_IN, typename T>
 struct StreamKernel {
-  static constexpr int TM = 16 * MT, WAVES = NW, THREADS = 64 * NW;
+  static constexpr int TM = 16, THREADS = 64 * NW;
   static constexpr int RING = DEPTH * 2048;   // bytes a wave
   static_assert(!DUAL || NW == 16, "a quantised output block is 16 waves of 8 columns");
 
@@ -49,7 +51,8 @@ struct StreamKernel {
     if (rt.rows <= 0) return;
     const int K = g.K, N = g.N, KB = (K + 127) / 128, NB = (N + 127) / 128;
     const int ks = s.ks, slice = wave % ks, tile = wave / ks;
-    // the wave's columns: 16 from n0, or 8 of gate's and the same 8 of up's
+    // the wave's columns: 16 from n0, or 8 of gate's and the same 8 of up's (whose waves do
+    // not share columns: ks is 1)
     const int n0 = DUAL ? nt * 128 + wave * 8 : (nt * (NW / ks) + tile) * 16;
     const int cols = max(0, min(DUAL ? 8 : 16, N - n0));   // 0: past the last column
     const size_t w_at = ((size_t)rt.expert * N + (cols ? n0 : 0)) * K;
@@ -73,8 +76,7 @@ struct StreamKernel {
 #pragma unroll
     for (int j = 0; j < DEPTH; ++j) issue(j);
 
-    f32x4_t acc[MT] = {};
-    const int rows = rt.rows;
+    f32x4_t acc = {0, 0, 0, 0};
     int j = 0;
     for (int c0 = 0; c0 < KB; c0 += s.chunk) {
       const int nb = min(s.chunk, KB - c0);
@@ -113,21 +115,18 @@ struct StreamKernel {
         }
         // a lane holds columns 4 quad .. + 3 of the 16: up's from 8 on
         const float t = tsw[(wave * 2 + (quad >> 1)) * s.chunk + b];
+        const int m = min(l16, s.rows - 1);
+        const uint8_t* row = ta + ((size_t)b * s.rows + m) * 128;
+        f32x4_t d = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int m = min(16 * i + l16, s.rows - 1);
-          const uint8_t* row = ta + ((size_t)b * s.rows + m) * 128;
-          f32x4_t d = {0, 0, 0, 0};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const i32x4_t p = *reinterpret_cast<const i32x4_t*>(row + (((quad + 4 * h) ^ (m & 7)) << 4));
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], e4m3_to_f16(p[0], p[1]), d, 0, 0, 0);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], e4m3_to_f16(p[2], p[3]), d, 0, 0, 0);
-          }
-          const float st = t * tsa[b * s.rows + m];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(st, d[r], acc[i][r]);
+        for (int h = 0; h < 2; ++h) {
+          const i32x4_t p = *reinterpret_cast<const i32x4_t*>(row + (((quad + 4 * h) ^ (m & 7)) << 4));
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], e4m3_to_f16(p[0], p[1]), d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], e4m3_to_f16(p[2], p[3]), d, 0, 0, 0);
         }
+        const float st = t * tsa[b * s.rows + m];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(st, d[r], acc[r]);
       }
     }
 
@@ -136,64 +135,45 @@ struct StreamKernel {
       __syncthreads();
       uint32_t* part = reinterpret_cast<uint32_t*>(smem);   // [NW][TM]
       // quads 0 and 1 hold gate's columns, 2 and 3 up's of the same rows
-      float h[MT][8] = {};
-      bool whole[MT];
+      float h[8] = {};
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float u = __shfl_xor(acc[i][r], 32, 64);
-          h[i][r] = silu_times(acc[i][r], u);
-        }
-        uint32_t m = max_finite(h[i], whole[i]);
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-        if (quad == 0) part[wave * TM + 16 * i + l16] = m;
-      }
+      for (int r = 0; r < 4; ++r) h[r] = silu_times(acc[r], __shfl_xor(acc[r], 32, 64));
+      bool whole;
+      uint32_t top = max_finite(h, whole);
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      if (quad == 0) part[wave * TM + l16] = top;
       __syncthreads();
+      top = 0;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = 16 * i + l16;
-        uint32_t top = 0;
-#pragma unroll
-        for (int v = 0; v < NW; ++v) top = max(top, part[v * TM + m]);
-        const uint32_t f = scale_field(top);
-        const float inv = inverse_scale_of(f);
-        if (m < rows && quad < 2) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.c) + (size_t)(rt.first + m) * N + n0 + 4 * quad) =
-              to_e4m3(h[i], inv, whole[i]).x;
-          if (wave == 0 && quad == 0) g.cs[(size_t)(rt.first + m) * NB + nt] = scale_of(f);
-        }
+      for (int v = 0; v < NW; ++v) top = max(top, part[v * TM + l16]);
+      const uint32_t f = scale_field(top);
+      if (l16 < rt.rows && quad < 2) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(g.c) + (size_t)(rt.first + l16) * N + n0 + 4 * quad) =
+            to_e4m3(h, inverse_scale_of(f), whole).x;
+        if (wave == 0 && quad == 0) g.cs[(size_t)(rt.first + l16) * NB + nt] = scale_of(f);
       }
     } else {
       if (ks > 1) {
         __syncthreads();
-        f32x4_t* part = reinterpret_cast<f32x4_t*>(smem);   // [NW][MT][64]
-#pragma unroll
-        for (int i = 0; i < MT; ++i) part[(wave * MT + i) * 64 + lane] = acc[i];
+        f32x4_t* part = reinterpret_cast<f32x4_t*>(smem);   // [NW][64]
+        part[wave * 64 + lane] = acc;
         __syncthreads();
         if (slice) return;
-        for (int v = 1; v < ks; ++v)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i] += part[((wave + v) * MT + i) * 64 + lane];
+        for (int v = 1; v < ks; ++v) acc += part[(wave + v) * 64 + lane];
       }
-      T* c = static_cast<T*>(g.c);
+      if (l16 >= rt.rows) return;
       const int n = n0 + 4 * quad;
+      T* row = static_cast<T*>(g.c) + (size_t)(rt.first + l16) * N;
+      if (N % 4 == 0) {
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        T4 o;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = 16 * i + l16;
-        if (m >= rows) continue;
-        T* row = c + (size_t)(rt.first + m) * N;
-        if (N % 4 == 0) {
-          typedef T T4 __attribute__((ext_vector_type(4)));
-          T4 o;
+        for (int r = 0; r < 4; ++r) o[r] = (T)acc[r];
+        if (n < N) *reinterpret_cast<T4*>(row + n) = o;
+      } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = (T)acc[i][r];
-          if (n < N) *reinterpret_cast<T4*>(row + n) = o;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < N) row[n + r] = (T)acc[i][r];
-        }
+        for (int r = 0; r < 4; ++r)
+          if (n + r < N) row[n + r] = (T)acc[r];
       }
     }
   }
@@ -204,7 +184,7 @@ struct StreamKernel {
                                                 float* tsa) {
     const GemmArgs& g = s.g;
     const int K = g.K, KB = (K + 127) / 128;
-    if constexpr (SRC == 0) {
+    if constexpr (!DUAL) {
       for (int i = threadIdx.x; i < nb * rt.rows * 8; i += THREADS) {
         const int p = i & 7, b = (i >> 3) % nb, m = (i >> 3) / nb;
         const int k = (c0 + b) * 128 + p * 16;

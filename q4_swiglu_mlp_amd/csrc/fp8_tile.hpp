@@ -10,8 +10,9 @@
 // one of two buffers while the waves multiply from the other; one barrier a
 // step.  An LDS row is 128 bytes, its eight 16-byte pieces stored in the order
 // piece ^ ((row >> 1) & 7) (w's: piece ^ w_turn(row)), so that the lanes of a read,
-// which run over rows, spread over all 64 banks (two rows fill them).  Which k a lane's piece holds is free as long as both
-// operands agree: lane quarter q takes pieces q and q + 4.
+// which run over rows, spread over all 64 banks (two rows fill them).  Which k a
+// lane's piece holds is free as long as both operands agree: lane quarter q takes
+// pieces q and q + 4.
 #pragma once
 
 #include "fp8_device.hpp"
@@ -20,7 +21,6 @@ namespace zinc {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 
 // Eight e4m3 bytes as fp16, exactly.
@@ -303,7 +303,8 @@ struct TileKernel {
       const int r = i * WAVES * 8;   // the instruction's first row, less the wave's
       const int in = r < TM ? r : (r - TM) % COLS;
       to_lds(r < TM ? ra : r < TM + COLS ? rw1 : rw2,
-             v0 + in * K + (ld.kb0 + lk) * 128 + 16 * (r < TM ? a_piece : w_piece), sm.tile[buf] + (i * WAVES + wave) * 1024);
+             v0 + in * K + (ld.kb0 + lk) * 128 + 16 * (r < TM ? a_piece : w_piece),
+             sm.tile[buf] + (i * WAVES + wave) * 1024);
     };
     auto copy_scales = [&](int buf) {
       if (wave * 64 < TM)
@@ -318,7 +319,8 @@ struct TileKernel {
         const int r = i * WAVES * 8, kb = ld.kb0 + lk;
         const int in = r < TM ? r : (r - TM) % COLS, piece = r < TM ? a_piece : w_piece;
         const bool is_in = kb * 128 + piece * 16 < K;
-        const i32x4_t v = load_piece(r < TM ? ra : r < TM + COLS ? rw1 : rw2, is_in ? v0 + in * K + kb * 128 + piece * 16 : 0);
+        const i32x4_t v = load_piece(r < TM ? ra : r < TM + COLS ? rw1 : rw2,
+                                     is_in ? v0 + in * K + kb * 128 + piece * 16 : 0);
         *reinterpret_cast<i32x4_t*>(sm.tile[buf] + (i * WAVES + wave) * 1024 + lane * 16) =
             is_in ? v : i32x4_t{0, 0, 0, 0};
       }
@@ -391,7 +393,7 @@ struct TileKernel {
     const bool two = whole();   // the second block's copies may be in flight behind the first's
     copy_all(1);
     if (two)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PIECES) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PIECES) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();

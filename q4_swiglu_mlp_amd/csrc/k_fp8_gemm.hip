@@ -14,10 +14,17 @@
 // it; the groups then add in fp32.  Products have eight bits, so only those
 // below 2^-6 of a group's largest lose any: measured 1.5e-5 of the result
 // (2-norm, normal data, K = 128), far below the rounding of a 16-bit output (2e-4
-// fp16, 1.7e-3 bf16).  fp32 outputs, and the products that feed an fp16 expert
-// layer's second quantisation (where 1.5e-5 moves a value in 5000 to the next
-// code, 1.2e-3 of y), take the fp16 MFMA on exactly converted operands instead:
-// half the rate, 7e-9 of the result.
+// fp16, 1.7e-3 bf16).  fp32 outputs (an expert layer's fp16 rows too) and the
+// products that feed an expert layer's second quantisation take the fp16 MFMA on exactly
+// converted operands instead: half the rate, 7e-9 of the result.  In that quantisation
+// 1.5e-5 moves a value in 5000 to the next code, which is 1.2e-3 of y beside the
+// 2e-4 and 1.7e-3 of its own rounding (measured for bf16: 3.3e-3 in all against 1.7e-3).
+//
+// What bounds it (TB/s and TFLOP/s of the whole call):
+// - few rows, the pass over w: 1 x 11008 x 4096 11 us, 4.1 TB/s;
+// - many rows, the matrix units at the clock that the power limit leaves (about 1.9 GHz):
+//   8192 x 11008 x 4096 bf16 331 us, 2230 TFLOP/s; fp32 by fp16 MFMAs 446 us for
+//   8192 x 8192 x 4096, 1230 TFLOP/s.
 #include <atomic>
 
 #include "fp8_stream.hpp"
@@ -99,23 +106,15 @@ hipError_t run_stream(StreamArgs s, int cols, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// c = sum of the parts of K in their order; rows outside the experts' ranges are
-// left alone.
+// c = the sum of the parts of K, in their order.  A thread takes four values; bound by
+// launch and HBM or L2: 3 us for eight parts of 64 x 4096.
 template <typename T>
-__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ parts, size_t part, int splits, int M,
-                                                    int N, const int32_t* __restrict__ offsets, int E,
-                                                    T* __restrict__ c) {
-  const size_t total = (size_t)M * N;
-  size_t from = 0, to = total;
-  if (offsets) {
-    from = (size_t)min(max(offsets[0], 0), M) * N;
-    to = (size_t)min(max(offsets[E], 0), M) * N;
-  }
-  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < to; i += (size_t)gridDim.x * 1024) {
-    if (i + 4 <= from) continue;
+__global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ parts, size_t part, int splits,
+                                                    size_t total, T* __restrict__ c) {
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += (size_t)gridDim.x * 1024) {
     f32x4_t v = *reinterpret_cast<const f32x4_t*>(parts + i);
     for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(parts + s * part + i);
-    if (i >= from && i + 4 <= to) {
+    if (i + 4 <= total) {
       typedef T T4 __attribute__((ext_vector_type(4)));
       T4 o;
 #pragma unroll
@@ -124,7 +123,7 @@ __global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ pa
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (i + r >= from && i + r < to) c[i + r] = (T)v[r];
+        if (i + r < total) c[i + r] = (T)v[r];
     }
   }
 }
@@ -191,7 +190,7 @@ hipError_t gemm(GemmArgs g, void* ws, hipStream_t stream) {
       s.g = g;
       const int tiles = (g.N + 15) / 16;
       s.ks = tiles >= 2048 ? 1 : tiles >= 640 ? 2 : tiles >= 320 ? 4 : 8;
-      return run_stream<StreamKernel<1, 8, 4, 0, false, float, T>>(s, 8 / s.ks * 16, stream);
+      return run_stream<StreamKernel<8, 4, false, float, T>>(s, 8 / s.ks * 16, stream);
     }
     case kSmall: {
       if (how.splits == 1) return small_tiles<EXACT, T>(g, 1, stream);
@@ -200,9 +199,9 @@ hipError_t gemm(GemmArgs g, void* ws, hipStream_t stream) {
       g.part = part_values(g.M, g.N);
       const hipError_t e = small_tiles<EXACT, float>(g, how.splits, stream);
       if (e != hipSuccess) return e;
-      const size_t quads = ((size_t)g.M * g.N + 1023) / 1024;
-      hipLaunchKernelGGL(k_join_parts<T>, dim3((unsigned)(quads < 2048 ? quads : 2048)), dim3(256), 0, stream,
-                         static_cast<const float*>(ws), g.part, how.splits, g.M, g.N, g.offsets, g.E, c);
+      const size_t total = (size_t)g.M * g.N, blocks = (total + 1023) / 1024;
+      hipLaunchKernelGGL(k_join_parts<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0,
+                         stream, static_cast<const float*>(ws), g.part, how.splits, total, c);
       return hipGetLastError();
     }
     case kMiddle: return run_tiles<TileKernel<128, 128, 2, 2, EXACT, false, T>>(g, 128, 1, stream);
@@ -219,7 +218,7 @@ hipError_t gemm(GemmArgs g, void* ws, hipStream_t stream) {
 
 template <typename T_IN>
 hipError_t stream_gate_up(const StreamArgs& s, hipStream_t stream) {
-  return run_stream<StreamKernel<1, 16, 3, 1, true, T_IN, float>>(s, 128, stream);
+  return run_stream<StreamKernel<16, 3, true, T_IN, float>>(s, 128, stream);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
