@@ -328,9 +328,10 @@ enum { ZINC_F16 = 0, ZINC_BF16 = 1, ZINC_F32 = 2 };
  *             (1 is then ORed into *dev_error as in zinc_moe_q4k_experts; may be NULL)
  *   row_slot  int32 [M x top_k]: a row's slot, -1 for the rows from offsets[n_experts] on
  * An expert may occur more than once in a token; each slot has a row.  M == 0 writes the
- * offsets (zeros) and needs no other pointer.  1 <= n_experts <= 1024, 1 <= top_k <= 1024, M * top_k <=
- * 2^24 (else ZINC_ERR_ARG; the size query returns 0, as it does where no workspace is needed:
- * workspace may then be NULL).  int32 pointers are 4-byte aligned, the workspace 16.
+ * offsets (zeros) and needs no other pointer.  1 <= n_experts <= 1024, 1 <= top_k <= 1024,
+ * M * top_k <= 2^24 (else ZINC_ERR_ARG; the size query returns 0, as it does where no
+ * workspace is needed: workspace may then be NULL).  int32 pointers are 4-byte aligned,
+ * the workspace 16.
  */
 size_t zinc_moe_sort_workspace_size(int32_t M, int32_t top_k, int32_t n_experts);
 int zinc_moe_sort(const int32_t* expert_ids, int32_t M, int32_t top_k, int32_t n_experts, int32_t* offsets,
@@ -386,9 +387,9 @@ int zinc_fp8_quantize(const void* x, int32_t type, int32_t rows, int32_t cols, i
  * Product of FP8 matrices, c[M x N] of out_type:
  *   c[m][n] = sum_kb a_scales[m][kb] w_scales[n / 128][kb] sum_{k in block kb} a[m][k] w[n][k]
  * accumulated in fp32 and rounded once; a [M x K] activations, w [N x K] weights.  For 16-bit
- * outputs of more than 16 rows the FP8 matrix instructions add products in groups of
- * eight k, cut at 2^-13 of the group's largest (about 1.5e-5 of a result, where the
- * output's rounding is 2e-4 or 1.7e-3); fp32 outputs, and up to 16 dense rows, take exact fp16 operands.
+ * outputs the FP8 matrix instructions add products in groups of eight k, cut at 2^-13
+ * of the group's largest (about 1.5e-5 of a result, where the output's rounding is 2e-4
+ * or 1.7e-3); fp32 outputs, and up to 4 dense rows, take exact fp16 operands.
  * zinc_moe_gemm_fp8: w holds n_experts matrices, and row r of a [rows x K] with
  * offsets[e] <= r < offsets[e + 1] takes expert e's (offsets int32 [n_experts + 1] on
  * the GPU, as zinc_moe_sort writes them; the host never reads them).  Rows outside

@@ -626,7 +626,7 @@ def test_outputs_given_by_the_caller_are_the_ones_returned():
 # ---------------------------------------------------------------- both sides of each choice by size; neighbours
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(4, 200, 8208), (5, 200, 8208), (16, 100, 11024), (64, 128, 640), (65, 128, 1296),
-                                   (64, 24, 65536), (5, 11000, 1040), (190, 4096, 256)])
+                                   (64, 24, 65536), (5, 11000, 1040), (190, 4096, 256), (4, 24, 65536), (3, 340, 40976)])
 def test_gemm_where_k_is_split(kind, M, N, K):
     test_gemm(kind, M, N, K)
 
