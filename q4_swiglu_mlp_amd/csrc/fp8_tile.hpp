@@ -158,9 +158,9 @@ __device__ __forceinline__ const __attribute__((address_space(4))) float* unifor
 //
 // What bounds it, on random data: with FP8 MFMAs the power limit (8192 x 11008 x 4096
 // 331 us, 2230 TFLOP/s at about 1.9 GHz; the MFMAs alone reach 3900 with their four FMAs).
-// With fp16 MFMAs the issue of vector instructions: 3.5 beside each MFMA (two conversions,
-// one FMA), of which about one hides in its 16 cycles; they are busy 53 % of the cycles,
-// 1230 TFLOP/s at 2.16 GHz for 8192^2 x 4096, and as many cycles go without the copies.
+// With fp16 MFMAs 1230 TFLOP/s for 8192^2 x 4096, the rate of a large bf16 library product
+// (1210): they are busy 53 % of the cycles, and with fewer vector instructions, no
+// copies' latency or other orders the time stays within 3 % while the clock moves against it.
 //
 // Workgroups are persistent: each walks its units (a tile, or a part of its K)
 // and copies the next unit's first blocks while it finishes the one before, so a
