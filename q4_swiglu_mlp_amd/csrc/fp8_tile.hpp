@@ -7,8 +7,8 @@
 //
 // Per step of one block of 128 the two tiles, [TM x 128] and [TN x 128] bytes,
 // are copied straight to LDS (16 bytes a lane, no registers in between) into
-// one of two buffers while the waves multiply from the other; one barrier a
-// step.  An LDS row is 128 bytes, its eight 16-byte pieces stored in the order
+// one of two or three buffers while the waves multiply from another; one barrier
+// a step.  An LDS row is 128 bytes, its eight 16-byte pieces stored in the order
 // piece ^ ((row >> 1) & 7) (w's: piece ^ w_turn(row)), so that the lanes of a read,
 // which run over rows, spread over all 64 banks (two rows fill them).  Which k a
 // lane's piece holds is free as long as both operands agree: lane quarter q takes
@@ -158,7 +158,7 @@ __device__ __forceinline__ const __attribute__((address_space(4))) float* unifor
 //
 // What bounds it, on random data: with FP8 MFMAs the power limit (8192 x 11008 x 4096
 // 331 us, 2230 TFLOP/s at about 1.9 GHz; the MFMAs alone reach 3900 with their four FMAs).
-// With fp16 MFMAs 1230 TFLOP/s for 8192^2 x 4096, the rate of a large bf16 library product
+// With fp16 MFMAs 1230 TFLOP/s for 8192^2 x 4096 (16-bit stores), the rate of a large bf16 library product
 // (1210): they are busy 53 % of the cycles, and with fewer vector instructions, no
 // copies' latency or other orders the time stays within 3 % while the clock moves against it.
 //
@@ -181,6 +181,11 @@ struct TileKernel {
   // 16-bit outputs are stored past the caches: 8192 x 11008 x 4096 328 us against 368, whose
   // stores push the operands' tiles out of L2.  fp32 ones may be parts of K, read again soon.
   static constexpr bool STREAMED = sizeof(T) == 2;
+  // Buffers: with three, the copies of two blocks are in flight; where one workgroup fits a
+  // CU either way.  Experts of 256 / 512 tokens, top-8 of 64, 105.5 us / 123.5 against 109 /
+  // 127.5 with two, 4001 tokens the same, 32000 fp32 rows of 2048 x 768 150 against 160.
+  // 256 x 256 has no room for a third, the small tiles fill LDS with more workgroups.
+  static constexpr int NBUF = TN == 256 && TM <= 128 ? 3 : 2;
   static constexpr int BAND = 8;                    // row tiles walked per column
   // workgroups a CU holds by registers: three waves a SIMD where a wave has 32 sums, else two
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
@@ -192,8 +197,8 @@ struct TileKernel {
   static __device__ __forceinline__ int w_turn(int row) { return ((row >> 1) & 1) + 2 * ((row >> 3) & 3); }
 
   struct Smem {
-    uint8_t tile[2][ROWS * 128];
-    float sa[2][TM];                      // a's scales of the buffer's block
+    uint8_t tile[NBUF][ROWS * 128];
+    float sa[NBUF][TM];                      // a's scales of the buffer's block
     uint32_t part[DUAL ? WN * TM : 1];    // the waves' row maxima
   };
   // behind it, where experts are grouped: starts[E + 1], the experts' first rows,
@@ -319,7 +324,7 @@ struct TileKernel {
     };
     auto whole = [&] { return lu < last && (ld.kb0 + lk + 1) * 128 <= K; };
     auto copy_cut = [&](int buf) {   // the last block of K, cut short: zeros behind it
-      if (lu >= last) return;
+      if (DUAL || lu >= last) return;   // (gate's and up's K has whole blocks only)
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int r = i * WAVES * 8, kb = ld.kb0 + lk;
@@ -396,10 +401,14 @@ struct TileKernel {
     };
 
     copy_all(0);
-    const bool two = whole();   // the second block's copies may be in flight behind the first's
+    bool ahead = whole();   // the later blocks' copies may be in flight behind the first's
     copy_all(1);
-    if (two)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PIECES) : "memory");
+    if constexpr (NBUF == 3) {
+      ahead = ahead && whole();
+      copy_all(2);
+    }
+    if (ahead)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 1) * PIECES) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -408,6 +417,7 @@ struct TileKernel {
     for (int j = 0; j < NT; ++j) read_w(j, 0);
     read_a(0, 0, 0);
     int buf = 0;
+    auto after = [](int b) { return NBUF == 2 ? b ^ 1 : b == NBUF - 1 ? 0 : b + 1; };
     for (; u < last; u += stride) {
       const Unit cu = unit_at(g, starts, ends, row_tiles, KB, u);
       const int n0 = cu.nt * COLS;
@@ -425,12 +435,13 @@ struct TileKernel {
       const size_t sw_at =
           ((size_t)cu.expert * NB + (DUAL ? cu.nt : min((n0 + wn * (TN / WN)) >> 7, NB - 1))) * KB + cu.kb0;
       const auto sw1 = uniform(g.sw + sw_at), sw2 = uniform((DUAL ? g.sw2 : g.sw) + sw_at);
-      for (int kb = 0; kb < cu.kbs; ++kb, buf ^= 1) {
+      for (int kb = 0; kb < cu.kbs; ++kb, buf = after(buf)) {
         const float t1 = sw1[kb], t2 = DUAL ? sw2[kb] : 0.0f;
         float sn[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) sn[i] = sm.sa[buf][wm * (TM / WM) + i * 16 + l16];
         const bool fast = whole();
+        const int next = after(buf);
         Frag<EXACT> fw[NT], fa[2];
 #pragma unroll
         for (int t0 = 0; t0 < TILES; t0 += GROUP) {
@@ -451,7 +462,10 @@ struct TileKernel {
               fa[0].set(ar[0]);
               fa[1].set(ar[1]);
               // the next block has landed, and every wave has read what it needs of this one
-              asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+              if (NBUF == 3 && ahead)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PIECES) : "memory");
+              else
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
               __builtin_amdgcn_s_barrier();
               asm volatile("" ::: "memory");
               if (!fast) copy_cut(buf);
@@ -472,8 +486,8 @@ struct TileKernel {
                   if (c < PIECES) copy_piece(c, buf);
                 if (t == TILES - 1) copy_scales(buf);
               }
-              if (v & 1) read_w(col_of(t), buf ^ 1);
-              if (t == TILES - 1) read_a(0, 0, buf ^ 1);
+              if (v & 1) read_w(col_of(t), next);
+              if (t == TILES - 1) read_a(0, 0, next);
             }
             if (t < LAG) {
               add(TILES - LAG + t);
@@ -491,6 +505,7 @@ struct TileKernel {
           __builtin_amdgcn_sched_barrier(0);
         }
         advance();
+        ahead = fast;
       }
 #pragma unroll
       for (int t = 0; t < LAG; ++t) add(TILES - LAG + t);

@@ -23,8 +23,8 @@
 // What bounds it (TB/s and TFLOP/s of the whole call):
 // - few rows, the pass over w: 1 x 11008 x 4096 11 us, 4.1 TB/s;
 // - many rows, the matrix units at the clock that the power limit leaves (about 1.9 GHz):
-//   8192 x 11008 x 4096 bf16 331 us, 2230 TFLOP/s; fp32 by fp16 MFMAs 446 us for
-//   8192 x 8192 x 4096, 1230 TFLOP/s.
+//   8192 x 11008 x 4096 bf16 331 us, 2230 TFLOP/s (345 us on another card); fp32 by
+//   fp16 MFMAs 490 us for 8192 x 8192 x 4096, 1120 TFLOP/s.
 #include <atomic>
 
 #include "fp8_stream.hpp"
@@ -318,10 +318,10 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   if (e != hipSuccess) return e;
   // The gate and up products, by the mean rows of an expert (64 experts, top-8, 2048 to
   // 768, ids at random; us of the whole call).  While no expert has more than 16 rows the
-  // weights stream past tokens that are quantised on the way: mean 8 84 against 96 with tiles
-  // of 64 rows, 13 93 against 100, 14 101 against 100.  Tiles of 64 rows where they
-  // hold any expert: mean 16 101 against 112 with tiles of 128 rows, 42 109 against 121,
-  // 44 123 each, 64 135 against 129.
+  // weights stream past tokens that are quantised on the way: mean 8 84 against 95 with tiles
+  // of 64 rows, 13 92 against 98, 14 101 against 98.  Tiles of 64 rows where they
+  // hold any expert: mean 16 99 against 110 with tiles of 128 rows, 42 104 against 117,
+  // 44 118 and 119, 64 132 against 125.
   const int mean = S / E;
   if (mean <= 13) {
     StreamArgs s{};
