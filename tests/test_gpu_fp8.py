@@ -637,12 +637,22 @@ def test_grouped_gemm_around_its_tiles(kind, mean):
     test_grouped_gemm(kind, [mean, mean + 2, mean - 2], 200, 272)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("mean", [1, 321])
+def test_grouped_gemm_of_the_most_experts(kind, mean):
+    test_grouped_gemm(kind, [mean] * 1024, 8, 16)
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("E,H,I,M,k", [(2, 256, 256, 13, 2), (2, 256, 256, 14, 2), (2, 128, 384, 43, 2),
                                        (2, 128, 384, 44, 2), (2, 16384, 128, 9, 2), (1, 128, 65536, 5, 1),
                                        (1024, 128, 128, 3, 1024)])
 def test_experts_around_their_kernels(kind, E, H, I, M, k):
     run_experts(np.random.default_rng(E + H + I + M), E, H, I, M, k, kind)
+
+
+def test_experts_of_the_most_experts():
+    run_experts(np.random.default_rng(29), 1024, 128, 128, 44, 1024, "f16")
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
