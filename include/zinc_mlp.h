@@ -413,8 +413,9 @@ int zinc_moe_gemm_fp8(const void* a, const float* a_scales, const void* w, const
  *   y[t] = sum_s p[t, s] W_down_e . hq,   hq = Q( silu(W_gate_e . xq) (*) (W_up_e . xq) ),   xq = Q(x[t])
  * with e = ids[t, s] and Q the quantiser above with one scale per row and 128
  * columns.  Gate and up rows and h are fp32 until Q, their products' sums exact to fp32
- * rounding; the experts' output rows are fp32 up to 2^22 values (M * top_k * hidden) and
- * rounded to x's type beyond, and the weighted sum is taken in fp32.  w_gate, w_up: n_experts
+ * rounding; the experts' output rows are fp32 too and the weighted sum is taken in fp32, so y's
+ * rounding to x's type is the only one.  (The down product of a bf16 layer takes the FP8 matrix
+ * instructions, as zinc_moe_gemm_fp8's 16-bit outputs do.)  w_gate, w_up: n_experts
  * [inter x hidden] FP8 weight matrices, w_down: n_experts [hidden x inter].
  * x and y [M x hidden] of `type`.  Ids outside [0, n_experts) contribute nothing and set
  * *dev_error; duplicate ids each count.  Nothing is read back by the host.

@@ -121,7 +121,7 @@ int zinc_moe_combine(const void* ys, int32_t type, int32_t M, int32_t top_k, int
   if (!aligned(ys, 16) || !aligned(y, 16) || !aligned(slot_row, 4) || !aligned(expert_weights, 4))
     return ZINC_ERR_ALIGN;
   return zinc::status_from_hip(
-      zinc::launch_moe_combine(ys, type, type, M, top_k, hidden, slot_row, expert_weights, y, begin(stream)));
+      zinc::launch_moe_combine(ys, type, M, top_k, hidden, slot_row, expert_weights, y, begin(stream)));
 }
 
 int zinc_moe_combine_backward(const void* dy, const void* ys, int32_t type, int32_t M, int32_t top_k, int32_t hidden,
@@ -173,7 +173,7 @@ int zinc_moe_gemm_fp8(const void* a, const float* a_scales, const void* w, const
 size_t zinc_moe_fp8_experts_workspace_size(int32_t M, int32_t top_k, int32_t n_experts, int32_t hidden, int32_t inter,
                                            int32_t type) {
   if (!dims_ok(hidden, inter) || !type_ok(type) || !experts_ok(M, top_k, n_experts)) return 0;
-  return zinc::moe_fp8_workspace_bytes(M, top_k, n_experts, hidden, inter, type);
+  return zinc::moe_fp8_workspace_bytes(M, top_k, n_experts, hidden, inter);
 }
 
 int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const void* w_up, const float* up_scales,
@@ -192,7 +192,7 @@ int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const voi
       !aligned(expert_weights, 4) || !aligned(dev_error, 4))
     return ZINC_ERR_ALIGN;
   const int st = check_workspace(workspace, workspace_bytes,
-                                 zinc::moe_fp8_workspace_bytes(M, top_k, n_experts, hidden, inter, type));
+                                 zinc::moe_fp8_workspace_bytes(M, top_k, n_experts, hidden, inter));
   if (st != ZINC_OK) return st;
   return zinc::status_from_hip(zinc::launch_moe_fp8(w_gate, gate_scales, w_up, up_scales, w_down, down_scales,
                                                     n_experts, hidden, inter, x, type, M, expert_ids, expert_weights,

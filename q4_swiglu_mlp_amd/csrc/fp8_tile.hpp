@@ -117,7 +117,6 @@ struct GemmArgs {
   int row_tiles, col_tiles;   // an upper bound of the row tiles, where experts are grouped
   int splits;           // parts of K, each with its own output,
   size_t part;          // this many values after the one before
-  bool read_soon;       // the output is read by the next launch: kept in the caches
   void* c;
   float* cs;            // scales of a quantised output
 };
@@ -179,7 +178,8 @@ struct TileKernel {
   static constexpr int ROWS = TM + TN;              // LDS rows of a buffer
   static constexpr int PIECES = ROWS * 8 / THREADS; // 16-byte pieces a thread copies per step
   // 16-bit outputs are stored past the caches: 8192 x 11008 x 4096 328 us against 368, whose
-  // stores push the operands' tiles out of L2.  fp32 ones may be parts of K, read again soon.
+  // stores push the operands' tiles out of L2.  fp32 ones may be parts of K or an
+  // expert layer's rows, read again soon.
   static constexpr bool STREAMED = sizeof(T) == 2;
   // Buffers: with three, the copies of two blocks are in flight; where one workgroup fits a
   // CU either way.  Experts of 256 / 512 tokens, top-8 of 64, 105.5 us / 123.5 against 109 /
@@ -529,10 +529,8 @@ struct TileKernel {
           float v[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
-          if (wide && STREAMED && !g.read_soon) {
+          if (wide) {
             if (n < N) store8<STREAMED>(row + n, v);
-          } else if (wide) {
-            if (n < N) store8(row + n, v);
           } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r)

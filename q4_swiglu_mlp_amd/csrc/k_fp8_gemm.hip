@@ -14,8 +14,8 @@
 // it; the groups then add in fp32.  Products have eight bits, so only those
 // below 2^-6 of a group's largest lose any: measured 1.5e-5 of the result
 // (2-norm, normal data, K = 128), far below the rounding of a 16-bit output (2e-4
-// fp16, 1.7e-3 bf16).  fp32 outputs (an expert layer's fp16 rows too) and the
-// products that feed an expert layer's second quantisation take the fp16 MFMA on exactly
+// fp16, 1.7e-3 bf16).  fp32 outputs (the expert rows of an fp16 or fp32 layer too; a bf16
+// layer's take the FP8 MFMA) and the products that feed an expert layer's second quantisation take the fp16 MFMA on exactly
 // converted operands instead: half the rate, 7e-9 of the result.  In that quantisation
 // 1.5e-5 moves a value in 5000 to the next code, which is 1.2e-3 of y beside the
 // 2e-4 and 1.7e-3 of its own rounding (measured for bf16: 3.3e-3 in all against 1.7e-3).
@@ -223,28 +223,17 @@ hipError_t stream_gate_up(const StreamArgs& s, hipStream_t stream) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// The type of the experts' output rows before they are combined.  In x's 16-bit type their
-// rounding is as large as the output's own (1.4 times its error); as fp32 they are
-// twice the bytes, which matters where they do not stay in the caches: 131 MB of
-// bf16 at 4001 tokens, top-8, hidden 2048.
-constexpr size_t kWideRows = 4 << 20;   // values kept as fp32
-int rows_type(size_t S, int H, int type) { return S * H <= kWideRows ? 2 : type; }
-// (not less for more rows)
-size_t rows_bytes(size_t S, int H, int type) {
-  const size_t wide = (S * H < kWideRows ? S * H : kWideRows) * 4, all = S * H * (type == 2 ? 4 : 2);
-  return wide > all ? wide : all;
-}
-
-// The expert call's workspace.
+// The expert call's workspace.  The experts' output rows are terms of y's sum: fp32, so that y's
+// rounding is the only one to 16 bits, and no row leaves fp16's range before its weight.
 struct ExpertsPlan {
   int32_t *offsets, *slot_row, *row_slot;
   void* sort_ws;
   uint8_t *xq, *hq;
   float *xs, *hs;
-  void* ys;
+  float* ys;
 };
 
-ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, size_t* total) {
+ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, size_t* total) {
   ExpertsPlan p;
   char* base = static_cast<char*>(ws);
   size_t off = 0;
@@ -258,7 +247,7 @@ ExpertsPlan carve(void* ws, int M, int top_k, int E, int H, int I, int type, siz
   p.xs = reinterpret_cast<float*>(take(S * (H / 128) * 4));
   p.hq = reinterpret_cast<uint8_t*>(take(S * I));
   p.hs = reinterpret_cast<float*>(take(S * (I / 128) * 4));
-  p.ys = take(rows_bytes(S, H, type));
+  p.ys = reinterpret_cast<float*>(take(S * H * 4));
   if (total) *total = off;
   return p;
 }
@@ -289,16 +278,16 @@ size_t gemm_fp8_workspace_bytes(int M, int E, int N, int K) {
   return how.splits > 1 ? (size_t)how.splits * part_values(M, N) * sizeof(float) : 0;
 }
 
-size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I, int type) {
+size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I) {
   size_t total = 0;
-  carve(nullptr, M, top_k, E, H, I, type, &total);
+  carve(nullptr, M, top_k, E, H, I, &total);
   return total;
 }
 
 hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const float* su, const void* wd,
                           const float* sd, int E, int H, int I, const void* x, int type, int M, const int32_t* ids,
                           const float* p, int top_k, void* y, void* ws, int32_t* dev_error, hipStream_t stream) {
-  const ExpertsPlan pl = carve(ws, M, top_k, E, H, I, type, nullptr);
+  const ExpertsPlan pl = carve(ws, M, top_k, E, H, I, nullptr);
   const int S = M * top_k;
   hipError_t e = launch_moe_sort(ids, S, E, pl.offsets, pl.slot_row, pl.row_slot, pl.sort_ws, dev_error, stream);
   GemmArgs g{};
@@ -347,14 +336,9 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.N = H;
   g.K = I;
   g.c = pl.ys;
-  g.read_soon = true;
-  const int ys_type = rows_type(S, H, type);
   if (e != hipSuccess) return e;
-  if (type == 1)
-    e = ys_type == 2 ? gemm<false, float>(g, nullptr, stream) : gemm<false, __bf16>(g, nullptr, stream);
-  else
-    e = ys_type == 2 ? gemm<true, float>(g, nullptr, stream) : gemm<true, _Float16>(g, nullptr, stream);
-  if (e == hipSuccess) e = launch_moe_combine(pl.ys, ys_type, type, M, top_k, H, pl.slot_row, p, y, stream);
+  e = type == 1 ? gemm<false, float>(g, nullptr, stream) : gemm<true, float>(g, nullptr, stream);
+  if (e == hipSuccess) e = launch_moe_combine_rows(pl.ys, type, M, top_k, H, pl.slot_row, p, y, stream);
   return e;
 }
 

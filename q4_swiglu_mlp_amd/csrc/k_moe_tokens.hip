@@ -316,16 +316,19 @@ dim3 token_grid(int M, int pieces) {
   return dim3((unsigned)(M < (1 << 18) ? M : (1 << 18)), (unsigned)((pieces + 255) / 256));
 }
 
-template <typename T_IN, typename T>
+template <typename T_IN, typename T, bool WEIGHTED>
 void combine(const void* ys, int M, int top_k, int H, const int32_t* slot_row, const float* p, void* y,
              hipStream_t stream) {
-  const dim3 grid = token_grid(M, H / 8);
-  if (p)
-    hipLaunchKernelGGL((k_combine<T_IN, T, true>), grid, dim3(256), 0, stream, static_cast<const T_IN*>(ys), H, M,
-                       top_k, slot_row, p, static_cast<T*>(y));
-  else
-    hipLaunchKernelGGL((k_combine<T_IN, T, false>), grid, dim3(256), 0, stream, static_cast<const T_IN*>(ys), H, M,
-                       top_k, slot_row, p, static_cast<T*>(y));
+  hipLaunchKernelGGL((k_combine<T_IN, T, WEIGHTED>), token_grid(M, H / 8), dim3(256), 0, stream,
+                     static_cast<const T_IN*>(ys), H, M, top_k, slot_row, p, static_cast<T*>(y));
+}
+
+template <bool WEIGHTED>
+void combine_type(const void* ys, int type, int M, int top_k, int H, const int32_t* slot_row, const float* p, void* y,
+                  hipStream_t stream) {
+  if (type == 0) combine<_Float16, _Float16, WEIGHTED>(ys, M, top_k, H, slot_row, p, y, stream);
+  if (type == 1) combine<__bf16, __bf16, WEIGHTED>(ys, M, top_k, H, slot_row, p, y, stream);
+  if (type == 2) combine<float, float, WEIGHTED>(ys, M, top_k, H, slot_row, p, y, stream);
 }
 
 template <typename T>
@@ -371,17 +374,20 @@ hipError_t launch_moe_gather(const void* x, int row_bytes, int M, int top_k, con
   return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const void* ys, int ys_type, int type, int M, int top_k, int H,
-                              const int32_t* slot_row, const float* p, void* y, hipStream_t stream) {
-  if (ys_type == 2) {
-    if (type == 0) combine<float, _Float16>(ys, M, top_k, H, slot_row, p, y, stream);
-    if (type == 1) combine<float, __bf16>(ys, M, top_k, H, slot_row, p, y, stream);
-    if (type == 2) combine<float, float>(ys, M, top_k, H, slot_row, p, y, stream);
-  } else if (type == 0) {
-    combine<_Float16, _Float16>(ys, M, top_k, H, slot_row, p, y, stream);
-  } else {
-    combine<__bf16, __bf16>(ys, M, top_k, H, slot_row, p, y, stream);
-  }
+hipError_t launch_moe_combine(const void* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
+                              const float* p, void* y, hipStream_t stream) {
+  if (p)
+    combine_type<true>(ys, type, M, top_k, H, slot_row, p, y, stream);
+  else
+    combine_type<false>(ys, type, M, top_k, H, slot_row, p, y, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_rows(const float* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
+                                   const float* p, void* y, hipStream_t stream) {
+  if (type == 0) combine<float, _Float16, true>(ys, M, top_k, H, slot_row, p, y, stream);
+  if (type == 1) combine<float, __bf16, true>(ys, M, top_k, H, slot_row, p, y, stream);
+  if (type == 2) combine<float, float, true>(ys, M, top_k, H, slot_row, p, y, stream);
   return hipGetLastError();
 }
 

@@ -71,9 +71,11 @@ hipError_t launch_moe_sort(const int32_t* ids, int S, int E, int32_t* offsets, i
                            void* ws, int32_t* dev_error, hipStream_t stream);
 hipError_t launch_moe_gather(const void* x, int row_bytes, int M, int top_k, const int32_t* slot_row, void* xs,
                              hipStream_t stream);
-// ys_type: type, or fp32.
-hipError_t launch_moe_combine(const void* ys, int ys_type, int type, int M, int top_k, int H,
-                              const int32_t* slot_row, const float* p, void* y, hipStream_t stream);
+hipError_t launch_moe_combine(const void* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
+                              const float* p, void* y, hipStream_t stream);
+// The same of fp32 rows; `type` is y's, p is given.
+hipError_t launch_moe_combine_rows(const float* ys, int type, int M, int top_k, int H, const int32_t* slot_row,
+                                   const float* p, void* y, hipStream_t stream);
 hipError_t launch_moe_combine_backward(const void* dy, const void* ys, int type, int M, int top_k, int H,
                                        const int32_t* slot_row, const float* p, void* dys, float* dp,
                                        hipStream_t stream);
@@ -89,7 +91,7 @@ hipError_t launch_moe_gather_fp8(const void* x, int type, int M, int top_k, int 
 size_t gemm_fp8_workspace_bytes(int M, int E, int N, int K);
 hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const float* sw, const int32_t* offsets,
                            int E, int M, int N, int K, int out_type, void* c, void* ws, hipStream_t stream);
-size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I, int type);
+size_t moe_fp8_workspace_bytes(int M, int top_k, int E, int H, int I);
 hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const float* su, const void* wd,
                           const float* sd, int E, int H, int I, const void* x, int type, int M, const int32_t* ids,
                           const float* p, int top_k, void* y, void* ws, int32_t* dev_error, hipStream_t stream);

@@ -734,3 +734,44 @@ def test_repeated_slot_rows_are_summed_by_the_gather_backward():
     got = host(Z.zinc_moe_gather_backward(dxs, slot_row))
     d = host(dxs)
     assert np.array_equal(got, np.float32(np.stack([2 * d[0], d[3], d[7] + d[3], 0 * d[0]])))
+
+
+# ---------------------------------------------------------------- expert rows: a sum's terms, held in fp32
+def _wide_rows(M, kind):
+    """A layer of 2^22 row values at 256 tokens, with rows of 1e5 and more, beyond fp16, under weights that bring y back
+    into its range; x has values that bf16 and fp16 both hold."""
+    rng = np.random.default_rng(30)
+    E, k, H, I = 8, 8, 2048, 128
+    w = [(c, s * np.float32(f)) for (c, s), f in ((fp8_matrix(rng, E, I, H), 0.3), (fp8_matrix(rng, E, I, H), 0.3),
+                                                  (fp8_matrix(rng, E, H, I), 1000.0))]
+    x = activations(rng, M, H, "f16").bfloat16().clamp(-4, 4)
+    x = torch.where(x.abs() < 2.0 ** -10, 0.0, x).to(TYPES[kind][0])
+    ids = np.argsort(rng.random((M, E)), axis=1).astype(np.int32)
+    p = rng.uniform(0.001, 0.004, size=ids.shape).astype(np.float32)
+    args = [v for c, s in w for v in (e4m3(c), dev(s))]
+    return w, x, ids, p, lambda v: Z.zinc_moe_fp8_experts(*args, v, dev(ids), dev(p))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [256, 257, 900])
+def test_experts_round_y_only(kind, M):
+    """A 16-bit layer's y is the fp32 layer's, rounded once: for fp16 bit for bit, as every step before is the same.  A
+    bf16 layer's down product takes the FP8 MFMA: beside the rounding y may be off by the cut (twice, as a code of h
+    next to a tie moves its group's exponent by one at most) and both products' fp32 sums."""
+    (_, _, down), x, ids, p, call = _wide_rows(M, kind)
+    y, y32 = call(x), call(x.float())
+    if kind == "f16":
+        assert torch.isfinite(y).all() and torch.equal(y, y32.half())
+        return
+    _, slots = F.experts(*_wide_rows(M, kind)[0], host(x), ids, p)
+    slack, top = np.zeros(tuple(x.shape)), 0.0
+    for e in range(len(down[0])):
+        t, w, h = (np.array([v[i] for v in slots if v[2] == e]) for i in (0, 1, 3))
+        q, s = F.quantize(h)
+        rows, wd = F.dequantize(q, s, 1), F.dequantize(down[0][e], down[1][e], 128)
+        top = max(top, np.abs(rows @ wd.T).max())
+        size = np.abs(rows) @ np.abs(wd).T
+        sums = 2 * ((h.shape[1] + 16) * 2.0 ** -23 + (ids.shape[1] + 1) * 2.0 ** -24) * size
+        np.add.at(slack, t, w[:, None] * (sums + 2 * cut(q, s, down[0][e], down[1][e])))
+    assert top > 65504
+    close(y, host(y32), slack, kind, "bf16 layer")
