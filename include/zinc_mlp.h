@@ -330,8 +330,8 @@ enum { ZINC_F16 = 0, ZINC_BF16 = 1, ZINC_F32 = 2 };
  * An expert may occur more than once in a token; each slot has a row.  M == 0 writes the
  * offsets (zeros) and needs no other pointer.  1 <= n_experts <= 1024, 1 <= top_k <= 1024,
  * M * top_k <= 2^24 (else ZINC_ERR_ARG; the size query returns 0, as it does where no
- * workspace is needed: workspace may then be NULL).  int32 pointers are 4-byte aligned,
- * the workspace 16.
+ * workspace is needed: workspace may then be NULL).  The workspace size is non-decreasing
+ * in M.  int32 pointers are 4-byte aligned, the workspace 16.
  */
 size_t zinc_moe_sort_workspace_size(int32_t M, int32_t top_k, int32_t n_experts);
 int zinc_moe_sort(const int32_t* expert_ids, int32_t M, int32_t top_k, int32_t n_experts, int32_t* offsets,

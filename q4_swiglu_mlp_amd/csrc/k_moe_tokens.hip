@@ -342,9 +342,12 @@ void combine_backward(const void* dy, const void* ys, int M, int top_k, int H, c
 
 }  // namespace
 
+// The workgroups' histograms, by a bound on their number that does not fall as slots are added:
+// past 262144 slots a workgroup takes more of them, and then there are fewer than 256.
 size_t moe_sort_workspace_bytes(int S, int E) {
-  const int b = sort_blocks(S);
-  return b > 1 ? (size_t)b * (1 + kSortWaves) * E * sizeof(int32_t) : 0;
+  if (S <= kOneBlockSlots) return 0;
+  const int b = (S + 1023) / 1024;
+  return (size_t)(b < kSortMaxBlocks ? b : kSortMaxBlocks) * (1 + kSortWaves) * E * sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int S, int E, int32_t* offsets, int32_t* slot_row, int32_t* row_slot,

@@ -188,3 +188,19 @@ def test_binding_checks(fn, good, wrong):
     for bad, msg in wrong:
         with pytest.raises(ValueError, match=msg):
             fn(**{**good, **bad})
+
+
+@pytest.mark.parametrize("E", [1, 64, 256, 1024])
+@pytest.mark.parametrize("k,H,I", [(1, 256, 128), (8, 2048, 768)])
+def test_workspaces_do_not_shrink_with_more_tokens(E, k, H, I):
+    """Token by token around each size where the sort is spread otherwise: 4096 slots, one workgroup or more; from
+    262144 on every 131072, 512 more slots a workgroup."""
+    k = min(k, E)
+    slots = [512, 4096, 5120, 131072] + [131072 * i for i in range(2, 129)]
+    for sizes in (lambda m: Z.moe_fp8_workspace_size(m, k, E, H, I, torch.bfloat16),
+                  lambda m: Z.moe_sort_workspace_size(m, k, E)):
+        last = 0
+        for m in sorted({s // k + d for s in slots for d in range(-2, 3)}):
+            if 0 < m * k <= 1 << 24:
+                assert sizes(m) >= last, m
+                last = sizes(m)
