@@ -140,7 +140,10 @@ struct StreamKernel {
       // quads 0 and 1 hold gate's columns, 2 and 3 up's of the same rows
       float h[8] = {};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) h[r] = silu_times(acc[r], __shfl_xor(acc[r], 32, 64));
+      for (int r = 0; r < 4; ++r) {
+        const float u = __shfl_xor(acc[r], 32, 64);
+        h[r] = __any(acc[r] < kTail) ? silu_times<true>(acc[r], u) : silu_times(acc[r], u);
+      }
       bool whole;
       uint32_t top = max_finite(h, whole);
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));

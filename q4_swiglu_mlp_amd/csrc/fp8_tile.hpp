@@ -136,15 +136,24 @@ __device__ __forceinline__ i32x4_t load_piece(Buffer b, int off) {
 }
 
 // silu(z) u = z u / (1 + e^-z).  e^-z as 2^t (1 + r ln 2) with t = -z log2(e) rounded and r what
-// the rounding left, log2(e) in two parts: within a few units in the last place.
-// t stops at 127, where the quotient is below 2^-126; the reciprocal is within one unit.
+// the rounding left, log2(e) in two parts: within a few units in the last place, and the reciprocal
+// within one.  z is cut for t: at 64, where e^-z adds nothing to 1, and at kTail.
+// From kTail on down (t > 119) the quotient is 2^-t, to 2^-119 of it, and soon leaves fp32's range,
+// where a large u may bring the product back.  TAIL leaves 2^-120 to the reciprocal and takes the rest,
+// 2^(120 - t), as two factors, u first, so that nothing falls out of range before the product does; for
+// other z it gives the same bits.  (Under e^-1024 every u vanishes.)
+constexpr float kTail = -83.0f;
+template <bool TAIL = false>
 __device__ __forceinline__ float silu_times(float z, float u) {
   constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float t = z * kHi;
-  const float r = fmaf(z, kLo, fmaf(z, kHi, -t));
-  const float e2 = __builtin_amdgcn_exp2f(fminf(t, 127.0f));
-  const float e = fmaf(e2, r * kLn2, e2);
-  return z * __builtin_amdgcn_rcpf(1.0f + e) * u;
+  const float c = __builtin_amdgcn_fmed3f(z, TAIL ? -1024.0f : kTail, 64.0f);
+  const float t = c * kHi;
+  const float r = fmaf(c, kLo, fmaf(c, kHi, -t));
+  const float e2 = __builtin_amdgcn_exp2f(TAIL ? fminf(t, 120.0f) : t);
+  const float s = z * __builtin_amdgcn_rcpf(1.0f + fmaf(e2, r * kLn2, e2));
+  if constexpr (!TAIL) return s * u;
+  const float f = __builtin_amdgcn_exp2f(fminf(120.0f - t, 0.0f) * 0.5f);
+  return u * f * f * s;
 }
 
 // The same for the whole workgroup and not written by the kernel: scalar loads.
@@ -542,12 +551,25 @@ struct TileKernel {
       // h = silu(gate) up; a row's maximum over the 128 columns: in the lane, over
       // the four lanes of the row, over the WN waves
       uint32_t* part = sm.part;
-      float h[MT][8];
+      float h[MT][8], low = 0.0f;
       bool whole[MT];
+      auto z = [&](int i, int r) { return acc[i][r >> 2][r & 3]; };
+      auto u = [&](int i, int r) { return acc[i][2 + (r >> 2)][r & 3]; };
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          h[i][r] = silu_times(z(i, r), u(i, r));
+          low = fminf(low, z(i, r));
+        }
+      if (__any(low < kTail)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 8; ++r) h[i][r] = silu_times<true>(z(i, r), u(i, r));
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) h[i][r] = silu_times(acc[i][r >> 2][r & 3], acc[i][2 + (r >> 2)][r & 3]);
         uint32_t m = max_finite(h[i], whole[i]);
         m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
         m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));

@@ -775,3 +775,40 @@ def test_experts_round_y_only(kind, M):
         np.add.at(slack, t, w[:, None] * (sums + 2 * cut(q, s, down[0][e], down[1][e])))
     assert top > 65504
     close(y, host(y32), slack, kind, "bf16 layer")
+
+
+# ---------------------------------------------------------------- gates far from zero
+def test_silu_far_from_zero_in_every_kernel():
+    """One-hot tokens give every h of expert e the gate z_e and the up value u_e exactly, and the down matrix hands
+    hq on, so y is the quantised silu(z) u, exactly: h's few last places do not reach a tie (asserted).  Gates near
+    -88 and below it (e^-z leaves fp32; u brings the product back), far below, and near fp32's largest."""
+    # (gate's code value, log2 of its scale, log2 of u)
+    cases = [(-80, 0, 0), (-88, 0, 0), (-88, 0, 110), (-96, 0, 120), (-104, 0, 120), (-112, 0, 125), (-144, 0, 125),
+             (-240, 0, 125), (-240, 12, 125), (-448, 119, 100), (-352, 119, 0), (88, 0, -30), (-20, 0, 3), (16, 1, 2),
+             (352, 118, -20), (352, 119, -20), (416, 119, -30), (448, 119, -100)]
+    E, H = len(cases), 128
+    def weight(values, logs, cols):
+        w = np.zeros((E, 128, 128))
+        w[:, :, cols] = np.array(values, dtype=np.float64)[:, None, None]
+        return F.e4m3_encode(w), 2.0 ** np.array(logs, dtype=np.float64).reshape(E, 1, 1)
+    gate = weight([c[0] for c in cases], [c[1] for c in cases], [0])
+    up = weight([1.0] * E, [c[2] for c in cases], [0])
+    down = np.broadcast_to(F.e4m3_encode(np.eye(128)), (E, 128, 128)), np.ones((E, 1, 1))
+    for each in (1, 20, 60):
+        ids = np.repeat(np.arange(E), each).astype(np.int32)[:, None]
+        x = np.zeros((E * each, H), np.float32)
+        x[:, 0] = 1.0
+        p = np.ones(ids.shape, np.float32)
+        with np.errstate(over="ignore"):
+            y_ref, slots = F.experts(gate, up, down, x, ids, p)
+        h = np.array([v[3][0] for v in slots])
+        s = F.block_scales(h[:, None], 1)[:, 0]
+        kept = np.abs(h) > 2.0 ** -126
+        near = F.e4m3_decode(F.e4m3_encode(h * (1 + 2.0 ** -18) / s)) == F.e4m3_decode(F.e4m3_encode(h * (1 - 2.0 ** -18) / s))
+        assert near[kept].all()
+        args = [v for c, sc in (gate, up, down) for v in (e4m3(c), dev(sc.astype(np.float32)))]
+        y = host(Z.zinc_moe_fp8_experts(*args, dev(x), dev(ids), dev(p)))
+        for e, c in enumerate(cases):
+            rows = slice(e * each, (e + 1) * each)
+            want = y_ref[rows] if kept[e * each] else 0.0
+            assert np.array_equal(y[rows], np.broadcast_to(want, y[rows].shape)), (each, c, y[rows][0, 0], y_ref[rows][0, 0])
