@@ -398,7 +398,11 @@ int zinc_fp8_quantize(const void* x, int32_t type, int32_t rows, int32_t cols, i
  * K a multiple of 16 up to 65536, 1 <= N <= 2^20 (else ZINC_ERR_SHAPE); 0 <= M <= 2^24,
  * n_experts <= 1024 (else ZINC_ERR_ARG).  a, w, c and the workspace are 16-byte
  * aligned, the others 4.  The size queries return 0 where no workspace is needed
- * (workspace may then be NULL) and for arguments out of range.
+ * (workspace may then be NULL) and for arguments out of range.  zinc_gemm_fp8's size rises
+ * and falls with M (parts of K are kept only where there are few rows: for N = K = 4096 none
+ * at 4 rows, 12 MiB at 128, none from 512 on), so a workspace sized for one M is not enough for
+ * every smaller one; it never exceeds 16 MiB, which serve every product.  zinc_moe_gemm_fp8
+ * needs none at any size.
  */
 size_t zinc_gemm_fp8_workspace_size(int32_t M, int32_t N, int32_t K);
 int zinc_gemm_fp8(const void* a, const float* a_scales, const void* w, const float* w_scales, int32_t M, int32_t N,

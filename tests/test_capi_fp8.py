@@ -204,3 +204,16 @@ def test_workspaces_do_not_shrink_with_more_tokens(E, k, H, I):
             if 0 < m * k <= 1 << 24:
                 assert sizes(m) >= last, m
                 last = sizes(m)
+
+
+def test_dense_product_workspace_by_rows():
+    """What the header says of it: it rises and falls with M, and 16 MiB are always enough."""
+    sizes = {m: Z.gemm_fp8_workspace_size(m, 4096, 4096) for m in (4, 5, 128, 512, 8192)}
+    assert sizes[4] == 0 and 0 < sizes[5] < sizes[128] == 12 << 20 and sizes[512] == sizes[8192] == 0
+    assert gemm(M=128, N=4096, K=4096, ws=None) == -1 and gemm(M=128, N=4096, K=4096, wsb=sizes[128] - 1) == -4
+    for n in (1, 24, 127, 128, 129, 1000, 4096, 11008, 32300, 1 << 20):
+        for tiles in range(1, 520):
+            assert Z.gemm_fp8_workspace_size(64 * tiles, n, 65536) <= 16 << 20
+    # parts of K times tiles of 64 x 128 are at most 380 + tiles / 2, and two parts need fewer than 254 tiles
+    assert (380 + 253 / 2) * 64 * 128 * 4 < 16 << 20
+    assert all(Z.moe_gemm_fp8_workspace_size(m, 8, 4096, 4096) == 0 for m in (1, 5, 64, 128, 4096))
