@@ -675,21 +675,27 @@ def _current_raw_stream(index: int) -> int:
     return _torch()._C._cuda_getCurrentRawStream(index)
 
 
+def _size(query, *counts: int) -> int:
+    """A size query's answer; 0, as for every argument out of range, for counts past the C entry points' 32 bits."""
+    return query(*counts) if all(-1 << 31 <= n < 1 << 31 for n in counts) else 0
+
+
 def moe_sort_workspace_size(M: int, top_k: int, n_experts: int) -> int:
-    return int(lib.zinc_moe_sort_workspace_size(M, top_k, n_experts))
+    return _size(lib.zinc_moe_sort_workspace_size, M, top_k, n_experts)
 
 
 def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
-    return int(lib.zinc_gemm_fp8_workspace_size(M, N, K))
+    """Rises and falls with M; never above 16 MiB."""
+    return _size(lib.zinc_gemm_fp8_workspace_size, M, N, K)
 
 
 def moe_gemm_fp8_workspace_size(rows: int, n_experts: int, N: int, K: int) -> int:
-    return int(lib.zinc_moe_gemm_fp8_workspace_size(rows, n_experts, N, K))
+    return _size(lib.zinc_moe_gemm_fp8_workspace_size, rows, n_experts, N, K)
 
 
 def moe_fp8_workspace_size(M: int, top_k: int, n_experts: int, hidden: int, inter: int, dtype) -> int:
-    return int(lib.zinc_moe_fp8_experts_workspace_size(M, top_k, n_experts, hidden, inter,
-                                                       _type_code(dtype, "dtype")))
+    return _size(lib.zinc_moe_fp8_experts_workspace_size, M, top_k, n_experts, hidden, inter,
+                 _type_code(dtype, "dtype"))
 
 
 def _dev_error(dev_error) -> None:
@@ -714,7 +720,7 @@ def zinc_moe_sort(expert_ids, n_experts: int, offsets=None, slot_row=None, row_s
         if t is not None:
             _fits(t, torch.int32, shape, what)
     _dev_error(dev_error)
-    need = moe_sort_workspace_size(M, top_k, n_experts)
+    need = lib.zinc_moe_sort_workspace_size(M, top_k, n_experts)
     _workspace(workspace, need)
     c = _Call(stream, expert_ids, offsets, slot_row, row_slot, workspace, dev_error)
     offsets = c.empty((n_experts + 1,), torch.int32) if offsets is None else offsets
@@ -808,6 +814,8 @@ def zinc_fp8_quantize(x, block_rows: int = 1, q=None, scales=None, stream=None):
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     code, rows, cols = _rows_of(x, 16, "x")
+    if rows >= 1 << 31:
+        raise ValueError("x must have fewer than 2**31 rows")
     blocks = (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
     if q is not None:
         _fits(q, torch.float8_e4m3fn, (rows, cols), "q")
@@ -855,7 +863,7 @@ def zinc_gemm_fp8(a, a_scales, w, w_scales, out_dtype=None, out=None, workspace=
     code = _type_code(dtype, "out_dtype")
     if out is not None:
         _fits(out, dtype, (M, N), "out")
-    need = gemm_fp8_workspace_size(M, N, K)
+    need = lib.zinc_gemm_fp8_workspace_size(M, N, K)
     _workspace(workspace, need)
     c = _Call(stream, a, a_scales, w, w_scales, out, workspace)
     out = c.empty((M, N), dtype) if out is None else out
@@ -881,7 +889,7 @@ def zinc_moe_gemm_fp8(a, a_scales, w, w_scales, offsets, out_dtype=None, out=Non
     code = _type_code(dtype, "out_dtype")
     if out is not None:
         _fits(out, dtype, (M, N), "out")
-    need = moe_gemm_fp8_workspace_size(M, E, N, K)
+    need = lib.zinc_moe_gemm_fp8_workspace_size(M, E, N, K)
     _workspace(workspace, need)
     c = _Call(stream, a, a_scales, w, w_scales, offsets, out, workspace)
     out = c.empty((M, N), dtype) if out is None else out
@@ -914,7 +922,7 @@ def zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scal
     if y is not None:
         _fits(y, x.dtype, (M, hidden), "y")
     _dev_error(dev_error)
-    need = moe_fp8_workspace_size(M, top_k, E, hidden, inter, x.dtype)
+    need = lib.zinc_moe_fp8_experts_workspace_size(M, top_k, E, hidden, inter, code)
     _workspace(workspace, need)
     c = _Call(stream, w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, expert_ids, expert_weights, y,
               workspace, dev_error)

@@ -217,3 +217,20 @@ def test_dense_product_workspace_by_rows():
     # parts of K times tiles of 64 x 128 are at most 380 + tiles / 2, and two parts need fewer than 254 tiles
     assert (380 + 253 / 2) * 64 * 128 * 4 < 16 << 20
     assert all(Z.moe_gemm_fp8_workspace_size(m, 8, 4096, 4096) == 0 for m in (1, 5, 64, 128, 4096))
+
+
+def test_counts_past_32_bits_are_refused():
+    """The C entry points take 32-bit counts: a larger one must not arrive there as its low bits."""
+    rows = torch.empty((1 << 32) + 3, 16, dtype=torch.float16, device="meta")
+    with pytest.raises(ValueError, match="rows"):
+        Z.zinc_fp8_quantize(rows)
+    with pytest.raises(ValueError, match="rows"):
+        Z.zinc_fp8_quantize(torch.empty(1 << 31, 16, dtype=torch.float16, device="meta"), 128)
+    wide = 1 << 32
+    assert Z.gemm_fp8_workspace_size(64, 256, 4096) > 0
+    for m, n, k in ((64 + wide, 256, 4096), (64, 256 + wide, 4096), (64, 256, 4096 + wide), (64 - wide, 256, 4096)):
+        assert Z.gemm_fp8_workspace_size(m, n, k) == 0
+    assert Z.moe_sort_workspace_size(4096 + wide, 8, 64) == 0 and Z.moe_sort_workspace_size(4096, 8, 64 + wide) == 0
+    assert Z.moe_gemm_fp8_workspace_size(64, 8 + wide, 256, 256) == 0
+    assert Z.moe_fp8_workspace_size(16 + wide, 8, 64, 2048, 768, torch.float16) == 0
+    assert Z.moe_fp8_workspace_size(16, 8, 64, 2048, 768 + wide, torch.float16) == 0
