@@ -761,7 +761,7 @@ def zinc_moe_gather_fp8(x, slot_row, q=None, scales=None, stream=None):
     return q, scales
 
 
-def _combine(ys, slot_row, expert_weights, y, stream, what: str):
+def _combine(ys, slot_row, expert_weights, y, stream, what: str, what_y: str):
     torch = _torch()
     code, rows, hidden = _rows_of(ys, 8, what)
     M, top_k = _slot_rows(slot_row, None)
@@ -770,7 +770,7 @@ def _combine(ys, slot_row, expert_weights, y, stream, what: str):
     if expert_weights is not None:
         _fits(expert_weights, torch.float32, (M, top_k), "expert_weights")
     if y is not None:
-        _fits(y, ys.dtype, (M, hidden), "y")
+        _fits(y, ys.dtype, (M, hidden), what_y)
     c = _Call(stream, ys, slot_row, expert_weights, y)
     y = c.empty((M, hidden), ys.dtype) if y is None else y
     c.run("zinc_moe_combine", _ptr(ys), code, M, top_k, hidden, _ptr(slot_row), _ptr(expert_weights), _ptr(y))
@@ -779,12 +779,12 @@ def _combine(ys, slot_row, expert_weights, y, stream, what: str):
 
 def zinc_moe_combine(ys, slot_row, expert_weights, y=None, stream=None):
     """``y[t] = sum_s expert_weights[t, s] * ys[slot_row[t, s]]`` (``expert_weights`` None: the plain sum)."""
-    return _combine(ys, slot_row, expert_weights, y, stream, "ys")
+    return _combine(ys, slot_row, expert_weights, y, stream, "ys", "y")
 
 
 def zinc_moe_gather_backward(dxs, slot_row, dx=None, stream=None):
     """The gradient of zinc_moe_gather's x: ``dx[t] = sum_s dxs[slot_row[t, s]]``."""
-    return _combine(dxs, slot_row, None, dx, stream, "dxs")
+    return _combine(dxs, slot_row, None, dx, stream, "dxs", "dx, the combine's y")
 
 
 def zinc_moe_combine_backward(dy, ys, slot_row, expert_weights, dys=None, dweights=None, stream=None):

@@ -234,3 +234,9 @@ def test_counts_past_32_bits_are_refused():
     assert Z.moe_gemm_fp8_workspace_size(64, 8 + wide, 256, 256) == 0
     assert Z.moe_fp8_workspace_size(16 + wide, 8, 64, 2048, 768, torch.float16) == 0
     assert Z.moe_fp8_workspace_size(16, 8, 64, 2048, 768 + wide, torch.float16) == 0
+
+
+def test_gather_backward_names_dx():
+    for bad in (h2(8, 64), h2(4, 32), f4(4, 64)):
+        with pytest.raises(ValueError, match="^dx"):
+            Z.zinc_moe_gather_backward(h2(8, 64), i4(4, 2), dx=bad)
