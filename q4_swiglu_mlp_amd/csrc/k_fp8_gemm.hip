@@ -165,12 +165,10 @@ Cut cut_dense(int M, int N, int K) {
 // Grouped, by the mean rows of an expert (64 experts, 768 x 2048): 128 rows 43 with
 // small tiles, 46 with 128 x 128, 44 with 256 x 256; 192 rows 54, 52 and 66; 256 rows 61, 56
 // and 70; 384 rows 85, 80 and 76; 1024 rows 190, 164 and 142.
-Cut cut_grouped(int rows, int E) {
+Shape cut_grouped(int rows, int E) {
   const int mean = rows / E;
-  return {mean <= 160 ? kSmall : mean <= 320 ? kMiddle : kLargest, 1};
+  return mean <= 160 ? kSmall : mean <= 320 ? kMiddle : kLargest;
 }
-
-Cut cut(int M, int E, int N, int K) { return E ? cut_grouped(M, E) : cut_dense(M, N, K); }
 
 // Values from one part of K to the next, a multiple of eight.
 size_t part_values(int M, int N) { return ((size_t)M * N + 7) / 8 * 8; }
@@ -180,40 +178,51 @@ hipError_t small_tiles(const GemmArgs& g, int splits, hipStream_t stream) {
   return run_tiles<TileKernel<64, 128, 1, 4, EXACT, false, T>>(g, 64, splits, stream);
 }
 
+// Twice the operand registers leave the fp16 MFMAs the 128 x 256 tile.
 template <bool EXACT, typename T>
-hipError_t gemm(GemmArgs g, void* ws, hipStream_t stream) {
-  const Cut how = cut(g.M, g.offsets ? g.E : 0, g.N, g.K);
-  switch (how.shape) {
-    case kStream: {
-      // waves that share 16 columns, until there are 2048 of them or eight share
-      StreamArgs s{};
-      s.g = g;
-      const int tiles = (g.N + 15) / 16;
-      s.ks = tiles >= 2048 ? 1 : tiles >= 640 ? 2 : tiles >= 320 ? 4 : 8;
-      return run_stream<StreamKernel<8, 4, false, float, T>>(s, 8 / s.ks * 16, stream);
-    }
-    case kSmall: {
-      if (how.splits == 1) return small_tiles<EXACT, T>(g, 1, stream);
-      T* c = static_cast<T*>(g.c);
-      g.c = ws;
-      g.part = part_values(g.M, g.N);
-      const hipError_t e = small_tiles<EXACT, float>(g, how.splits, stream);
-      if (e != hipSuccess) return e;
-      const size_t total = (size_t)g.M * g.N, blocks = (total + 1023) / 1024;
-      hipLaunchKernelGGL(k_join_parts<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0,
-                         stream, static_cast<const float*>(ws), g.part, how.splits, total, c);
-      return hipGetLastError();
-    }
-    case kMiddle: return run_tiles<TileKernel<128, 128, 2, 2, EXACT, false, T>>(g, 128, 1, stream);
-    case kLarge: return run_tiles<TileKernel<128, 256, 2, 4, EXACT, false, T>>(g, 128, 1, stream);
-    case kLargest:
-      // twice the operand registers leave the fp16 MFMAs the 128 x 256 tile
-      if constexpr (EXACT)
-        return run_tiles<TileKernel<128, 256, 2, 4, true, false, T>>(g, 128, 1, stream);
-      else
-        return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 1, stream);
+hipError_t largest_tiles(const GemmArgs& g, hipStream_t stream) {
+  if constexpr (EXACT)
+    return run_tiles<TileKernel<128, 256, 2, 4, true, false, T>>(g, 128, 1, stream);
+  else
+    return run_tiles<TileKernel<256, 256, 2, 4, false, false, T>>(g, 256, 1, stream);
+}
+
+template <bool EXACT, typename T>
+hipError_t dense(GemmArgs g, void* ws, hipStream_t stream) {
+  const Cut how = cut_dense(g.M, g.N, g.K);
+  if (how.shape == kLargest) return largest_tiles<EXACT, T>(g, stream);
+  if (how.shape == kLarge) return run_tiles<TileKernel<128, 256, 2, 4, EXACT, false, T>>(g, 128, 1, stream);
+  if (how.shape == kStream) {
+    // waves that share 16 columns, until there are 2048 of them or eight share
+    StreamArgs s{};
+    s.g = g;
+    const int tiles = (g.N + 15) / 16;
+    s.ks = tiles >= 2048 ? 1 : tiles >= 640 ? 2 : tiles >= 320 ? 4 : 8;
+    return run_stream<StreamKernel<8, 4, false, float, T>>(s, 8 / s.ks * 16, stream);
   }
-  return hipErrorUnknown;
+  if (how.splits == 1) return small_tiles<EXACT, T>(g, 1, stream);
+  T* c = static_cast<T*>(g.c);
+  g.c = ws;
+  g.part = part_values(g.M, g.N);
+  const hipError_t e = small_tiles<EXACT, float>(g, how.splits, stream);
+  if (e != hipSuccess) return e;
+  const size_t total = (size_t)g.M * g.N, blocks = (total + 1023) / 1024;
+  hipLaunchKernelGGL(k_join_parts<T>, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream,
+                     static_cast<const float*>(ws), g.part, how.splits, total, c);
+  return hipGetLastError();
+}
+
+template <bool EXACT, typename T>
+hipError_t grouped(const GemmArgs& g, hipStream_t stream) {
+  const Shape shape = cut_grouped(g.M, g.E);
+  if (shape == kSmall) return small_tiles<EXACT, T>(g, 1, stream);
+  if (shape == kMiddle) return run_tiles<TileKernel<128, 128, 2, 2, EXACT, false, T>>(g, 128, 1, stream);
+  return largest_tiles<EXACT, T>(g, stream);
+}
+
+template <bool EXACT, typename T>
+hipError_t gemm(const GemmArgs& g, void* ws, hipStream_t stream) {
+  return g.offsets ? grouped<EXACT, T>(g, stream) : dense<EXACT, T>(g, ws, stream);
 }
 
 template <typename T_IN>
@@ -273,8 +282,8 @@ hipError_t launch_gemm_fp8(const void* a, const float* sa, const void* w, const 
 }
 
 size_t gemm_fp8_workspace_bytes(int M, int E, int N, int K) {
-  if (M == 0) return 0;
-  const Cut how = cut(M, E, N, K);
+  if (M == 0 || E) return 0;
+  const Cut how = cut_dense(M, N, K);
   return how.splits > 1 ? (size_t)how.splits * part_values(M, N) * sizeof(float) : 0;
 }
 
@@ -337,7 +346,7 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.K = I;
   g.c = pl.ys;
   if (e != hipSuccess) return e;
-  e = type == 1 ? gemm<false, float>(g, nullptr, stream) : gemm<true, float>(g, nullptr, stream);
+  e = type == 1 ? grouped<false, float>(g, stream) : grouped<true, float>(g, stream);
   if (e == hipSuccess) e = launch_moe_combine_rows(pl.ys, type, M, top_k, H, pl.slot_row, p, y, stream);
   return e;
 }
