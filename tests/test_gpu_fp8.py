@@ -812,3 +812,28 @@ def test_silu_far_from_zero_in_every_kernel():
             rows = slice(e * each, (e + 1) * each)
             want = y_ref[rows] if kept[e * each] else 0.0
             assert np.array_equal(y[rows], np.broadcast_to(want, y[rows].shape)), (each, c, y[rows][0, 0], y_ref[rows][0, 0])
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_16_bit_calls_repeat_bit_for_bit(kind):
+    """Every tile of the dense product, the grouped one, and the expert call: the same inputs, the same bits."""
+    rng = np.random.default_rng(31)
+    calls = []
+    for M, N, K in ((3, 512, 1040), (60, 512, 1040), (300, 20000, 272), (2100, 5200, 1040)):
+        (a, sa), (w, sw) = fp8_rows(rng, M, K), fp8_matrix(rng, N, K)
+        args = e4m3(a), dev(sa), e4m3(w), dev(sw), TYPES[kind][0]
+        calls.append(lambda args=args: Z.zinc_gemm_fp8(*args))
+    for counts in ([60, 0, 200], [300, 250], [900, 700]):
+        (a, sa), (w, sw) = fp8_rows(rng, sum(counts), 528), fp8_matrix(rng, len(counts), 1000, 528)
+        off = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+        args = e4m3(a), dev(sa), e4m3(w), dev(sw), off, TYPES[kind][0]
+        calls.append(lambda args=args: Z.zinc_moe_gemm_fp8(*args))
+    for M in (20, 100, 2600):
+        w, x, ids, p, _ = _layer(rng, M)
+        calls.append(lambda w=w, x=x.to(TYPES[kind][0]), ids=ids, p=p: Z.zinc_moe_fp8_experts(*w, x, ids, p))
+    first = [call() for call in calls]
+    for _ in range(4):
+        junk = torch.full((1 << 24,), float("nan"), device=DEV)
+        del junk
+        for call, want in zip(calls, first):
+            assert torch.equal(call(), want)
