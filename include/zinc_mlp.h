@@ -314,7 +314,8 @@ int zinc_moe_route_topk(const float* logits, int32_t M, int32_t n_experts, int32
  *   weights [n x k], the contraction dimension last: scales [ceil(n / 128) x
  *     ceil(k / 128)], one per 128 x 128 tile; experts' matrices and their scales
  *     lie back to back.
- * The last block of a dimension may be cut short.  Scales may be any fp32 values.
+ * The last block of a dimension may be cut short.  Scales may be any fp32 values; a product takes
+ * a_scale * w_scale in fp32, which loses bits below 2^-126 and is infinite from 2^128 on.
  */
 enum { ZINC_F16 = 0, ZINC_BF16 = 1, ZINC_F32 = 2 };
 
@@ -394,7 +395,8 @@ int zinc_fp8_quantize(const void* x, int32_t type, int32_t rows, int32_t cols, i
  * offsets[e] <= r < offsets[e + 1] takes expert e's (offsets int32 [n_experts + 1] on
  * the GPU, as zinc_moe_sort writes them; the host never reads them).  Rows outside
  * every range are left as they were; offsets are cut to [0, rows] and have to ascend.
- * The result is a function of the inputs alone, run after run.
+ * The result is a function of the inputs alone, run after run.  Which kernel takes a product goes
+ * by its sizes, so a row's last bits may change with the number of rows beside it.
  * K a multiple of 16 up to 65536, 1 <= N <= 2^20 (else ZINC_ERR_SHAPE); 0 <= M <= 2^24,
  * n_experts <= 1024 (else ZINC_ERR_ARG).  a, w, c and the workspace are 16-byte
  * aligned, the others 4.  The size queries return 0 where no workspace is needed

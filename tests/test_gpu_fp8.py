@@ -837,3 +837,24 @@ def test_16_bit_calls_repeat_bit_for_bit(kind):
         del junk
         for call, want in zip(calls, first):
             assert torch.equal(call(), want)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("M", [3, 40, 2000])
+@pytest.mark.parametrize("log_a,log_w", [(-126, 100), (110, -120), (-60, -66), (60, 67)])
+def test_gemm_with_scales_near_the_ends_of_fp32(kind, M, log_a, log_w):
+    """Scales far from 1, alone and as a product down to 2^-126 and up to 2^127: nothing is lost of the sum."""
+    rng = np.random.default_rng(32)
+    N, K = 200, 272
+    a, w = F.e4m3_encode(rng.choice([-1.5, 1.0, 1.25], (M, K))), F.e4m3_encode(rng.choice([-1.0, 1.75], (N, K)))
+    sa, sw = np.full((M, 3), 2.0 ** log_a, np.float32), np.full((2, 3), 2.0 ** log_w, np.float32)
+    if log_a + log_w == 127:
+        a[:, 1:], w[:, 1:] = 0, 0                                      # one term a sum: it stays below 2^129
+        a[:], w[:] = np.where(a == 0, a, F.e4m3_encode(0.5)), np.where(w == 0, w, F.e4m3_encode(0.5))
+    c = Z.zinc_gemm_fp8(e4m3(a), dev(sa), e4m3(w), dev(sw), TYPES[kind][0])
+    want = F.gemm(a, sa, w, sw)
+    if kind == "f16":
+        want = np.where(np.abs(want) > 65519, np.copysign(np.inf, want), want)
+        assert np.array_equal(np.isinf(host(c)), np.isinf(want))
+        want, c = np.nan_to_num(want, posinf=0, neginf=0), torch.nan_to_num(c, posinf=0, neginf=0)
+    close(c, want, product_slack(a, sa, w, sw, kind), kind, f"2^{log_a} 2^{log_w}")
