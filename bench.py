@@ -895,8 +895,9 @@ def decode_lines(args, torch, np, Z, S, dev, t):
 
 def fp8_lines(args, torch, np, Z, S, dev, t):
     """The expert layer of the MoE workload (64 experts, top-8, 2048 -> 768) on
-    block-scaled FP8 weights, two rotated expert sets, by tokens; then its operators one
-    by one at 4096 tokens, and the dense product at the headline layer's sizes."""
+    block-scaled FP8 weights, by tokens; then its operators one by one at 4096 tokens, and
+    the dense product at the headline layer's sizes.  Weights and rows are rotated past the
+    last-level cache."""
     out = []
     w = S.WORKLOADS["moe_e64"]
     E, k, H, I = w.n_experts, w.top_k, w.hidden, w.inter
@@ -923,38 +924,51 @@ def fp8_lines(args, torch, np, Z, S, dev, t):
         log(f"[bench] {out[-1]}")
 
     sets = [weight(I, H) + weight(I, H) + weight(H, I) for _ in range(2)]
-    for M in (1, 32, 512, 4096):
-        x = randn(M, H)
-        ids, p = Z.zinc_moe_route_topk(torch.randn((M, E), device=dev, generator=gen), k)
+    for M, dtype in ((1, torch.bfloat16), (32, torch.bfloat16), (512, torch.bfloat16), (4096, torch.bfloat16),
+                     (1, torch.float32), (512, torch.float32), (4096, torch.float32)):
+        x = randn(M, H).to(dtype)
+        # of few tokens' experts the last-level cache would hold every weight: other ones with each call
+        routes = [Z.zinc_moe_route_topk(torch.randn((M, E), device=dev, generator=gen), k) for _ in range(16)]
         ws = torch.empty(Z.moe_fp8_workspace_size(M, k, E, H, I, x.dtype), dtype=torch.uint8, device=dev)
         y = torch.empty_like(x)
-        timed(f"FP8 MoE E={E} top-{k}, {H}->{I}, M={M}, bf16, two rotated expert sets",
-              lambda i: Z.zinc_moe_fp8_experts(*sets[i % 2], x, ids, p, y=y, workspace=ws),
+        timed(f"FP8 MoE E={E} top-{k}, {H}->{I}, M={M}, {str(dtype)[6:]}, two rotated expert sets, 16 routings",
+              lambda i: Z.zinc_moe_fp8_experts(*sets[i % 2], x, *routes[i % 16], y=y, workspace=ws),
               tflops=6.0 * M * k * H * I)
+        del ws
+    # the steps, each on three rotated sets of rows (more than the last-level cache holds)
+    ids, p = routes[0]
     offsets, slot_row, _ = Z.zinc_moe_sort(ids, E)
     rows = M * k
-    xs = Z.zinc_moe_gather(x, slot_row)
-    dy = randn(M, H)
+    x = [randn(M, H) for _ in range(3)]
+    xs = [Z.zinc_moe_gather(v, slot_row) for v in x]
+    dys = [torch.empty_like(v) for v in xs]
+    q = [Z.zinc_moe_gather_fp8(v, slot_row) for v in x]
     timed(f"sort, M={M} top-{k} E={E}", lambda i: Z.zinc_moe_sort(ids, E))
-    timed(f"gather, bf16 {M} x {H}", lambda i: Z.zinc_moe_gather(x, slot_row), tb_s=2.0 * (M + rows) * H)
-    timed(f"FP8 gather, bf16 {M} x {H}", lambda i: Z.zinc_moe_gather_fp8(x, slot_row), tb_s=(2.0 * M + rows) * H)
-    timed(f"combine, bf16 {M} x {H}", lambda i: Z.zinc_moe_combine(xs, slot_row, p), tb_s=2.0 * (M + rows) * H)
-    timed(f"combine backward, bf16 {M} x {H}", lambda i: Z.zinc_moe_combine_backward(dy, xs, slot_row, p),
+    timed(f"gather, bf16 {M} x {H}", lambda i: Z.zinc_moe_gather(x[i % 3], slot_row, xs=dys[i % 3]),
+          tb_s=2.0 * (M + rows) * H)
+    timed(f"FP8 gather, bf16 {M} x {H}",
+          lambda i: Z.zinc_moe_gather_fp8(x[i % 3], slot_row, q=q[i % 3][0], scales=q[i % 3][1]),
+          tb_s=(2.0 * M + rows) * H)
+    timed(f"combine, bf16 {M} x {H}", lambda i: Z.zinc_moe_combine(xs[i % 3], slot_row, p),
+          tb_s=2.0 * (M + rows) * H)
+    timed(f"combine backward, bf16 {M} x {H}",
+          lambda i: Z.zinc_moe_combine_backward(x[i % 3], xs[i % 3], slot_row, p, dys=dys[i % 3]),
           tb_s=2.0 * (M + 2 * rows) * H)
-    xq, xsc = Z.zinc_moe_gather_fp8(x, slot_row)
-    timed(f"grouped product, {rows} rows, {I} x {H}, bf16",
-          lambda i: Z.zinc_moe_gemm_fp8(xq, xsc, sets[i % 2][0], sets[i % 2][1], offsets, torch.bfloat16),
-          tflops=2.0 * rows * I * H)
-    del sets, xs, xq
+    for dtype in (torch.bfloat16, torch.float32):
+        timed(f"grouped product, {rows} rows, {I} x {H}, {str(dtype)[6:]} output",
+              lambda i: Z.zinc_moe_gemm_fp8(*q[i % 3], sets[i % 2][0], sets[i % 2][1], offsets, dtype),
+              tflops=2.0 * rows * I * H)
+    del sets, xs, dys, q
+    # dense: 12 rotated weights, 540 MB, as the layers of a model pass by
     N, K = 11008, 4096
-    big = randn(N, K) / K ** 0.5
-    timed(f"quantise {N} x {K}, 128 x 128 blocks", lambda i: Z.zinc_fp8_quantize(big, 128), tb_s=3.0 * N * K)
-    wq, wsc = Z.zinc_fp8_quantize(big, 128)
+    big = [randn(N, K) / K ** 0.5 for _ in range(4)]
+    timed(f"quantise {N} x {K}, 128 x 128 blocks", lambda i: Z.zinc_fp8_quantize(big[i % 4], 128), tb_s=3.0 * N * K)
+    weights = [Z.zinc_fp8_quantize(big[i % 4], 128) for i in range(12)]
     for M in (1, 64, 1024, 8192):
         a, sa = Z.zinc_fp8_quantize(randn(M, K), 1)
         for dtype in (torch.bfloat16, torch.float32):
-            timed(f"product {M} x {N} x {K}, {str(dtype)[6:]} output",
-                  lambda i: Z.zinc_gemm_fp8(a, sa, wq, wsc, dtype), tflops=2.0 * M * N * K)
+            timed(f"product {M} x {N} x {K}, {str(dtype)[6:]} output, 12 rotated weights",
+                  lambda i: Z.zinc_gemm_fp8(a, sa, *weights[i % 12], dtype), tflops=2.0 * M * N * K)
     return out
 
 
