@@ -13,8 +13,9 @@
 // - The products run on the fp16 MFMA (16x16x32) after exact conversion: the
 //   matrix rate does not matter here, and its sums lose nothing.
 //
-// Bound by the stream: one row of 11008 x 4096 11.8 us (3.8 TB/s; a large copy moves 5.2),
-// gate and up of 32 tokens, top-8 of 64 experts, 2048 -> 768, 44 us (4.6 TB/s).
+// Bound by the stream, from HBM: one row of 11008 x 4096 12.5 us (3.6 TB/s; a large copy moves 5.2;
+// 11.7 us where the last-level cache holds w), gate and up of 32 tokens, top-8 of 64 experts,
+// 2048 -> 768, 44.6 us (4.5 TB/s).
 #pragma once
 
 #include "fp8_tile.hpp"

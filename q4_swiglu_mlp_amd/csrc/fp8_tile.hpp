@@ -165,7 +165,8 @@ __device__ __forceinline__ const __attribute__((address_space(4))) float* unifor
 // output is silu(gate) up quantised to e4m3 (one block of 128 columns a tile).
 //
 // What bounds it, on random data: with FP8 MFMAs the power limit (8192 x 11008 x 4096
-// 331 us, 2230 TFLOP/s at about 1.9 GHz; the MFMAs alone reach 3900 with their four FMAs).
+// 330 us, 2240 TFLOP/s at about 1.9 GHz, on one weight again and again, 379 us with weights that
+// come from HBM; the MFMAs alone reach 3900 with their four FMAs).
 // With fp16 MFMAs 1230 TFLOP/s for 8192^2 x 4096 (16-bit stores), the rate of a large bf16 library product
 // (1210): they are busy 53 % of the cycles, and with fewer vector instructions, no
 // copies' latency or other orders the time stays within 3 % while the clock moves against it.
@@ -191,8 +192,8 @@ struct TileKernel {
   // expert layer's rows, read again soon.
   static constexpr bool STREAMED = sizeof(T) == 2;
   // Buffers: with three, the copies of two blocks are in flight; where one workgroup fits a
-  // CU either way.  Experts of 256 / 512 tokens, top-8 of 64, 105.5 us / 123.5 against 109 /
-  // 127.5 with two, 4001 tokens the same, 32000 fp32 rows of 2048 x 768 150 against 160.
+  // CU either way.  Within 1.5 % of two for the experts, top-8 of 64 (256 tokens 103.8 us against 105,
+  // 512 130 both, 4001 414 against 409); 32000 fp32 rows of 2048 x 768 148 - 151 against 148 - 158.
   // 256 x 256 has no room for a third, the small tiles fill LDS with more workgroups.
   static constexpr int NBUF = TN == 256 && TM <= 128 ? 3 : 2;
   static constexpr int BAND = 8;                    // row tiles walked per column

@@ -15,16 +15,17 @@
 // below 2^-6 of a group's largest lose any: measured 1.5e-5 of the result
 // (2-norm, normal data, K = 128), far below the rounding of a 16-bit output (2e-4
 // fp16, 1.7e-3 bf16).  fp32 outputs (the expert rows of an fp16 or fp32 layer too; a bf16
-// layer's take the FP8 MFMA) and the products that feed an expert layer's second quantisation take the fp16 MFMA on exactly
-// converted operands instead: half the rate, 7e-9 of the result.  In that quantisation
-// 1.5e-5 moves a value in 5000 to the next code, which is 1.2e-3 of y beside the
-// 2e-4 and 1.7e-3 of its own rounding (measured for bf16: 3.3e-3 in all against 1.7e-3).
+// layer's take the FP8 MFMA) and the products that feed an expert layer's second
+// quantisation take the fp16 MFMA on exactly converted operands instead: half the rate, 7e-9
+// of the result.  In that quantisation 1.5e-5 moves a value in 5000 to the next code, which is
+// 1.2e-3 of y beside the 2e-4 and 1.7e-3 of its own rounding (a bf16 layer of 4001 tokens has
+// 1.7e-3 in all, as in plain fp32; with the FP8 MFMA there, and 16-bit expert rows, 3.3e-3).
 //
 // What bounds it (TB/s and TFLOP/s of the whole call):
-// - few rows, the pass over w: 1 x 11008 x 4096 11 us, 4.1 TB/s;
+// - few rows, the pass over w: 1 x 11008 x 4096 12.7 us, 3.6 TB/s, with w in HBM;
 // - many rows, the matrix units at the clock that the power limit leaves (about 1.9 GHz):
-//   8192 x 11008 x 4096 bf16 331 us, 2230 TFLOP/s (345 us on another card); fp32 by
-//   fp16 MFMAs 490 us for 8192 x 8192 x 4096, 1120 TFLOP/s.
+//   8192 x 11008 x 4096 bf16 330 us, 2240 TFLOP/s, 379 us with weights that come from HBM
+//   (up to 5 % more on other cards); fp32 by fp16 MFMAs 480 us for 8192 x 8192 x 4096, 1145 TFLOP/s.
 #include <atomic>
 
 #include "fp8_stream.hpp"
@@ -128,7 +129,8 @@ __global__ __launch_bounds__(256) void k_join_parts(const float* __restrict__ pa
   }
 }
 
-// How a product is cut, by its sizes alone.  Times: us, 256 CUs, bf16 output, calls replayed.
+// How a product is cut, by its sizes alone.  Times: us, 256 CUs, bf16 output, calls replayed; on one
+// weight, which the last-level cache holds, where nothing else is said.
 enum Shape { kStream, kSmall, kMiddle, kLarge, kLargest };
 struct Cut {
   Shape shape;
@@ -138,7 +140,9 @@ struct Cut {
 // Dense.
 // - Up to 4 rows the weight's stream: 11008 x 4096 12.1 against 12.8 for the best parts of
 //   small tiles, 4096 x 11008 14.7 and 15.2, 4096 x 4096 7.8 and 9.9; with 8 rows 13.3
-//   and 12.9, 18.2 and 15.3, 9.3 and 10.1; with 16 rows 16.1 and 13.2, 24 and 15.6.
+//   and 12.9, 18.2 and 15.3, 9.3 and 10.1; with 16 rows 16.1 and 13.2, 24 and 15.6.  Weights
+//   from HBM: 14.2 and 16.0, 18.0 and 18.4, 8.8 and 12.0; 8 rows 15.3 and 16.2, 20.8 and
+//   18.3, 9.9 and 12.1; 16 rows 17.7 and 16.6, 26.5 and 18.6, 12.5 and 12.4.
 // - Else the largest tile (256 x 256, 128 x 256) with 160 units, five eighths of the CUs:
 //   1024 x 11008 x 4096 53 with the first (172 units) against 74 with small tiles, 512 rows
 //   35 with the second against 49 and 39, 2048 x 4096 x 11008 (128 and 256 units) 95 with
@@ -162,9 +166,13 @@ Cut cut_dense(int M, int N, int K) {
   return {kSmall, (KB + each - 1) / each};   // no part is empty
 }
 
-// Grouped, by the mean rows of an expert (64 experts, 768 x 2048): 128 rows 43 with
-// small tiles, 46 with 128 x 128, 44 with 256 x 256; 192 rows 54, 52 and 66; 256 rows 61, 56
-// and 70; 384 rows 85, 80 and 76; 1024 rows 190, 164 and 142.
+// Grouped, by the mean rows of an expert.  64 experts of uneven sizes, 768 x 2048: 128 rows 43
+// with small tiles, 46 with 128 x 128, 44 with 256 x 256; 192 rows 54, 52 and 66; 256 rows 61,
+// 56 and 70; 384 rows 85, 80 and 76; 1024 rows 190, 164 and 142.  Where the sizes are even, an
+// expert below 256 rows fills one tile of 256, which the mean cannot tell: 64 x 768 x 2048, 192 rows
+// 51, 47 and 39, 256 rows 61, 59 and 73; 16 x 1536 x 4096, 192 rows 55, 52 and 66, 256 rows 72, 58
+// and 71, 384 rows 81, 88 and 67; 128 x 512 x 2048, 192 rows 63, 55 and 47, 256 rows 78, 71 and 78;
+// 8 x 14336 x 4096, 128 rows 183, 173 and 139, 256 rows 243, 248 and 209.
 Shape cut_grouped(int rows, int E) {
   const int mean = rows / E;
   return mean <= 160 ? kSmall : mean <= 320 ? kMiddle : kLargest;
@@ -193,7 +201,10 @@ hipError_t dense(GemmArgs g, void* ws, hipStream_t stream) {
   if (how.shape == kLargest) return largest_tiles<EXACT, T>(g, stream);
   if (how.shape == kLarge) return run_tiles<TileKernel<128, 256, 2, 4, EXACT, false, T>>(g, 128, 1, stream);
   if (how.shape == kStream) {
-    // waves that share 16 columns, until there are 2048 of them or eight share
+    // ks waves share 16 columns: as many as make 1280 waves, eight at most; one alone from 2048 on.
+    // Weights from HBM, one row, K = 4096: N = 4096 8.1 us with eight, 8.7 with four, 11.5 with two;
+    // 6144 10.7, 9.5 and 11.8; 11008 15.0 with four, 13.9 with two, 20.0 with one; 16384 19.9, 18.1 and
+    // 20.9; 22016 24.7 with two, 23.5 with one; 32768 31.3 and 36.3 (four rows 34.2 and 35.8)
     StreamArgs s{};
     s.g = g;
     const int tiles = (g.N + 15) / 16;
@@ -314,12 +325,14 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
   g.c = pl.hq;
   g.cs = pl.hs;
   if (e != hipSuccess) return e;
-  // The gate and up products, by the mean rows of an expert (64 experts, top-8, 2048 to
-  // 768, ids at random; us of the whole call).  While no expert has more than 16 rows the
-  // weights stream past tokens that are quantised on the way: mean 8 84 against 95 with tiles
-  // of 64 rows, 13 92 against 98, 14 101 against 98.  Tiles of 64 rows where they
-  // hold any expert: mean 16 99 against 110 with tiles of 128 rows, 42 104 against 117,
-  // 44 118 and 119, 64 132 against 125.
+  // The gate and up products, by the mean rows of an expert (us of the whole call, bf16, experts
+  // hit evenly, weights from HBM).  While no expert has more than 16 rows the weights stream past
+  // tokens that are quantised on the way; then tiles of 64 rows while they hold any expert.
+  //   64 experts, top-8, 2048 to 768: mean 13 82 with the stream, 91 with 64 rows, 100 with 128;
+  //     20 103, 94 and 102; 44 102 with 64 rows, 111 with 128; 64 129 and 121
+  //   16, top-2, 4096 to 1536: 13 84, 87 and 93; 20 116, 89 and 95; 44 98 and 102; 64 142 and 110
+  //   128, top-8, 2048 to 512: 8 96, 101 and 108; 13 111, 106 and 112; 44 129 and 134; 64 157 and 151
+  //   8, top-2, 4096 to 14336: 8 314, 314 and 334; 13 324, 316 and 337; 44 327 and 347; 64 425 and 389
   const int mean = S / E;
   if (mean <= 13) {
     StreamArgs s{};

@@ -3,9 +3,11 @@
 // places an expert sort gives them (the FP8 gather).
 //
 // Bound by HBM: one read of x, one write of q.  A row's block is 16 lanes of
-// eight values, so its maximum is four DPP steps and x is read once.  Measured, bf16:
-// 11008 x 4096 by tiles 24 us, rows of 8192 x 4096 18 us, 4096 x 2048 to eight places
-// each 15 us, all 5.5 TB/s; a few rows cost a launch, 2.3 us.
+// eight values, so its maximum is four DPP steps and x is read once.  Measured, bf16, input and
+// output in HBM: 11008 x 4096 by tiles 29 us into a fresh output, 32.6 over outputs in turn (4.2 TB/s;
+// a large copy 5.2), rows of 8192 x 4096 23 us (4.4), 4096 x 2048 to eight places each 17.3 us (4.9).
+// On the tensors of the call before, in the last-level cache: 24, 18 and 15 us.  A few rows cost a
+// launch, 2.3 us.
 #include "fp8_device.hpp"
 #include "launch.hpp"
 

@@ -5,7 +5,7 @@
 // slot of a smaller expert and behind the earlier slots of its own, so the
 // order, and with it every later sum, is a function of the ids alone (no
 // atomic decides a place).  It is bound by its launches and the latency of its few steps:
-// 64 experts, 512 slots 3 us, 32768 slots 8.5 us in two launches (floor 0.1 us by bytes).
+// 64 experts, 512 slots 3.3 us, 32768 slots 7.7 us in two launches (floor 0.1 us by bytes).
 #include "fp8_device.hpp"
 #include "launch.hpp"
 
@@ -221,8 +221,9 @@ __global__ void k_sort_empty(int E, int32_t* __restrict__ offsets) {
 }
 
 // xs[slot_row[t, s]] = x[t]: a thread carries 16 bytes of one token's row to
-// its top_k places, so x is read once.  Bound by the stores: 4096 x 2048 bf16 to eight
-// places each 23.5 us, 6.4 TB/s (a large copy: 5.2).
+// its top_k places, so x is read once.  Bound by HBM, the stores: 4096 x 2048 bf16 to eight
+// places each 29 us, 5.2 TB/s, a large copy's rate (23.5 us into a tensor that the last-level cache
+// still holds).
 __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ x, int pieces, int M, int top_k,
                                                 const int32_t* __restrict__ slot_row, uint4* __restrict__ xs) {
   const int c = (int)blockIdx.y * 256 + (int)threadIdx.x, n_rows = M * top_k;
@@ -241,8 +242,9 @@ __global__ __launch_bounds__(256) void k_gather(const uint4* __restrict__ x, int
 }
 
 // y[t] = sum_s p[t, s] ys[slot_row[t, s]] in fp32, in the order of s; eight slots' rows
-// are in flight at a time.  Bound by the rows' reads: 4096 x 2048 bf16, eight slots,
-// 23 us, 6.5 TB/s.
+// are in flight at a time.  Bound by the rows' reads from HBM: 4096 x 2048 bf16, eight slots, 30 us,
+// 5.1 TB/s (23 us where the last-level cache holds the rows; an expert call's fp32 rows, just written,
+// 46 us, 6.1 TB/s).
 template <typename T_IN, typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_combine(const T_IN* __restrict__ ys, int H, int M, int top_k,
                                                  const int32_t* __restrict__ slot_row, const float* __restrict__ p,
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(256) void k_combine(const T_IN* __restrict__ ys, in
 
 // One wave per slot: dys[row] = p dy[t], dp = <dy[t], ys[row]>, so a token's dy is
 // read once a slot, from the caches after the first.  Bound by HBM: 4096 x 2048 bf16,
-// eight slots, 50 us, 5.7 TB/s.
+// eight slots, 57 us, 5.0 TB/s (50 us on the same rows again).
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_backward(const T* __restrict__ dy, const T* __restrict__ ys, int H,
                                                           int S, int top_k, const int32_t* __restrict__ slot_row,
