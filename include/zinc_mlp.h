@@ -306,6 +306,7 @@ int zinc_moe_route_topk(const float* logits, int32_t M, int32_t n_experts, int32
  *
  * Element types: ZINC_F16, ZINC_BF16, ZINC_F32 name the type of the activations
  * (and of outputs) a call reads and writes; every other value -> ZINC_ERR_ARG.
+ * No output of these calls may overlap an input, another output or the workspace.
  *
  * FP8 values are e4m3 bytes (OCP: bias 7, largest value 448, 0x7F / 0xFF NaN),
  * with one fp32 scale per block of 128; a value stands for q * scale:

@@ -858,3 +858,83 @@ def test_gemm_with_scales_near_the_ends_of_fp32(kind, M, log_a, log_w):
         assert np.array_equal(np.isinf(host(c)), np.isinf(want))
         want, c = np.nan_to_num(want, posinf=0, neginf=0), torch.nan_to_num(c, posinf=0, neginf=0)
     close(c, want, product_slack(a, sa, w, sw, kind), kind, f"2^{log_a} 2^{log_w}")
+
+
+# ---------------------------------------------------------------- the ends of what the calls allow
+@pytest.mark.parametrize("M", [3, 60, 300])
+def test_experts_without_a_valid_id(M):
+    w, x, ids, p, (E, H, I, k) = _layer(np.random.default_rng(33), M)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = torch.full_like(x, 5.0)
+    Z.zinc_moe_fp8_experts(*w, x, torch.where(ids % 2 == 0, E, -1 - ids), p, y=y, dev_error=err)
+    assert not y.any() and int(err) == 1
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [40, 200, 700])
+def test_experts_all_tokens_on_one_expert(kind, M):
+    """The kernel is chosen by the mean over eight experts: 5, 25 and 87 rows, where one holds all of them."""
+    run_experts(np.random.default_rng(34 + M), 8, 256, 256, M, 1, kind, np.full((M, 1), 2, np.int32))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_row_calls_at_the_widest(kind):
+    rng = np.random.default_rng(35)
+    M, k, H = 3, 2, 65536
+    slot_row = dev(np.array([[5, 0], [2, -1], [1, 3]], np.int32))
+    x, ys = activations(rng, M, H, kind), activations(rng, M * k, H, kind)
+    p = dev(rng.uniform(size=(M, k)).astype(np.float32))
+    xs = Z.zinc_moe_gather(x, slot_row, xs=torch.zeros_like(ys))
+    assert torch.equal(xs[[5, 0, 2, 1, 3, 4]], torch.stack([x[0], x[0], x[1], x[2], x[2], torch.zeros_like(x[0])]))
+    q, s = Z.zinc_moe_gather_fp8(x, slot_row)
+    q1, s1 = Z.zinc_fp8_quantize(x)
+    q2, s2 = F.quantize(host(x))
+    assert np.array_equal(codes(q1), q2) and np.array_equal(host(s1), s2)
+    for t, row in ((0, 5), (0, 0), (1, 2), (2, 1), (2, 3)):
+        assert np.array_equal(codes(q[row]), q2[t]) and np.array_equal(host(s[row]), s2[t])
+    y = Z.zinc_moe_combine(ys, slot_row, p)
+    sr, pn = host(slot_row), host(p)
+    size = F.combine(np.abs(host(ys)), sr, pn)
+    close(y, F.combine(host(ys), sr, pn), (k + 1) * 2.0 ** -24 * size, kind, "combine")
+    dys, dp = Z.zinc_moe_combine_backward(x, ys, slot_row, p, dys=torch.zeros_like(ys))
+    want, dp_want = F.combine_backward(host(x), host(ys), sr, pn, np.zeros((M * k, H)))
+    _, dp_size = F.combine_backward(np.abs(host(x)), np.abs(host(ys)), sr, pn, np.zeros((M * k, H)))
+    close(dys, want, 2.0 ** -24 * np.abs(want), kind, "dys")
+    close(dp, dp_want, (H + 1) * 2.0 ** -24 * dp_size, "f32", "dweights")
+
+
+@pytest.mark.parametrize("M,k,E", [(1 << 21, 8, 64), (1 << 14, 1024, 1024)])
+def test_sort_of_the_most_slots(M, k, E):
+    g = torch.Generator(device=DEV).manual_seed(36)
+    ids = torch.randint(-1, E, (M, k), dtype=torch.int32, device=DEV, generator=g)
+    off, slot_row, row_slot = Z.zinc_moe_sort(ids, E)
+    flat = ids.reshape(-1).long()
+    counts = torch.bincount(flat + 1, minlength=E + 1)
+    assert torch.equal(off[1:].long(), counts[1:].cumsum(0)) and int(off[0]) == 0
+    valid = int(off[E])
+    # ordered by expert and slot, every valid slot once, -1 behind
+    rows = row_slot[:valid].long()
+    key = flat[rows] * (M * k) + rows
+    assert bool((key[1:] > key[:-1]).all()) and bool((flat[rows] >= 0).all()) and bool((row_slot[valid:] == -1).all())
+    back = torch.full((M * k,), -1, dtype=torch.int32, device=DEV)
+    back[rows] = torch.arange(valid, dtype=torch.int32, device=DEV)
+    assert torch.equal(back, slot_row.reshape(-1))
+
+
+def test_expert_rows_past_32_bits():
+    """Expert rows and activations behind 2^32 bytes: the last tokens' y is that of a call with them alone, whose mean
+    takes the same kernels."""
+    M, E, H, I, tail = 66000, 2, 16384, 128, 1400
+    assert M * H * 4 > 1 << 32
+    rng = np.random.default_rng(37)
+    w = [v for c, s in (fp8_matrix(rng, E, I, H), fp8_matrix(rng, E, I, H), fp8_matrix(rng, E, H, I))
+         for v in (e4m3(c), dev(s * np.float32(0.3)))]
+    g = torch.Generator(device=DEV).manual_seed(38)
+    x = torch.randn((M, H), device=DEV, generator=g).half()
+    ids = (torch.arange(M, device=DEV, dtype=torch.int32) % E)[:, None].contiguous()
+    p = torch.rand((M, 1), device=DEV, generator=g)
+    y = Z.zinc_moe_fp8_experts(*w, x, ids, p)
+    last = slice(M - tail, M)
+    assert torch.equal(y[last], Z.zinc_moe_fp8_experts(*w, x[last].contiguous(), ids[last].contiguous(),
+                                                       p[last].contiguous()))
+    assert bool(y[last].any())
