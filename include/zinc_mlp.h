@@ -439,12 +439,88 @@ int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const voi
                          size_t workspace_bytes, int32_t* dev_error, void* stream);
 
 /*
+ * The expert layer in 16 bits, for training: the products between zinc_moe_gather and
+ * zinc_moe_combine with their gradients, and SwiGLU between them.
+ *
+ * Product by expert, of ZINC_F16 or ZINC_BF16 operands (`type`): row r of a [rows x K] with
+ * offsets[e] <= r < offsets[e + 1] takes expert e's w [N x K] of n_experts back to back:
+ *   c[r][n] = sum_k a[r][k] w_e[n][k]                                  c [rows x N]
+ * _backward, from dc [rows x N]:
+ *   da[r][k] = sum_n dc[r][n] w_e[n][k]                               da [rows x K]
+ *   dw_e[n][k] = sum_r dc[r][n] a[r][k] over the rows of e            dw [n_experts x N x K]
+ * accumulated in fp32 and rounded once to c's (da's, dw's) type: the operands' or ZINC_F32.  offsets:
+ * int32 [n_experts + 1] on the GPU, as zinc_moe_sort writes them (a dense product: one expert, offsets
+ * 0 and rows); the host never reads them.  Rows outside every range are left as they were, and add to
+ * no dw; offsets are cut to [0, rows] and have to ascend.  dw of an expert without rows is zeros (also
+ * where rows is 0, which needs no other input).  da or dw may be NULL: it is then not computed, and w
+ * (a) not read.  The result is a function of the inputs alone, run after run; which kernel takes a
+ * product goes by its sizes, so a row's last bits may change with the number of rows beside it.
+ * N and K: multiples of 8 up to 65536 (else ZINC_ERR_SHAPE); rows <= 2^24, n_experts <= 1024, types as above
+ * (else ZINC_ERR_ARG).  Matrices and the workspace are 16-byte aligned, offsets 4.  The size queries
+ * return 0 where no workspace is needed (workspace may then be NULL) and for arguments out of range.
+ * No output of these calls, of SwiGLU's or the adapters' may overlap an input, another output or the
+ * workspace, but for y (dx) in the place of base.
+ */
+size_t zinc_moe_gemm_workspace_size(int32_t rows, int32_t n_experts, int32_t N, int32_t K);
+int zinc_moe_gemm(const void* a, const void* w, int32_t type, const int32_t* offsets, int32_t n_experts, int32_t rows,
+                  int32_t N, int32_t K, int32_t out_type, void* c, void* workspace, size_t workspace_bytes,
+                  void* stream);
+size_t zinc_moe_gemm_backward_workspace_size(int32_t rows, int32_t n_experts, int32_t N, int32_t K);
+int zinc_moe_gemm_backward(const void* dc, const void* a, const void* w, int32_t type, const int32_t* offsets,
+                           int32_t n_experts, int32_t rows, int32_t N, int32_t K, int32_t da_type, void* da,
+                           int32_t dw_type, void* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * SwiGLU of rows [rows x cols], and its gradients:
+ *   h = silu(gate) up;   dgate = dh up s (1 + gate (1 - s)),  dup = dh gate s,   s = 1 / (1 + e^-gate)
+ * in fp32 and rounded once to `type` (ZINC_F16, ZINC_BF16 or ZINC_F32), which every array has.
+ * Infinite gates give NaN where the formula does (-inf, and dgate of both).  cols a multiple of 8 up to 65536
+ * (else ZINC_ERR_SHAPE), rows <= 2^24 (else ZINC_ERR_ARG), all arrays 16-byte aligned.  No workspace.
+ */
+int zinc_swiglu(const void* gate, const void* up, int32_t type, int32_t rows, int32_t cols, void* h, void* stream);
+int zinc_swiglu_backward(const void* dh, const void* gate, const void* up, int32_t type, int32_t rows, int32_t cols,
+                         void* dgate, void* dup, void* stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they share:
+ *   y[m] = base[m] + scales[e] B_e (A_e x[m])         e: row m's adapter
+ * x [M x K], base and y [M x N], a [n_adapters x rank x K], b [n_adapters x N x rank] of `type` (ZINC_F16
+ * or ZINC_BF16); scales fp32 [n_adapters] (NULL: ones).  base is the shared projection's output; it
+ * may be y itself (in place), or NULL (zeros).  The plan is zinc_moe_sort's of the rows' adapter
+ * ids [M x 1] with n_experts = n_adapters: offsets [n_adapters + 1], slot_row [M] and row_slot [M] on
+ * the GPU; it serves every projection of a batch.  Rows whose id is outside [0, n_adapters) have no adapter:
+ * y[m] = base[m] (in place they are not touched).  Adapters of smaller rank have rows of zeros in a
+ * and columns of zeros in b.
+ * _backward, from dy [M x N], with dh[m] = B_e^T dy[m]:
+ *   dx[m] = base[m] + scales[e] A_e^T dh[m]           base: the projection's own gradient of x
+ *   da_e = scales[e] sum_m dh[m] x[m]^T,   db_e = scales[e] sum_m dy[m] (A_e x[m])^T     over the rows of e
+ * (zeros for an adapter without rows, also where M is 0).  The gradient of base is dy itself.  dx, da or db
+ * may be NULL: it is then not computed.
+ * A x and dh are kept in fp32; where they are operands again they are split in two 16-bit terms (16
+ * bits of a value in bf16, 21 in fp16), sums are fp32 and results are rounded once.  Nothing depends on the
+ * order of the GPU's work: equal inputs give equal bits.
+ * K and N: multiples of 8 up to 65536, rank a multiple of 8 up to 256 (else ZINC_ERR_SHAPE); M <= 2^24,
+ * n_adapters <= 1024 (else ZINC_ERR_ARG).  Matrices and the workspace are 16-byte aligned, scales and the
+ * plan 4.  The workspace sizes are non-decreasing in M.
+ */
+size_t zinc_lora_workspace_size(int32_t M, int32_t n_adapters, int32_t K, int32_t N, int32_t rank);
+int zinc_lora(const void* x, int32_t type, int32_t M, int32_t K, const void* a, const void* b, int32_t rank,
+              int32_t n_adapters, int32_t N, const float* scales, const int32_t* offsets, const int32_t* slot_row,
+              const int32_t* row_slot, const void* base, void* y, void* workspace, size_t workspace_bytes,
+              void* stream);
+size_t zinc_lora_backward_workspace_size(int32_t M, int32_t n_adapters, int32_t K, int32_t N, int32_t rank);
+int zinc_lora_backward(const void* dy, const void* x, int32_t type, int32_t M, int32_t K, const void* a, const void* b,
+                       int32_t rank, int32_t n_adapters, int32_t N, const float* scales, const int32_t* offsets,
+                       const int32_t* slot_row, const int32_t* row_slot, const void* base, void* dx, void* da, void* db,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Kernel timing for benchmarks and profiles (off by default; not needed for
  * correct use).  After zinc_timing_enable(capacity), every prefill, decode and
  * MoE call records a HIP event pair on its stream immediately around its main
  * kernel -- the fused unit kernel for prefill and MoE; for decode, one pair
- * around the gate/up matvec and one around the down matvec; for an FP8 product one around
- * its main kernel, for the FP8 experts one around the gate/up and one around the down
+ * around the gate/up matvec and one around the down matvec; for an FP8 or 16-bit product one around
+ * its main kernel (two with both gradients), for the FP8 experts one around the gate/up and one around the down
  * product -- for up to `capacity` pairs.  The events are recorded without a system-scope fence
  * (hipEventDisableSystemFence), so they add no cache write-back of their own
  * to the work they bracket.  zinc_timing_collect() waits for the recorded events,

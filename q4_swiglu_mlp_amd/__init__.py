@@ -28,6 +28,13 @@ The FP8 expert layer (float16, bfloat16 or float32 activations; FP8 tensors are
 * ``zinc_gemm_fp8(a, a_scales, w, w_scales)``, ``zinc_moe_gemm_fp8(a, a_scales, w, w_scales, offsets)`` -> c
 * ``zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scales, x, ids, p)`` -> y
 
+The expert layer in 16 bits, for training, and low-rank adapters beside a projection:
+
+* ``zinc_moe_gemm(a, w, offsets)`` -> c, ``zinc_moe_gemm_backward(dc, a, w, offsets)`` -> (da, dw)
+* ``zinc_swiglu(gate, up)`` -> h, ``zinc_swiglu_backward(dh, gate, up)`` -> (dgate, dup)
+* ``zinc_lora(x, a, b, scales, offsets, slot_row, row_slot, base)`` -> y,
+  ``zinc_lora_backward(dy, x, a, b, scales, offsets, slot_row, row_slot, base)`` -> (dx, da, db)
+
 Q4_K weights are uint8 tensors holding the raw 144-byte blocks ([rows,
 cols/256, 144] or flat); x is fp16 ``[M, hidden]``.
 """
@@ -80,6 +87,16 @@ EXPORTS = (
     "zinc_moe_gemm_fp8",
     "zinc_moe_fp8_experts_workspace_size",
     "zinc_moe_fp8_experts",
+    "zinc_moe_gemm_workspace_size",
+    "zinc_moe_gemm",
+    "zinc_moe_gemm_backward_workspace_size",
+    "zinc_moe_gemm_backward",
+    "zinc_swiglu",
+    "zinc_swiglu_backward",
+    "zinc_lora_workspace_size",
+    "zinc_lora",
+    "zinc_lora_backward_workspace_size",
+    "zinc_lora_backward",
     "zinc_timing_enable",
     "zinc_timing_collect",
     "zinc_timing_disable",
@@ -147,7 +164,11 @@ def _load() -> ctypes.CDLL:
             ("zinc_moe_sort_workspace_size", [I32, I32, I32]),
             ("zinc_gemm_fp8_workspace_size", [I32, I32, I32]),
             ("zinc_moe_gemm_fp8_workspace_size", [I32, I32, I32, I32]),
-            ("zinc_moe_fp8_experts_workspace_size", [I32, I32, I32, I32, I32, I32])):
+            ("zinc_moe_fp8_experts_workspace_size", [I32, I32, I32, I32, I32, I32]),
+            ("zinc_moe_gemm_workspace_size", [I32, I32, I32, I32]),
+            ("zinc_moe_gemm_backward_workspace_size", [I32, I32, I32, I32]),
+            ("zinc_lora_workspace_size", [I32, I32, I32, I32, I32]),
+            ("zinc_lora_backward_workspace_size", [I32, I32, I32, I32, I32])):
         getattr(lib, name).restype = SZ
         getattr(lib, name).argtypes = args
     for name, args in (
@@ -159,7 +180,14 @@ def _load() -> ctypes.CDLL:
             ("zinc_fp8_quantize", [P, I32, I32, I32, I32, P, P, P]),
             ("zinc_gemm_fp8", [P, P, P, P, I32, I32, I32, I32, P, P, SZ, P]),
             ("zinc_moe_gemm_fp8", [P, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
-            ("zinc_moe_fp8_experts", [P, P, P, P, P, P, I32, I32, I32, P, I32, I32, P, P, I32, P, P, SZ, P, P])):
+            ("zinc_moe_fp8_experts", [P, P, P, P, P, P, I32, I32, I32, P, I32, I32, P, P, I32, P, P, SZ, P, P]),
+            ("zinc_moe_gemm", [P, P, I32, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
+            ("zinc_moe_gemm_backward", [P, P, P, I32, P, I32, I32, I32, I32, I32, P, I32, P, P, SZ, P]),
+            ("zinc_swiglu", [P, P, I32, I32, I32, P, P]),
+            ("zinc_swiglu_backward", [P, P, P, I32, I32, I32, P, P, P]),
+            ("zinc_lora", [P, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, P, P, SZ, P]),
+            ("zinc_lora_backward",
+             [P, P, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, P, P, P, P, SZ, P])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = args
     lib.zinc_timing_enable.restype = ctypes.c_int
@@ -932,3 +960,210 @@ def zinc_moe_fp8_experts(w_gate, gate_scales, w_up, up_scales, w_down, down_scal
           _ptr(down_scales), E, hidden, inter, _ptr(x), code, M, _ptr(expert_ids), _ptr(expert_weights), top_k, _ptr(y),
           ws, ws_bytes, _ptr(dev_error))
     return y
+
+
+# ---------------------------------------------------------------------------
+# the expert layer in 16 bits, and low-rank adapters
+# ---------------------------------------------------------------------------
+def moe_gemm_workspace_size(rows: int, n_experts: int, N: int, K: int) -> int:
+    return _size(lib.zinc_moe_gemm_workspace_size, rows, n_experts, N, K)
+
+
+def moe_gemm_backward_workspace_size(rows: int, n_experts: int, N: int, K: int) -> int:
+    return _size(lib.zinc_moe_gemm_backward_workspace_size, rows, n_experts, N, K)
+
+
+def lora_workspace_size(M: int, n_adapters: int, K: int, N: int, rank: int) -> int:
+    return _size(lib.zinc_lora_workspace_size, M, n_adapters, K, N, rank)
+
+
+def lora_backward_workspace_size(M: int, n_adapters: int, K: int, N: int, rank: int) -> int:
+    return _size(lib.zinc_lora_backward_workspace_size, M, n_adapters, K, N, rank)
+
+
+def _rows16(x, what: str):
+    """_rows_of for the calls on 16-bit operands."""
+    code, rows, cols = _rows_of(x, 8, what)
+    if code == 2:
+        raise ValueError(f"{what} must be float16 or bfloat16")
+    if rows > 1 << 24:
+        raise ValueError(f"{what} must have at most 2**24 rows")
+    return code, rows, cols
+
+
+def _out_code(dtype, of, what: str) -> int:
+    if dtype is not of and dtype is not _torch().float32:
+        raise ValueError(f"{what} must be {of} or torch.float32, got {dtype}")
+    return _type_code(dtype, what)
+
+
+def _expert_weights(w, dtype, what: str = "w"):
+    """(experts, rows, columns) of contiguous 16-bit matrices [n_experts, N, K]."""
+    if w is None or w.dim() != 3:
+        raise ValueError(f"{what} must be a 3-D [n_experts, N, K] tensor")
+    E, N, K = w.shape
+    if E < 1 or E > 1024:
+        raise ValueError(f"{what} must hold 1..1024 matrices")
+    for n in (N, K):
+        if n <= 0 or n % 8 or n > 65536:
+            raise ValueError(f"{what}'s matrices must have multiples of 8 rows and columns, at most 65536")
+    _fits(w, dtype, (E, N, K), what)
+    return E, N, K
+
+
+def zinc_moe_gemm(a, w, offsets, out_dtype=None, out=None, workspace=None, stream=None):
+    """Rows ``offsets[e]`` .. ``offsets[e + 1] - 1`` of a ``[rows, K]`` times ``w[e]`` (w ``[E, N, K]``, float16 or
+    bfloat16 as a) transposed: ``c [rows, N]`` of ``out_dtype``, a's (the default) or float32; rows outside every range
+    are left as they were."""
+    torch = _torch()
+    code, rows, K = _rows16(a, "a")
+    E, N, _ = _expert_weights(w, a.dtype)
+    _fits(w, a.dtype, (E, N, K), "w")
+    _fits(offsets, torch.int32, (E + 1,), "offsets")
+    dtype = out_dtype or (a.dtype if out is None else out.dtype)
+    out_code = _out_code(dtype, a.dtype, "out_dtype")
+    if out is not None:
+        _fits(out, dtype, (rows, N), "out")
+    need = lib.zinc_moe_gemm_workspace_size(rows, E, N, K)
+    _workspace(workspace, need)
+    c = _Call(stream, a, w, offsets, out, workspace)
+    out = c.empty((rows, N), dtype) if out is None else out
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
+    c.run("zinc_moe_gemm", _ptr(a), _ptr(w), code, _ptr(offsets), E, rows, N, K, out_code, _ptr(out), ws, ws_bytes)
+    return out
+
+
+def zinc_moe_gemm_backward(dc, a, w, offsets, da_dtype=None, dw_dtype=None, da=None, dw=None, want_da=True,
+                           want_dw=True, workspace=None, stream=None):
+    """Gradients of zinc_moe_gemm from dc ``[rows, N]``: ``(da [rows, K], dw [E, N, K])``, of the operands' type or
+    float32 each; None where ``want_da`` (``want_dw``) is false.  Rows of da outside every range are left as they
+    were; dw of an expert without rows is zeros."""
+    torch = _torch()
+    code, rows, N = _rows16(dc, "dc")
+    E, _, K = _expert_weights(w, dc.dtype)
+    _fits(w, dc.dtype, (E, N, K), "w")
+    _fits(a, dc.dtype, (rows, K), "a")
+    _fits(offsets, torch.int32, (E + 1,), "offsets")
+    if not want_da and not want_dw or (da is not None and not want_da) or (dw is not None and not want_dw):
+        raise ValueError("want_da and want_dw say which gradients are computed, one at least")
+    a_type = da_dtype or (dc.dtype if da is None else da.dtype)
+    w_type = dw_dtype or (dc.dtype if dw is None else dw.dtype)
+    a_code, w_code = _out_code(a_type, dc.dtype, "da_dtype"), _out_code(w_type, dc.dtype, "dw_dtype")
+    if da is not None:
+        _fits(da, a_type, (rows, K), "da")
+    if dw is not None:
+        _fits(dw, w_type, (E, N, K), "dw")
+    need = lib.zinc_moe_gemm_backward_workspace_size(rows, E, N, K)
+    _workspace(workspace, need)
+    c = _Call(stream, dc, a, w, offsets, da, dw, workspace)
+    if want_da and da is None:
+        da = c.empty((rows, K), a_type)
+    if want_dw and dw is None:
+        dw = c.empty((E, N, K), w_type)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
+    # (an empty tensor has no address, which would say that da is not wanted: the library needs none then)
+    if want_dw or rows:
+        c.run("zinc_moe_gemm_backward", _ptr(dc), _ptr(a), _ptr(w), code, _ptr(offsets), E, rows, N, K, a_code,
+              _ptr(da), w_code, _ptr(dw), ws, ws_bytes)
+    return da, dw
+
+
+def _same_rows(first, what: str, **others):
+    code, rows, cols = _rows_of(first, 8, what)
+    if rows > 1 << 24:
+        raise ValueError(f"{what} must have at most 2**24 rows")
+    for name, t in others.items():
+        _fits(t, first.dtype, (rows, cols), name)
+    return code, rows, cols
+
+
+def zinc_swiglu(gate, up, h=None, stream=None):
+    """``h = silu(gate) * up``, ``[rows, cols]`` (float16, bfloat16 or float32), computed in float32."""
+    code, rows, cols = _same_rows(gate, "gate", up=up)
+    if h is not None:
+        _fits(h, gate.dtype, (rows, cols), "h")
+    c = _Call(stream, gate, up, h)
+    h = c.empty((rows, cols), gate.dtype) if h is None else h
+    c.run("zinc_swiglu", _ptr(gate), _ptr(up), code, rows, cols, _ptr(h))
+    return h
+
+
+def zinc_swiglu_backward(dh, gate, up, dgate=None, dup=None, stream=None):
+    """Gradients of zinc_swiglu: ``(dgate, dup)``."""
+    code, rows, cols = _same_rows(gate, "gate", up=up, dh=dh)
+    for t, what in ((dgate, "dgate"), (dup, "dup")):
+        if t is not None:
+            _fits(t, gate.dtype, (rows, cols), what)
+    c = _Call(stream, dh, gate, up, dgate, dup)
+    dgate = c.empty((rows, cols), gate.dtype) if dgate is None else dgate
+    dup = c.empty((rows, cols), gate.dtype) if dup is None else dup
+    c.run("zinc_swiglu_backward", _ptr(dh), _ptr(gate), _ptr(up), code, rows, cols, _ptr(dgate), _ptr(dup))
+    return dgate, dup
+
+
+def _adapters(x, a, b, scales, offsets, slot_row, row_slot):
+    """(type code, M, K, adapters, rank, N) of an adapter call's inputs."""
+    torch = _torch()
+    code, M, K = _rows16(x, "x")
+    if a is None or a.dim() != 3 or b is None or b.dim() != 3:
+        raise ValueError("a must be a 3-D [n_adapters, rank, K] and b a 3-D [n_adapters, N, rank] tensor")
+    E, rank, N = a.shape[0], a.shape[1], b.shape[1]
+    if E < 1 or E > 1024:
+        raise ValueError("there must be 1..1024 adapters")
+    if rank <= 0 or rank % 8 or rank > 256:
+        raise ValueError(f"the rank must be a multiple of 8, at most 256, got {rank}")
+    if N <= 0 or N % 8 or N > 65536:
+        raise ValueError(f"b's matrices must have a multiple of 8 rows, at most 65536, got {N}")
+    _fits(a, x.dtype, (E, rank, K), "a")
+    _fits(b, x.dtype, (E, N, rank), "b")
+    if scales is not None:
+        _fits(scales, torch.float32, (E,), "scales")
+    _fits(offsets, torch.int32, (E + 1,), "offsets")
+    _fits(slot_row, torch.int32, (M, 1), "slot_row")
+    _fits(row_slot, torch.int32, (M,), "row_slot")
+    return code, M, K, E, rank, N
+
+
+def zinc_lora(x, a, b, scales, offsets, slot_row, row_slot, base=None, y=None, workspace=None, stream=None):
+    """``y[m] = base[m] + scales[e] * b[e] @ (a[e] @ x[m])``, ``[M, N]``, for row m's adapter e; rows without one are
+    base's.  a ``[n_adapters, rank, K]``, b ``[n_adapters, N, rank]``, float16 or bfloat16 as x ``[M, K]``; ``scales``
+    float32 (None: ones).  ``offsets, slot_row, row_slot`` is what ``zinc_moe_sort(ids[:, None], n_adapters)`` gives
+    for the rows' adapter ids.  ``base`` is the shared projection's output (None: zeros); ``y`` may be ``base``."""
+    code, M, K, E, rank, N = _adapters(x, a, b, scales, offsets, slot_row, row_slot)
+    for t, what in ((base, "base"), (y, "y")):
+        if t is not None:
+            _fits(t, x.dtype, (M, N), what)
+    need = lib.zinc_lora_workspace_size(M, E, K, N, rank)
+    _workspace(workspace, need)
+    c = _Call(stream, x, a, b, scales, offsets, slot_row, row_slot, base, y, workspace)
+    y = c.empty((M, N), x.dtype) if y is None else y
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
+    c.run("zinc_lora", _ptr(x), code, M, K, _ptr(a), _ptr(b), rank, E, N, _ptr(scales), _ptr(offsets), _ptr(slot_row),
+          _ptr(row_slot), _ptr(base), _ptr(y), ws, ws_bytes)
+    return y
+
+
+def zinc_lora_backward(dy, x, a, b, scales, offsets, slot_row, row_slot, base=None, dx=None, da=None, db=None,
+                       want_dx=True, want_da=True, want_db=True, workspace=None, stream=None):
+    """Gradients of zinc_lora from dy ``[M, N]``: ``(dx, da, db)``, None where the ``want_`` flag is false.  ``base`` is
+    the shared projection's own gradient of x, which dx is added to (None: zeros; ``dx`` may be ``base``).  da and db of
+    an adapter without rows are zeros."""
+    code, M, K, E, rank, N = _adapters(x, a, b, scales, offsets, slot_row, row_slot)
+    _fits(dy, x.dtype, (M, N), "dy")
+    wanted = ((dx, want_dx, (M, K), "dx"), (da, want_da, (E, rank, K), "da"), (db, want_db, (E, N, rank), "db"))
+    if not (want_dx or want_da or want_db) or any(t is not None and not want for t, want, _, _ in wanted):
+        raise ValueError("want_dx, want_da and want_db say which gradients are computed, one at least")
+    if base is not None:
+        _fits(base, x.dtype, (M, K), "base")
+    for t, _, shape, what in wanted:
+        if t is not None:
+            _fits(t, x.dtype, shape, what)
+    need = lib.zinc_lora_backward_workspace_size(M, E, K, N, rank)
+    _workspace(workspace, need)
+    c = _Call(stream, dy, x, a, b, scales, offsets, slot_row, row_slot, base, dx, da, db, workspace)
+    dx, da, db = (c.empty(shape, x.dtype) if want and t is None else t for t, want, shape, _ in wanted)
+    ws, ws_bytes, _keep = c.workspace(workspace, need)
+    if M or want_da or want_db:   # (an empty dx has no address)
+        c.run("zinc_lora_backward", _ptr(dy), _ptr(x), code, M, K, _ptr(a), _ptr(b), rank, E, N, _ptr(scales),
+              _ptr(offsets), _ptr(slot_row), _ptr(row_slot), _ptr(base), _ptr(dx), _ptr(da), _ptr(db), ws, ws_bytes)
+    return dx, da, db

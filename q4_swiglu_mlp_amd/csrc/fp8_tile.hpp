@@ -16,10 +16,11 @@
 #pragma once
 
 #include "fp8_device.hpp"
+#include "silu.hpp"
+#include "tiles.hpp"
 
 namespace zinc {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 
@@ -65,46 +66,6 @@ __device__ __forceinline__ void mfma_blocks(const Frag<true>& a0, const Frag<tru
   }
 }
 
-// The rows [first, first + rows) of tile `tile` (TM rows each) of the experts'
-// row ranges, and its expert; rows <= 0 past the last tile.  Offsets outside
-// [0, total] or not ascending are cut to that range.
-struct RowTile {
-  int expert, first, rows;
-};
-
-template <int TM>
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int E, int total, int tile) {
-  if (!offsets) return {0, tile * TM, min(TM, total - tile * TM)};
-  const int lane = threadIdx.x & 63;
-  int seen = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = e < E ? min(max(offsets[e], 0), total) : 0;
-    const int hi = e < E ? min(max(offsets[e + 1], lo), total) : 0;
-    const int n = (hi - lo + TM - 1) / TM;
-    int scan = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(scan, d, 64);
-      if (lane >= d) scan += o;
-    }
-    const uint64_t here = __ballot(seen + scan > tile);
-    if (here) {
-      const int l = (int)__builtin_ctzll(here);
-      const int before = seen + __builtin_amdgcn_readlane(scan - n, l);
-      const int first = __builtin_amdgcn_readlane(lo, l) + (tile - before) * TM;
-      return {e0 + l, first, min(TM, __builtin_amdgcn_readlane(hi, l) - first)};
-    }
-    seen += __builtin_amdgcn_readlane(scan, 63);
-  }
-  return {0, 0, 0};
-}
-
-// Row tiles a grouped product can have: every expert's last one may be partly filled.
-inline long long max_row_tiles(long long rows, int experts, int TM) {
-  return experts ? (rows + TM - 1) / TM + (experts < rows ? experts : rows) : (rows + TM - 1) / TM;
-}
-
 struct GemmArgs {
   const uint8_t* a;
   const float* sa;
@@ -120,41 +81,6 @@ struct GemmArgs {
   void* c;
   float* cs;            // scales of a quantised output
 };
-
-// Buffer loads bounded by a matrix's `bytes` from p: bytes behind them read as zero
-// and touch no memory.
-using Buffer = __amdgpu_buffer_rsrc_t;
-__device__ __forceinline__ Buffer tile_buffer(const uint8_t* p, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
-}
-// Sixteen bytes a lane to LDS, lane after lane from dst.
-__device__ __forceinline__ void to_lds(Buffer b, int off, uint8_t* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
-}
-__device__ __forceinline__ i32x4_t load_piece(Buffer b, int off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
-}
-
-// silu(z) u = z u / (1 + e^-z).  e^-z as 2^t (1 + r ln 2) with t = -z log2(e) rounded and r what
-// the rounding left, log2(e) in two parts: within a few units in the last place, and the reciprocal
-// within one.  z is cut for t: at 64, where e^-z adds nothing to 1, and at kTail.
-// From kTail on down (t > 119) the quotient is 2^-t, to 2^-119 of it, and soon leaves fp32's range,
-// where a large u may bring the product back.  TAIL leaves 2^-120 to the reciprocal and takes the rest,
-// 2^(120 - t), as two factors, u first, so that nothing falls out of range before the product does; for
-// other z it gives the same bits.  (Under e^-1024 every u vanishes.)
-constexpr float kTail = -83.0f;
-template <bool TAIL = false>
-__device__ __forceinline__ float silu_times(float z, float u) {
-  constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float c = __builtin_amdgcn_fmed3f(z, TAIL ? -1024.0f : kTail, 64.0f);
-  const float t = c * kHi;
-  const float r = fmaf(c, kLo, fmaf(c, kHi, -t));
-  const float e2 = __builtin_amdgcn_exp2f(TAIL ? fminf(t, 120.0f) : t);
-  const float s = z * __builtin_amdgcn_rcpf(1.0f + fmaf(e2, r * kLn2, e2));
-  if constexpr (!TAIL) return s * u;
-  const float f = __builtin_amdgcn_exp2f(fminf(120.0f - t, 0.0f) * 0.5f);
-  return u * f * f * s;
-}
 
 // The same for the whole workgroup and not written by the kernel: scalar loads.
 __device__ __forceinline__ const __attribute__((address_space(4))) float* uniform(const float* p) {
@@ -220,32 +146,6 @@ struct TileKernel {
     int nt, split, kb0, kbs;   // its column tile and blocks of K
   };
 
-  // Row tiles of all experts, and the tables; offsets are cut to [0, M] and, where
-  // they do not ascend, the range is empty.
-  static __device__ __forceinline__ int make_tables(const GemmArgs& g, int32_t* starts, int32_t* ends) {
-    const int lane = threadIdx.x & 63;
-    int seen = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int lo = e < g.E ? min(max(g.offsets[e], 0), g.M) : 0;
-      const int hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.M) : 0;
-      const int n = (hi - lo + TM - 1) / TM;
-      int scan = n;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(scan, d, 64);
-        if (lane >= d) scan += o;
-      }
-      if (threadIdx.x < 64 && e < g.E) {
-        starts[e] = lo;
-        if (e == g.E - 1) starts[g.E] = hi;
-        ends[e] = seen + scan;
-      }
-      seen += __builtin_amdgcn_readlane(scan, 63);
-    }
-    return seen;
-  }
-
   static __device__ __forceinline__ Unit unit_at(const GemmArgs& g, const int32_t* starts, const int32_t* ends,
                                                  int row_tiles, int KB, long long u) {
     Unit r;
@@ -265,20 +165,7 @@ struct TileKernel {
       r.rows = min(TM, g.M - r.first);
       return r;
     }
-    const int lane = threadIdx.x & 63;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int end = e < g.E ? ends[e] : 0x7FFFFFFF;
-      const uint64_t here = __ballot(end > mt);
-      if (here) {
-        r.expert = e0 + (int)__builtin_ctzll(here);
-        break;
-      }
-    }
-    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
-    const int before = r.expert ? ends[r.expert - 1] : 0, lo = starts[r.expert];
-    r.first = __builtin_amdgcn_readfirstlane(lo + (mt - before) * TM);
-    r.rows = __builtin_amdgcn_readfirstlane(min(TM, max(lo, starts[r.expert + 1]) - r.first));
+    tile_rows<TM>(g, starts, ends, mt, r);
     return r;
   }
 
@@ -290,7 +177,7 @@ struct TileKernel {
     int32_t* ends = starts + g.E + 1;
     int row_tiles = g.row_tiles;
     if (g.offsets) {
-      row_tiles = make_tables(g, starts, ends);
+      row_tiles = make_tables<TM>(g, starts, ends);
       __syncthreads();
     }
     // this workgroup's units: u, u + stride, ... below last

@@ -1,0 +1,363 @@
+// The tiled kernel of the 16-bit products by group (k_gemm16.hip), all three of a training step:
+//   forward  c[r][n]      = sum_k a[r][k]  w[e][n][k]      the rows r of group e
+//   input    da[r][k]     = sum_n dc[r][n] w[e][n][k]
+//   weight   dw[e][n][k]  = sum_r dc[r][n] a[r][k]
+// One workgroup computes TM x TN outputs, its waves a WM x WN grid of them, on 16x16x32 MFMAs.  P is the
+// operand of the output's rows, Q that of its columns; Q is the MFMA's row operand, so that a lane holds
+// neighbouring columns of one output row.
+//
+// Per step of 64 along the summed dimension both tiles are copied straight to LDS (16 bytes a lane, no
+// registers in between) into one of two or three buffers while the waves multiply from another; one
+// barrier a step.  An operand whose summed dimension is contiguous lies in LDS as [rows][64], one whose
+// rows are summed over as [64][columns], read by transposing loads (ds_read_b64_tr_b16: lanes 4 i .. 4 i + 3
+// of 16 name row i's 16 values, lane 4 c + t gets value t of piece c from each of the four rows).  The 16-byte pieces
+// of a row are turned by the row's number, so that the lanes of a read spread over the banks.
+#pragma once
+
+#include "fp8_device.hpp"
+#include "tiles.hpp"
+
+namespace zinc {
+
+enum Product { kForward, kInput, kWeight };
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef short i16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4_t mfma16(i16x8_t a, i16x8_t b, f32x4_t c, _Float16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0,
+                                                0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(i16x8_t a, i16x8_t b, f32x4_t c, __bf16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bhalf8_t, a), __builtin_bit_cast(bhalf8_t, b), c,
+                                                 0, 0, 0);
+}
+
+__device__ __forceinline__ i16x4_t read_turned(const uint8_t* lds) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)lds);
+}
+
+struct Gemm16Args {
+  const void* p;    // a, or dc
+  const void* q;    // w, or a
+  const int32_t* offsets;
+  int E, M, N, K;   // groups, rows, w's rows and columns
+  void* c;
+};
+
+template <Product F, int TM, int TN, int WM, int WN, typename T, typename O>
+struct Gemm16 {
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
+  static constexpr bool P_T = F == kWeight, Q_T = F != kForward;   // summed over rows of the matrix
+  // Columns of two neighbouring 16-wide tiles taken in turns of four, so that a lane's sums are eight
+  // neighbours.  The transposing reads would meet two to a bank so; their lanes hold two times four.
+  static constexpr bool WIDE = !Q_T;
+  static constexpr int PI = TM / 8 / WAVES, QI = TN / 8 / WAVES, COPIES = PI + QI;   // copies a wave, a step
+  static constexpr int BUFFER = (TM + TN) * 128;
+  static constexpr int NBUF = 3 * BUFFER <= 152 * 1024 && TN == 256 ? 3 : 2;
+  static constexpr int BAND = 8;   // row tiles walked per column
+  // workgroups a CU holds by registers
+  static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
+  static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 4 == 0, "whole copies");
+  static_assert(MT >= 4 && NT % 2 == 0, "tile shape");
+  static_assert((!P_T || WAVES * (512 / TM) % 16 == 0) && (!Q_T || WAVES * (512 / TN) % 16 == 0),
+                "a lane's turn is the same in all of its copies");
+
+  // LDS: the buffers, and for grouped rows starts[E + 1], the groups' first rows, and ends[E], the row
+  // tiles up to and with each
+  static size_t smem_bytes(int E) { return NBUF * BUFFER + (F == kWeight ? 0 : 4 * (2 * (size_t)E + 1)); }
+
+  struct Unit {
+    int expert, first, rows;   // rows of the matrix: the tile's, or the expert's (kWeight)
+    int p0, q0, steps;        // first output row (kWeight) and column
+  };
+
+  // How a row's pieces are turned.  [rows][64] of P: two rows fill the banks; of Q, whose rows are read as
+  // 8 q + r with q and r below 4, likewise.  [64][columns]: the eight rows of half a wave's read.
+  static __device__ __forceinline__ int p_turn(int row) { return (row >> 1) & 7; }
+  static __device__ __forceinline__ int q_turn(int row) { return ((row >> 1) & 1) + 2 * ((row >> 3) & 3); }
+  template <int W>
+  static __device__ __forceinline__ int t_turn(int row) {
+    return W >= 128 ? 2 * ((row & 3) + 4 * ((row >> 3) & 1)) : 2 * (((row >> 1) & 1) + 2 * ((row >> 3) & 1));
+  }
+
+  static __device__ __forceinline__ Unit unit_at(const Gemm16Args& g, const int32_t* starts, const int32_t* ends,
+                                                 int row_tiles, int col_tiles, long long u) {
+    Unit r;
+    if constexpr (F == kWeight) {
+      const int row_t = (g.N + TM - 1) / TM, each = row_t * col_tiles;
+      r.expert = (int)(u / each);
+      const int in = (int)(u - (long long)r.expert * each);
+      const int band = in / (BAND * col_tiles), at = in - band * BAND * col_tiles;
+      const int size = min(BAND, row_t - band * BAND), col = at / size;
+      r.p0 = (band * BAND + at - col * size) * TM;
+      r.q0 = col * TN;
+      const int lo = min(max(g.offsets[r.expert], 0), g.M), hi = min(max(g.offsets[r.expert + 1], lo), g.M);
+      r.first = __builtin_amdgcn_readfirstlane(lo);
+      r.rows = __builtin_amdgcn_readfirstlane(hi - lo);
+      r.steps = max(1, (r.rows + 63) / 64);   // a group without rows: one step of zeros
+    } else {
+      const int band = (int)(u / ((long long)BAND * col_tiles));
+      const int in = (int)(u - (long long)band * BAND * col_tiles);
+      const int size = min(BAND, row_tiles - band * BAND), col = in / size;
+      tile_rows<TM>(g, starts, ends, band * BAND + in - col * size, r);
+      r.p0 = 0;
+      r.q0 = col * TN;
+      r.steps = ((F == kForward ? g.K : g.N) + 63) / 64;
+    }
+    return r;
+  }
+
+  static __device__ __forceinline__ void run(const Gemm16Args& g, uint8_t* smem) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, l16 = lane & 15, quad = lane >> 4;
+    // the matrices' row lengths, the output's columns
+    const int ldp = F == kForward ? g.K : g.N, ldq = g.K, cols = F == kForward ? g.N : g.K;
+    const int col_tiles = (cols + TN - 1) / TN;
+    int32_t* starts = reinterpret_cast<int32_t*>(smem + NBUF * BUFFER);
+    int32_t* ends = starts + g.E + 1;
+    int row_tiles = 0;
+    long long total;
+    if constexpr (F == kWeight) {
+      total = (long long)g.E * ((g.N + TM - 1) / TM) * col_tiles;
+    } else {
+      row_tiles = make_tables<TM>(g, starts, ends);
+      __syncthreads();
+      total = (long long)row_tiles * col_tiles;
+    }
+    // this workgroup's units: u, u + stride, ... below last; an XCD takes a contiguous run of them
+    const long long per = (total + 7) / 8;
+    const int stride = gridDim.x / 8;
+    const long long last = min(total, (long long)((blockIdx.x & 7) + 1) * per);
+    long long u = (long long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (u >= last) return;
+
+    // Copies run ahead of the products: unit `ld`, its step `lk`.  Copy i of a wave carries the KB of LDS
+    // i WAVES + wave of its operand.  Buffer loads are bounded by the tile's part of the matrix; what lies
+    // behind it, or behind the summed dimension, arrives as zeros.
+    constexpr int kOut = 0x7FFFFFF0;
+    constexpr int PR = P_T ? 512 / TM : 8, QR = Q_T ? 512 / TN : 8;   // rows a copy carries
+    const int prow = wave * PR + lane / (64 / PR), qrow = wave * QR + lane / (64 / QR);
+    const int ppiece = P_T ? (lane % (64 / PR)) ^ t_turn<TM>(prow) : (lane & 7) ^ p_turn(prow);
+    const int qpiece = Q_T ? (lane % (64 / QR)) ^ t_turn<TN>(qrow) : (lane & 7) ^ q_turn(qrow);
+    const int pv = prow * ldp * 2 + ppiece * 16, qv = qrow * ldq * 2 + qpiece * 16;
+    Unit ld = unit_at(g, starts, ends, row_tiles, col_tiles, u);
+    long long lu = u;
+    int lk = 0;
+    Buffer rp, rq;
+    auto part = [](const void* m, size_t row, int col, int rows, int length) {
+      return tile_buffer(static_cast<const uint8_t*>(m) + (row * length + col) * 2,
+                         rows > 0 ? (rows * length - col) * 2 : 0);
+    };
+    // the operands' parts for step lk: fixed over a unit where the summed dimension is contiguous
+    auto open = [&](bool unit) {
+      const int k0 = lk * 64;
+      if constexpr (F == kForward) {
+        if (unit) {
+          rp = part(g.p, ld.first, 0, ld.rows, ldp);
+          rq = part(g.q, (size_t)ld.expert * g.N + ld.q0, 0, min(TN, g.N - ld.q0), ldq);
+        }
+      } else if constexpr (F == kInput) {
+        if (unit) rp = part(g.p, ld.first, 0, ld.rows, ldp);
+        rq = part(g.q, (size_t)ld.expert * g.N + k0, ld.q0, min(64, g.N - k0), ldq);
+      } else {
+        const int rows = min(64, ld.rows - k0);
+        rp = part(g.p, (size_t)ld.first + k0, ld.p0, rows, ldp);
+        rq = part(g.q, (size_t)ld.first + k0, ld.q0, rows, ldq);
+      }
+    };
+    open(true);
+    auto copy_piece = [&](int i, int buf) {
+      uint8_t* dst = smem + buf * BUFFER;
+      if (i < PI) {
+        int off = pv + i * (WAVES * PR) * ldp * 2;
+        if constexpr (!P_T) off = lk * 64 + ppiece * 8 < ldp ? off + lk * 128 : kOut;
+        to_lds(rp, off, dst + (i * WAVES + wave) * 1024);
+      } else {
+        int off = qv + (i - PI) * (WAVES * QR) * ldq * 2;
+        if constexpr (!Q_T) off = lk * 64 + qpiece * 8 < ldq ? off + lk * 128 : kOut;
+        to_lds(rq, off, dst + TM * 128 + ((i - PI) * WAVES + wave) * 1024);
+      }
+    };
+    auto advance = [&] {
+      if (lu >= last) return;
+      if (++lk < ld.steps) {
+        open(false);
+        return;
+      }
+      lk = 0;
+      lu += stride;
+      if (lu < last) {
+        ld = unit_at(g, starts, ends, row_tiles, col_tiles, lu);
+        open(true);
+      }
+    };
+    auto copy_all = [&](int buf) {
+      if (lu < last) {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy_piece(i, buf);
+      }
+      advance();
+    };
+
+    // A lane's fragment of 16 rows (columns) x 64: two of eight values, h = 0 and 1.
+    f32x4_t acc[MT][NT];
+    const int p_at = wm * (TM / WM), q_at = wn * (TN / WN);   // the wave's first
+    int pa[2], qa[2];
+    if constexpr (!P_T) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pa[h] = (p_at + l16) * 128 + (((quad + 4 * h) ^ p_turn(l16)) << 4);
+    } else {
+      const int row = 8 * quad + (l16 >> 2);
+      pa[0] = row * TM * 2 + (((p_at / 8 + ((l16 & 3) >> 1)) ^ t_turn<TM>(row)) << 4) + (l16 & 1) * 8;
+      pa[1] = 0;
+    }
+    if constexpr (!Q_T) {
+      const int row = 8 * (l16 >> 2) + (l16 & 3);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) qa[h] = TM * 128 + (q_at + row) * 128 + (((quad + 4 * h) ^ q_turn(row)) << 4);
+    } else {
+      const int row = 8 * quad + (l16 >> 2);
+      qa[0] = TM * 128 + row * TN * 2 + (((q_at / 8 + ((l16 & 3) >> 1)) ^ t_turn<TN>(row)) << 4) + (l16 & 1) * 8;
+      qa[1] = 0;
+    }
+    auto read_t = [](const uint8_t* at, int width, int h) {
+      const i16x4_t lo = read_turned(at + (32 * h) * width * 2), hi = read_turned(at + (32 * h + 4) * width * 2);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    i16x8_t pf[2][2], qf[NT][2];
+    auto read_p = [&](int i, int slot, int buf) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (!P_T)
+          pf[slot][h] = *reinterpret_cast<const i16x8_t*>(smem + buf * BUFFER + pa[h] + i * 2048);
+        else
+          pf[slot][h] = read_t(smem + buf * BUFFER + (pa[0] ^ (i << 5)), TM, h);
+      }
+    };
+    auto read_q = [&](int j, int buf) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (!Q_T)
+          qf[j][h] = *reinterpret_cast<const i16x8_t*>(smem + buf * BUFFER + qa[h] + (j >> 1) * 4096 + (j & 1) * 512);
+        else
+          qf[j][h] = read_t(smem + buf * BUFFER + TM * 128 + ((qa[0] - TM * 128) ^ (j << 5)), TN, h);
+      }
+    };
+
+    copy_all(0);
+    bool ahead = lu < last;   // the later steps' copies may be in flight behind the first's
+    copy_all(1);
+    if constexpr (NBUF == 3) {
+      ahead = ahead && lu < last;
+      copy_all(2);
+    }
+    if (ahead)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 1) * COPIES) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < NT; ++j) read_q(j, 0);
+    read_p(0, 0, 0);
+    int buf = 0;
+    auto after = [](int b) { return NBUF == 2 ? b ^ 1 : b == NBUF - 1 ? 0 : b + 1; };
+    constexpr int EACH = (COPIES + NT - 1) / NT;   // copies beside a column of the last two row tiles
+    for (; u < last; u += stride) {
+      const Unit cu = unit_at(g, starts, ends, row_tiles, col_tiles, u);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+      for (int k = 0; k < cu.steps; ++k, buf = after(buf)) {
+        const int next = after(buf);
+        // all columns of one row tile after the other, the next tile's fragment on its way
+#pragma unroll
+        for (int i = 0; i < MT - 2; ++i) {
+          if (i + 1 < MT - 2) {
+            read_p(i + 1, (i + 1) & 1, buf);
+          } else {
+            read_p(MT - 2, MT & 1, buf);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = mfma16(qf[j][h], pf[i & 1][h], acc[i][j], T{});
+          if (i == MT - 3) read_p(MT - 1, (MT - 1) & 1, buf);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        // the next step's tiles have landed, and every wave has read what it needs of this one's
+        if (NBUF == 3 && ahead)
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
+        else
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // the last two row tiles column by column, so that Q's fragments fall free for the next step's
+        const bool more = lu < last;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            acc[MT - 2][j] = mfma16(qf[j][h], pf[MT & 1][h], acc[MT - 2][j], T{});
+            acc[MT - 1][j] = mfma16(qf[j][h], pf[(MT - 1) & 1][h], acc[MT - 1][j], T{});
+          }
+          if (more) {
+#pragma unroll
+            for (int i = j * EACH; i < (j + 1) * EACH; ++i)
+              if (i < COPIES) copy_piece(i, buf);
+          }
+          read_q(j, next);
+          if (j == NT - 1) read_p(0, 0, next);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        advance();
+        ahead = more;
+      }
+      store(g, cu, cols, wm, wn, l16, quad, acc);
+    }
+  }
+
+  static __device__ __forceinline__ void store(const Gemm16Args& g, const Unit& cu, int cols, int wm, int wn, int l16,
+                                               int quad, f32x4_t (&acc)[MT][NT]) {
+    const int rows = F == kWeight ? min(TM, g.N - cu.p0) : cu.rows;
+    O* c = static_cast<O*>(g.c) +
+           (F == kWeight ? (size_t)cu.expert * g.N + cu.p0 : (size_t)cu.first) * (size_t)cols;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = wm * (TM / WM) + i * 16 + l16;
+      if (m >= rows) continue;
+      O* row = c + (size_t)m * cols;
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {
+        if constexpr (WIDE) {
+          const int n = cu.q0 + wn * (TN / WN) + j * 16 + 8 * quad;
+          float v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
+          if (n < cols) store8<sizeof(O) == 2>(row + n, v);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int n = cu.q0 + wn * (TN / WN) + (j + b) * 16 + 4 * quad;
+            typedef O O4 __attribute__((ext_vector_type(4)));
+            O4 o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = (O)acc[i][j + b][r];
+            if (n < cols) *reinterpret_cast<O4*>(row + n) = o;
+          }
+        }
+      }
+    }
+  }
+};
+
+template <typename KERNEL>
+__global__ __launch_bounds__(KERNEL::THREADS) void k_gemm16(Gemm16Args g) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  KERNEL::run(g, smem);
+}
+
+}  // namespace zinc

@@ -26,42 +26,11 @@
 // - many rows, the matrix units at the clock that the power limit leaves (about 1.9 GHz):
 //   8192 x 11008 x 4096 bf16 330 us, 2240 TFLOP/s, 379 us with weights that come from HBM
 //   (up to 5 % more on other cards); fp32 by fp16 MFMAs 480 us for 8192 x 8192 x 4096, 1145 TFLOP/s.
-#include <atomic>
-
 #include "fp8_stream.hpp"
 #include "launch.hpp"
 
 namespace zinc {
 namespace {
-
-// Raises the kernel's LDS limit, once a device.
-template <typename KERNEL>
-hipError_t allow_lds(const void* kernel, int bytes) {
-  static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready.load(std::memory_order_relaxed) & bit) return hipSuccess;
-  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
-constexpr int kLds = 160 * 1024;
-
-// Compute units of the current device (looked up once a device).
-hipError_t compute_units(int* n) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (*n) return hipSuccess;
-  e = hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, dev);
-  if (e == hipSuccess && dev < 64) known[dev].store(*n, std::memory_order_relaxed);
-  return e;
-}
 
 // As many persistent workgroups as the CUs hold, a multiple of the eight XCDs.
 template <typename KERNEL>

@@ -1,0 +1,92 @@
+// SwiGLU of rows and its gradients, elementwise:
+//   h = silu(g) u,   dg = dh u s (1 + g (1 - s)),   du = dh g s,   s = 1 / (1 + e^-g)
+// in fp32, rounded once to the rows' type.  Bound by the memory: one read of each input and one write of
+// each output, eight values a lane at a time.
+#include "fp8_device.hpp"
+#include "launch.hpp"
+#include "silu.hpp"
+
+namespace zinc {
+namespace {
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_swiglu(const T* __restrict__ gate, const T* __restrict__ up, size_t n,
+                                                T* __restrict__ h) {
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (size_t)gridDim.x * 2048) {
+    float g[8], u[8], v[8];
+    load8(gate + i, g);
+    load8(up + i, u);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const Sigmoid s = sigmoid(g[r]);
+      v[r] = (u[r] * s.factor) * (g[r] * s.value) * s.factor;
+    }
+    store8(h + i, v);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_swiglu_backward(const T* __restrict__ dh, const T* __restrict__ gate,
+                                                         const T* __restrict__ up, size_t n, T* __restrict__ dgate,
+                                                         T* __restrict__ dup) {
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (size_t)gridDim.x * 2048) {
+    float d[8], g[8], u[8], dg[8], du[8];
+    load8(dh + i, d);
+    load8(gate + i, g);
+    load8(up + i, u);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const Sigmoid s = sigmoid(g[r]);
+      const float slope = s.value * fmaf(g[r], s.rest, 1.0f);
+      dg[r] = (d[r] * s.factor * slope) * (u[r] * s.factor);
+      du[r] = (d[r] * s.factor) * (g[r] * s.value) * s.factor;
+    }
+    store8(dgate + i, dg);
+    store8(dup + i, du);
+  }
+}
+
+template <typename T>
+void forward(const void* gate, const void* up, size_t n, void* h, unsigned blocks, hipStream_t stream) {
+  hipLaunchKernelGGL(k_swiglu<T>, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(gate),
+                     static_cast<const T*>(up), n, static_cast<T*>(h));
+}
+template <typename T>
+void backward(const void* dh, const void* gate, const void* up, size_t n, void* dgate, void* dup, unsigned blocks,
+              hipStream_t stream) {
+  hipLaunchKernelGGL(k_swiglu_backward<T>, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(dh),
+                     static_cast<const T*>(gate), static_cast<const T*>(up), n, static_cast<T*>(dgate),
+                     static_cast<T*>(dup));
+}
+
+unsigned blocks_for(size_t n) {
+  const size_t blocks = (n + 2047) / 2048;
+  return (unsigned)(blocks < 8192 ? blocks : 8192);
+}
+
+}  // namespace
+
+hipError_t launch_swiglu(const void* gate, const void* up, int type, size_t n, void* h, hipStream_t stream) {
+  const unsigned blocks = blocks_for(n);
+  if (type == 0)
+    forward<_Float16>(gate, up, n, h, blocks, stream);
+  else if (type == 1)
+    forward<__bf16>(gate, up, n, h, blocks, stream);
+  else
+    forward<float>(gate, up, n, h, blocks, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* up, int type, size_t n, void* dgate,
+                                  void* dup, hipStream_t stream) {
+  const unsigned blocks = blocks_for(n);
+  if (type == 0)
+    backward<_Float16>(dh, gate, up, n, dgate, dup, blocks, stream);
+  else if (type == 1)
+    backward<__bf16>(dh, gate, up, n, dgate, dup, blocks, stream);
+  else
+    backward<float>(dh, gate, up, n, dgate, dup, blocks, stream);
+  return hipGetLastError();
+}
+
+}  // namespace zinc

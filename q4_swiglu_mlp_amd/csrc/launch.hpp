@@ -96,4 +96,30 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
                           const float* sd, int E, int H, int I, const void* x, int type, int M, const int32_t* ids,
                           const float* p, int top_k, void* y, void* ws, int32_t* dev_error, hipStream_t stream);
 
+// 16-bit products by group (k_gemm16_*.hip): rows offsets[e] .. offsets[e + 1] - 1 of M take group e's matrix
+// [N x K].  type: the operands' (0 or 1); out_type: the same or 2.
+//   forward  c [M x N] = a [M x K] w^T;  input  c = da [M x K] = dc [M x N] w;  weight  c = dw [E x N x K] = dc^T a
+hipError_t launch_gemm16_forward(const void* a, const void* w, int type, const int32_t* offsets, int E, int M, int N,
+                                 int K, int out_type, void* c, hipStream_t stream);
+hipError_t launch_gemm16_input(const void* dc, const void* w, int type, const int32_t* offsets, int E, int M, int N,
+                               int K, int out_type, void* c, hipStream_t stream);
+hipError_t launch_gemm16_weight(const void* dc, const void* a, int type, const int32_t* offsets, int E, int M, int N,
+                                int K, int out_type, void* c, hipStream_t stream);
+
+// SwiGLU and its gradients over n values, a multiple of eight (k_swiglu.hip).
+hipError_t launch_swiglu(const void* gate, const void* up, int type, size_t n, void* h, hipStream_t stream);
+hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* up, int type, size_t n, void* dgate,
+                                  void* dup, hipStream_t stream);
+
+// Low-rank adapters beside a projection (k_lora.hip).  base may be null or y (dx); dx, da, db may be null.
+size_t lora_workspace_bytes(int M, int rank);
+hipError_t launch_lora(const void* x, const void* a, const void* b, const float* scales, const int32_t* offsets,
+                       const int32_t* slot_row, const int32_t* row_slot, int E, int M, int K, int N, int rank, int type,
+                       const void* base, void* y, void* ws, hipStream_t stream);
+size_t lora_backward_workspace_bytes(int M, int E, int K, int N, int rank);
+hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, const void* b, const float* scales,
+                                const int32_t* offsets, const int32_t* slot_row, const int32_t* row_slot, int E, int M,
+                                int K, int N, int rank, int type, const void* base, void* dx, void* da, void* db,
+                                void* ws, hipStream_t stream);
+
 }  // namespace zinc
