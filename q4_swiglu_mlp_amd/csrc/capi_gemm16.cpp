@@ -35,6 +35,9 @@ hipStream_t begin(void* stream) {
   return static_cast<hipStream_t>(stream);
 }
 
+bool gemm_ok(int32_t rows, int32_t E, int32_t N, int32_t K) {
+  return rows_ok(rows) && groups_ok(E) && cols_ok(N) && cols_ok(K);
+}
 bool lora_shape_ok(int32_t K, int32_t N, int32_t rank) {
   return cols_ok(K) && cols_ok(N) && rank > 0 && rank % 8 == 0 && rank <= kMaxRank;
 }
@@ -43,26 +46,35 @@ bool lora_shape_ok(int32_t K, int32_t N, int32_t rank) {
 
 extern "C" {
 
-size_t zinc_moe_gemm_workspace_size(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t zinc_moe_gemm_workspace_size(int32_t rows, int32_t n_experts, int32_t N, int32_t K) {
+  if (!gemm_ok(rows, n_experts, N, K)) return 0;
+  return zinc::gemm16_workspace_bytes(rows, n_experts, N, K);
+}
 
 int zinc_moe_gemm(const void* a, const void* w, int32_t type, const int32_t* offsets, int32_t n_experts, int32_t rows,
-                  int32_t N, int32_t K, int32_t out_type, void* c, void*, size_t, void* stream) {
+                  int32_t N, int32_t K, int32_t out_type, void* c, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   if (!cols_ok(N) || !cols_ok(K)) return ZINC_ERR_SHAPE;
-  if (!rows_ok(rows) || !groups_ok(n_experts) || !half_type(type) || !out_ok(type, out_type)) return ZINC_ERR_ARG;
+  if (!gemm_ok(rows, n_experts, N, K) || !half_type(type) || !out_ok(type, out_type)) return ZINC_ERR_ARG;
   if (rows == 0) return ZINC_OK;
   if (!a || !w || !offsets || !c) return ZINC_ERR_NULL;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(c, 16) || !aligned(offsets, 4)) return ZINC_ERR_ALIGN;
+  const int st = check_workspace(workspace, workspace_bytes, zinc::gemm16_workspace_bytes(rows, n_experts, N, K));
+  if (st != ZINC_OK) return st;
   return zinc::status_from_hip(
-      zinc::launch_gemm16_forward(a, w, type, offsets, n_experts, rows, N, K, out_type, c, begin(stream)));
+      zinc::launch_gemm16_forward(a, w, type, offsets, n_experts, rows, N, K, out_type, c, workspace, begin(stream)));
 }
 
-size_t zinc_moe_gemm_backward_workspace_size(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t zinc_moe_gemm_backward_workspace_size(int32_t rows, int32_t n_experts, int32_t N, int32_t K) {
+  if (!gemm_ok(rows, n_experts, N, K)) return 0;
+  return zinc::gemm16_backward_workspace_bytes(rows, n_experts, N, K);
+}
 
 int zinc_moe_gemm_backward(const void* dc, const void* a, const void* w, int32_t type, const int32_t* offsets,
                            int32_t n_experts, int32_t rows, int32_t N, int32_t K, int32_t da_type, void* da,
-                           int32_t dw_type, void* dw, void*, size_t, void* stream) {
+                           int32_t dw_type, void* dw, void* workspace, size_t workspace_bytes, void* stream) {
   if (!cols_ok(N) || !cols_ok(K)) return ZINC_ERR_SHAPE;
-  if (!rows_ok(rows) || !groups_ok(n_experts) || !half_type(type) || (da && !out_ok(type, da_type)) ||
+  if (!gemm_ok(rows, n_experts, N, K) || !half_type(type) || (da && !out_ok(type, da_type)) ||
       (dw && !out_ok(type, dw_type)))
     return ZINC_ERR_ARG;
   if (!da && !dw) return ZINC_ERR_NULL;
@@ -71,12 +83,11 @@ int zinc_moe_gemm_backward(const void* dc, const void* a, const void* w, int32_t
   if (!aligned(dc, 16) || !aligned(a, 16) || !aligned(w, 16) || !aligned(da, 16) || !aligned(dw, 16) ||
       !aligned(offsets, 4))
     return ZINC_ERR_ALIGN;
-  hipStream_t s = begin(stream);
-  hipError_t e = hipSuccess;
-  if (da && rows > 0) e = zinc::launch_gemm16_input(dc, w, type, offsets, n_experts, rows, N, K, da_type, da, s);
-  if (e == hipSuccess && dw)
-    e = zinc::launch_gemm16_weight(dc, a, type, offsets, n_experts, rows, N, K, dw_type, dw, s);
-  return zinc::status_from_hip(e);
+  const int st =
+      check_workspace(workspace, workspace_bytes, zinc::gemm16_backward_workspace_bytes(rows, n_experts, N, K));
+  if (st != ZINC_OK) return st;
+  return zinc::status_from_hip(zinc::launch_gemm16_backward(dc, a, w, type, offsets, n_experts, rows, N, K, da_type, da,
+                                                            dw_type, dw, workspace, begin(stream)));
 }
 
 int zinc_swiglu(const void* gate, const void* up, int32_t type, int32_t rows, int32_t cols, void* h, void* stream) {

@@ -1,5 +1,5 @@
-// The tiled kernel of the 16-bit products by group (k_gemm16.hip), all three of a training step:
-//   forward  c[r][n]      = sum_k a[r][k]  w[e][n][k]      the rows r of group e
+// The tiled kernel of the 16-bit products by expert (k_gemm16_*.hip), all three of a training step:
+//   forward  c[r][n]      = sum_k a[r][k]  w[e][n][k]      the rows r of expert e
 //   input    da[r][k]     = sum_n dc[r][n] w[e][n][k]
 //   weight   dw[e][n][k]  = sum_r dc[r][n] a[r][k]
 // One workgroup computes TM x TN outputs, its waves a WM x WN grid of them, on 16x16x32 MFMAs.  P is the
@@ -41,12 +41,16 @@ struct Gemm16Args {
   const void* p;    // a, or dc
   const void* q;    // w, or a
   const int32_t* offsets;
-  int E, M, N, K;   // groups, rows, w's rows and columns
+  int E, M, N, K;   // experts, rows, w's rows and columns
   void* c;
+  int splits;       // parts of the summed dimension, each with its own output,
+  size_t part;      // this many values after the one before
+  int32_t* queue;   // the next unit of each XCD, 32 apart, from gridDim.x / 8 on; or null: dealt out in turn
 };
 
-template <Product F, int TM, int TN, int WM, int WN, typename T, typename O>
+template <Product F, int TM, int TN, int WM, int WN, int BUFFERS, typename T, typename O>
 struct Gemm16 {
+  static constexpr Product kProduct = F;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
   static constexpr bool P_T = F == kWeight, Q_T = F != kForward;   // summed over rows of the matrix
@@ -55,8 +59,10 @@ struct Gemm16 {
   static constexpr bool WIDE = !Q_T;
   static constexpr int PI = TM / 8 / WAVES, QI = TN / 8 / WAVES, COPIES = PI + QI;   // copies a wave, a step
   static constexpr int BUFFER = (TM + TN) * 128;
-  static constexpr int NBUF = 3 * BUFFER <= 152 * 1024 && TN == 256 ? 3 : 2;
+  static constexpr int NBUF = BUFFERS;
   static constexpr int BAND = 8;   // row tiles walked per column
+  // fp32 gradients of the weights are stored past the caches
+  static constexpr bool STREAMED = F == kWeight && sizeof(O) == 4;
   // workgroups a CU holds by registers
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
   static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 4 == 0, "whole copies");
@@ -64,13 +70,14 @@ struct Gemm16 {
   static_assert((!P_T || WAVES * (512 / TM) % 16 == 0) && (!Q_T || WAVES * (512 / TN) % 16 == 0),
                 "a lane's turn is the same in all of its copies");
 
-  // LDS: the buffers, and for grouped rows starts[E + 1], the groups' first rows, and ends[E], the row
-  // tiles up to and with each
-  static size_t smem_bytes(int E) { return NBUF * BUFFER + (F == kWeight ? 0 : 4 * (2 * (size_t)E + 1)); }
+  // LDS: the buffers, the numbers of the units in hand, and tables: starts[E + 1], the experts' first rows,
+  // and ends[E], the row tiles up to and with each; kWeight: rows[E] and the experts in the order of their units
+  static size_t smem_bytes(int E) { return NBUF * BUFFER + 16 + 4 * (2 * (size_t)E + 1); }
 
   struct Unit {
     int expert, first, rows;   // rows of the matrix: the tile's, or the expert's (kWeight)
     int p0, q0, steps;        // first output row (kWeight) and column
+    int split, k0;            // its part of the summed dimension, from this step (row, kWeight) on
   };
 
   // How a row's pieces are turned.  [rows][64] of P: two rows fill the banks; of Q, whose rows are read as
@@ -83,30 +90,62 @@ struct Gemm16 {
   }
 
   static __device__ __forceinline__ Unit unit_at(const Gemm16Args& g, const int32_t* starts, const int32_t* ends,
-                                                 int row_tiles, int col_tiles, long long u) {
+                                                 int row_tiles, int col_tiles, int u) {
     Unit r;
     if constexpr (F == kWeight) {
-      const int row_t = (g.N + TM - 1) / TM, each = row_t * col_tiles;
-      r.expert = (int)(u / each);
-      const int in = (int)(u - (long long)r.expert * each);
-      const int band = in / (BAND * col_tiles), at = in - band * BAND * col_tiles;
-      const int size = min(BAND, row_t - band * BAND), col = at / size;
-      r.p0 = (band * BAND + at - col * size) * TM;
+      const int row_t = (g.N + TM - 1) / TM, each = row_t * col_tiles, at = u / (each * g.splits);
+      const int inside = u - at * each * g.splits, in = inside % each;
+      r.split = inside / each;
+      r.expert = __builtin_amdgcn_readfirstlane(ends[at]);
+      const int band = in / (BAND * col_tiles), k = in - band * BAND * col_tiles;
+      const int size = min(BAND, row_t - band * BAND), col = k / size;
+      r.p0 = (band * BAND + k - col * size) * TM;
       r.q0 = col * TN;
       const int lo = min(max(g.offsets[r.expert], 0), g.M), hi = min(max(g.offsets[r.expert + 1], lo), g.M);
-      r.first = __builtin_amdgcn_readfirstlane(lo);
-      r.rows = __builtin_amdgcn_readfirstlane(hi - lo);
-      r.steps = max(1, (r.rows + 63) / 64);   // a group without rows: one step of zeros
+      const int part = ((hi - lo + g.splits - 1) / g.splits + 63) / 64 * 64;
+      r.k0 = min(r.split * part, hi - lo);
+      r.first = __builtin_amdgcn_readfirstlane(lo + r.k0);
+      r.rows = __builtin_amdgcn_readfirstlane(min(part, hi - lo - r.k0));
+      r.steps = max(NBUF + 1, (r.rows + 63) / 64);   // steps behind the last row: zeros
     } else {
-      const int band = (int)(u / ((long long)BAND * col_tiles));
-      const int in = (int)(u - (long long)band * BAND * col_tiles);
-      const int size = min(BAND, row_tiles - band * BAND), col = in / size;
-      tile_rows<TM>(g, starts, ends, band * BAND + in - col * size, r);
+      const int per_row = col_tiles * g.splits, band = u / (BAND * per_row), in = u - band * BAND * per_row;
+      const int size = min(BAND, row_tiles - band * BAND), column = in / size;
+      r.split = column / col_tiles;
+      const int col = column - r.split * col_tiles;
+      tile_rows<TM>(g, starts, ends, band * BAND + in - column * size, r);
       r.p0 = 0;
       r.q0 = col * TN;
-      r.steps = ((F == kForward ? g.K : g.N) + 63) / 64;
+      const int all = ((F == kForward ? g.K : g.N) + 63) / 64, each = (all + g.splits - 1) / g.splits;
+      r.k0 = r.split * each;
+      r.steps = max(NBUF + 1, min(each, all - r.k0));
     }
     return r;
+  }
+
+  // The experts with most rows first, dealt out to the XCDs' queues (each a contiguous run of the order)
+  // back and forth: 0 .. 7, 7 .. 0, ...; fewer than eight keep their order.
+  static __device__ __forceinline__ void order_experts(const Gemm16Args& g, int32_t* rows, int32_t* order) {
+    for (int e = threadIdx.x; e < g.E; e += THREADS) {
+      const int lo = min(max(g.offsets[e], 0), g.M);
+      rows[e] = max(min(g.offsets[e + 1], g.M) - lo, 0);
+    }
+    __syncthreads();
+    const int whole = g.E / 8, rest = g.E % 8;
+    for (int e = threadIdx.x; e < g.E; e += THREADS) {
+      const int mine = rows[e];
+      int rank = 0;
+      for (int o = 0; o < g.E; ++o) rank += rows[o] > mine || (rows[o] == mine && o < e);
+      int at = rank;
+      if (whole) {
+        const int turn = rank / 8;
+        auto xcd_of = [](int turn, int in) { return turn & 1 ? 7 - in : in; };
+        const int xcd = xcd_of(turn, rank % 8);
+        at = xcd * whole + turn;
+        for (int i = 0; i < rest; ++i) at += xcd_of(whole, i) < xcd;
+      }
+      order[at] = e;
+    }
+    __syncthreads();
   }
 
   static __device__ __forceinline__ void run(const Gemm16Args& g, uint8_t* smem) {
@@ -115,23 +154,49 @@ struct Gemm16 {
     // the matrices' row lengths, the output's columns
     const int ldp = F == kForward ? g.K : g.N, ldq = g.K, cols = F == kForward ? g.N : g.K;
     const int col_tiles = (cols + TN - 1) / TN;
-    int32_t* starts = reinterpret_cast<int32_t*>(smem + NBUF * BUFFER);
+    int32_t* ring = reinterpret_cast<int32_t*>(smem + NBUF * BUFFER);   // unit n of this workgroup: ring[n & 3]
+    int32_t* starts = ring + 4;
     int32_t* ends = starts + g.E + 1;
-    int row_tiles = 0;
-    long long total;
+    int row_tiles = 0, total;
     if constexpr (F == kWeight) {
-      total = (long long)g.E * ((g.N + TM - 1) / TM) * col_tiles;
+      order_experts(g, starts, ends);
+      total = g.E * ((g.N + TM - 1) / TM) * col_tiles * g.splits;
     } else {
       row_tiles = make_tables<TM>(g, starts, ends);
       __syncthreads();
-      total = (long long)row_tiles * col_tiles;
+      total = row_tiles * col_tiles * g.splits;
     }
-    // this workgroup's units: u, u + stride, ... below last; an XCD takes a contiguous run of them
-    const long long per = (total + 7) / 8;
-    const int stride = gridDim.x / 8;
-    const long long last = min(total, (long long)((blockIdx.x & 7) + 1) * per);
-    long long u = (long long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (u >= last) return;
+    // An XCD has a contiguous run of the units.  Its workgroups take them in turn, or from its queue and, when
+    // that is empty, from the others': then `got` is a number from queue `from`, on its way.
+    const int per = (total + 7) / 8, stride = gridDim.x / 8, xcd = blockIdx.x & 7;
+    int from = xcd, got = blockIdx.x >> 3;
+    auto ask = [&] {   // (one wave)
+      if (g.queue && lane == 0) got = atomicAdd(g.queue + 32 * from, 1);
+      if (!g.queue) got += stride;
+    };
+    auto answer = [&] {   // the next unit, or -1; (one wave)
+      for (;;) {
+        const int at = __builtin_amdgcn_readfirstlane(got);
+        if (at < min(per, total - from * per)) return from * per + at;
+        if (!g.queue || ((from + 1) & 7) == xcd) return -1;
+        from = (from + 1) & 7;
+        ask();
+      }
+    };
+    // A unit's number is asked for when the one two before it is done, before the outputs are stored, and told
+    // behind that; the copies need it a barrier later at the earliest, since a unit has more steps than buffers.
+    auto tell = [&](int n) {
+      if (wave == 0) {
+        const int unit = answer();
+        if (lane == 0) ring[n & 3] = unit;
+      }
+    };
+    tell(0);
+    if (wave == 0) ask();
+    tell(1);
+    __syncthreads();
+    auto unit_of = [&](int n) { return __builtin_amdgcn_readfirstlane(ring[n & 3]); };
+    if (unit_of(0) < 0) return;
 
     // Copies run ahead of the products: unit `ld`, its step `lk`.  Copy i of a wave carries the KB of LDS
     // i WAVES + wave of its operand.  Buffer loads are bounded by the tile's part of the matrix; what lies
@@ -142,17 +207,23 @@ struct Gemm16 {
     const int ppiece = P_T ? (lane % (64 / PR)) ^ t_turn<TM>(prow) : (lane & 7) ^ p_turn(prow);
     const int qpiece = Q_T ? (lane % (64 / QR)) ^ t_turn<TN>(qrow) : (lane & 7) ^ q_turn(qrow);
     const int pv = prow * ldp * 2 + ppiece * 16, qv = qrow * ldq * 2 + qpiece * 16;
-    Unit ld = unit_at(g, starts, ends, row_tiles, col_tiles, u);
-    long long lu = u;
-    int lk = 0;
-    Buffer rp, rq;
+    Unit ld = unit_at(g, starts, ends, row_tiles, col_tiles, unit_of(0));
+    int ln = 0, lk = 0;   // the unit that is copied and its step
+    bool is_more = true;
+    i32x4_t rp, rq;
     auto part = [](const void* m, size_t row, int col, int rows, int length) {
-      return tile_buffer(static_cast<const uint8_t*>(m) + (row * length + col) * 2,
+      return buffer_words(static_cast<const uint8_t*>(m) + (row * length + col) * 2,
                          rows > 0 ? (rows * length - col) * 2 : 0);
     };
-    // the operands' parts for step lk: fixed over a unit where the summed dimension is contiguous
+    // the operands' parts for step lk: fixed over a unit where the summed dimension is contiguous, and then cut at
+    // the unit's end of it
+    int end = 0;
     auto open = [&](bool unit) {
-      const int k0 = lk * 64;
+      const int k0 = F == kWeight ? lk * 64 : (ld.k0 + lk) * 64;
+      if (unit && F != kWeight) {
+        const int length = F == kForward ? g.K : g.N;
+        end = g.splits == 1 ? length : min(length, (ld.k0 + (((length + 63) / 64) + g.splits - 1) / g.splits) * 64);
+      }
       if constexpr (F == kForward) {
         if (unit) {
           rp = part(g.p, ld.first, 0, ld.rows, ldp);
@@ -160,11 +231,12 @@ struct Gemm16 {
         }
       } else if constexpr (F == kInput) {
         if (unit) rp = part(g.p, ld.first, 0, ld.rows, ldp);
-        rq = part(g.q, (size_t)ld.expert * g.N + k0, ld.q0, min(64, g.N - k0), ldq);
+        rq = part(g.q, (size_t)ld.expert * g.N + min(k0, end), ld.q0, min(64, end - k0), ldq);
       } else {
         const int rows = min(64, ld.rows - k0);
-        rp = part(g.p, (size_t)ld.first + k0, ld.p0, rows, ldp);
-        rq = part(g.q, (size_t)ld.first + k0, ld.q0, rows, ldq);
+        const size_t at = (size_t)ld.first + min(k0, ld.rows);
+        rp = part(g.p, at, ld.p0, rows, ldp);
+        rq = part(g.q, at, ld.q0, rows, ldq);
       }
     };
     open(true);
@@ -172,33 +244,29 @@ struct Gemm16 {
       uint8_t* dst = smem + buf * BUFFER;
       if (i < PI) {
         int off = pv + i * (WAVES * PR) * ldp * 2;
-        if constexpr (!P_T) off = lk * 64 + ppiece * 8 < ldp ? off + lk * 128 : kOut;
-        to_lds(rp, off, dst + (i * WAVES + wave) * 1024);
+        if constexpr (!P_T) off = (ld.k0 + lk) * 64 + ppiece * 8 < end ? off + (ld.k0 + lk) * 128 : kOut;
+        copy_to_lds(rp, off, dst + (i * WAVES + wave) * 1024);
       } else {
         int off = qv + (i - PI) * (WAVES * QR) * ldq * 2;
-        if constexpr (!Q_T) off = lk * 64 + qpiece * 8 < ldq ? off + lk * 128 : kOut;
-        to_lds(rq, off, dst + TM * 128 + ((i - PI) * WAVES + wave) * 1024);
+        if constexpr (!Q_T) off = (ld.k0 + lk) * 64 + qpiece * 8 < end ? off + (ld.k0 + lk) * 128 : kOut;
+        copy_to_lds(rq, off, dst + TM * 128 + ((i - PI) * WAVES + wave) * 1024);
       }
     };
+    // Behind a step's barrier: the next step, which may be the next unit's.
     auto advance = [&] {
-      if (lu >= last) return;
+      if (!is_more) return;
       if (++lk < ld.steps) {
         open(false);
         return;
       }
       lk = 0;
-      lu += stride;
-      if (lu < last) {
-        ld = unit_at(g, starts, ends, row_tiles, col_tiles, lu);
-        open(true);
+      const int next = unit_of(++ln);
+      if (next < 0) {
+        is_more = false;
+        return;
       }
-    };
-    auto copy_all = [&](int buf) {
-      if (lu < last) {
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy_piece(i, buf);
-      }
-      advance();
+      ld = unit_at(g, starts, ends, row_tiles, col_tiles, next);
+      open(true);
     };
 
     // A lane's fragment of 16 rows (columns) x 64: two of eight values, h = 0 and 1.
@@ -246,17 +314,24 @@ struct Gemm16 {
       }
     };
 
-    copy_all(0);
-    bool ahead = lu < last;   // the later steps' copies may be in flight behind the first's
-    copy_all(1);
-    if constexpr (NBUF == 3) {
-      ahead = ahead && lu < last;
-      copy_all(2);
+#pragma unroll
+    for (int b = 0; b < NBUF; ++b) {
+#pragma unroll
+      for (int i = 0; i < COPIES; ++i) copy_piece(i, b);
+      advance();
     }
-    if (ahead)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 1) * COPIES) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    int ahead = NBUF - 1;   // copies of whole steps that may be in flight behind those of the step that is waited for
+    // waits for all copies but those of the last `ahead` steps
+    auto landed = [&](int ahead) {
+      if (ahead == NBUF - 1)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 1) * COPIES) : "memory");
+      else if (ahead == NBUF - 2)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NBUF - 2) * COPIES) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    };
+    landed(ahead);
+    ahead = NBUF - 2;
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -265,8 +340,10 @@ struct Gemm16 {
     int buf = 0;
     auto after = [](int b) { return NBUF == 2 ? b ^ 1 : b == NBUF - 1 ? 0 : b + 1; };
     constexpr int EACH = (COPIES + NT - 1) / NT;   // copies beside a column of the last two row tiles
-    for (; u < last; u += stride) {
-      const Unit cu = unit_at(g, starts, ends, row_tiles, col_tiles, u);
+    for (int n = 0;; ++n) {
+      const int unit = unit_of(n);
+      if (unit < 0) return;
+      const Unit cu = unit_at(g, starts, ends, row_tiles, col_tiles, unit);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -276,11 +353,7 @@ struct Gemm16 {
         // all columns of one row tile after the other, the next tile's fragment on its way
 #pragma unroll
         for (int i = 0; i < MT - 2; ++i) {
-          if (i + 1 < MT - 2) {
-            read_p(i + 1, (i + 1) & 1, buf);
-          } else {
-            read_p(MT - 2, MT & 1, buf);
-          }
+          read_p(i + 1, (i + 1) & 1, buf);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -289,14 +362,11 @@ struct Gemm16 {
           __builtin_amdgcn_sched_barrier(0);
         }
         // the next step's tiles have landed, and every wave has read what it needs of this one's
-        if (NBUF == 3 && ahead)
-          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
-        else
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        landed(ahead);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         // the last two row tiles column by column, so that Q's fragments fall free for the next step's
-        const bool more = lu < last;
+        const bool more = is_more;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -314,40 +384,47 @@ struct Gemm16 {
           __builtin_amdgcn_sched_barrier(0);
         }
         advance();
-        ahead = more;
+        if (!more) ahead = 0;
       }
+      const bool asks = is_more && wave == 0;
+      if (asks) ask();
       store(g, cu, cols, wm, wn, l16, quad, acc);
+      if (asks) tell(n + 2);
     }
   }
 
   static __device__ __forceinline__ void store(const Gemm16Args& g, const Unit& cu, int cols, int wm, int wn, int l16,
                                                int quad, f32x4_t (&acc)[MT][NT]) {
+    // bounded by the tile's rows
     const int rows = F == kWeight ? min(TM, g.N - cu.p0) : cu.rows;
-    O* c = static_cast<O*>(g.c) +
-           (F == kWeight ? (size_t)cu.expert * g.N + cu.p0 : (size_t)cu.first) * (size_t)cols;
+    const size_t first = F == kWeight ? (size_t)cu.expert * g.N + cu.p0 : (size_t)cu.first;
+    const Buffer c = tile_buffer(static_cast<const uint8_t*>(g.c) + (cu.split * g.part + first * cols) * sizeof(O),
+                                 rows * cols * (int)sizeof(O));
+    constexpr int NT_STORE = STREAMED ? 2 : 0;
+    const int n0 = cu.q0 + wn * (TN / WN), at = (wm * (TM / WM) + l16) * cols;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const int m = wm * (TM / WM) + i * 16 + l16;
-      if (m >= rows) continue;
-      O* row = c + (size_t)m * cols;
 #pragma unroll
-      for (int j = 0; j < NT; j += 2) {
-        if constexpr (WIDE) {
-          const int n = cu.q0 + wn * (TN / WN) + j * 16 + 8 * quad;
-          float v[8];
+      for (int j = 0; j < NT; j += WIDE ? 2 : 1) {
+        const int n = n0 + j * 16 + (WIDE ? 8 : 4) * quad;
+        const int off = n < cols ? (at + i * 16 * cols + n) * (int)sizeof(O) : 0x7FFFFFF0;
+        if constexpr (sizeof(O) == 4) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, acc[i][j]), c, off, 0, NT_STORE);
+          if constexpr (WIDE)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, acc[i][j + 1]), c, off + 16, 0, NT_STORE);
+        } else if constexpr (WIDE) {
+          typedef O O8 __attribute__((ext_vector_type(8)));
+          O8 o;
 #pragma unroll
-          for (int r = 0; r < 8; ++r) v[r] = acc[i][j + (r >> 2)][r & 3];
-          if (n < cols) store8<sizeof(O) == 2>(row + n, v);
+          for (int r = 0; r < 8; ++r) o[r] = (O)acc[i][j + (r >> 2)][r & 3];
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, o), c, off, 0, NT_STORE);
         } else {
+          typedef O O4 __attribute__((ext_vector_type(4)));
+          typedef int i32x2_t __attribute__((ext_vector_type(2)));
+          O4 o;
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int n = cu.q0 + wn * (TN / WN) + (j + b) * 16 + 4 * quad;
-            typedef O O4 __attribute__((ext_vector_type(4)));
-            O4 o;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = (O)acc[i][j + b][r];
-            if (n < cols) *reinterpret_cast<O4*>(row + n) = o;
-          }
+          for (int r = 0; r < 4; ++r) o[r] = (O)acc[i][j][r];
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2_t, o), c, off, 0, NT_STORE);
         }
       }
     }

@@ -3,16 +3,14 @@
 namespace zinc {
 
 hipError_t launch_gemm16_forward(const void* p, const void* q, int type, const int32_t* offsets, int E, int M, int N,
-                               int K, int out_type, void* c, hipStream_t stream) {
-  const Gemm16Args g{p, q, offsets, E, M, N, K, c};
-  const int mean = M / E;
-  return by_types(type, out_type, [&](auto t, auto o) {
-    using T = decltype(t);
-    using O = decltype(o);
-    if (mean <= 160) return run_gemm16<kForward, 64, 128, 1, 4, T, O>(g, stream);
-    if (mean <= 320) return run_gemm16<kForward, 128, 128, 2, 2, T, O>(g, stream);
-    return run_gemm16<kForward, 256, 256, 2, 4, T, O>(g, stream);
-  });
+                               int K, int out_type, void* c, void* ws, hipStream_t stream) {
+  return launch_gemm16<kForward>(p, q, type, offsets, E, M, N, K, out_type, c, ws, stream);
+}
+
+size_t gemm16_workspace_bytes(int M, int E, int N, int K) {
+  if (M == 0) return 0;
+  const Gemm16Plan p = plan_gemm16(kForward, M, E, N, K);
+  return p.queue || p.splits > 1 ? kQueueBytes + gemm16_part_bytes(p) : 0;
 }
 
 }  // namespace zinc

@@ -100,18 +100,25 @@ hipError_t launch_moe_fp8(const void* wg, const float* sg, const void* wu, const
 // [N x K].  type: the operands' (0 or 1); out_type: the same or 2.
 //   forward  c [M x N] = a [M x K] w^T;  input  c = da [M x K] = dc [M x N] w;  weight  c = dw [E x N x K] = dc^T a
 hipError_t launch_gemm16_forward(const void* a, const void* w, int type, const int32_t* offsets, int E, int M, int N,
-                                 int K, int out_type, void* c, hipStream_t stream);
+                                 int K, int out_type, void* c, void* ws, hipStream_t stream);
 hipError_t launch_gemm16_input(const void* dc, const void* w, int type, const int32_t* offsets, int E, int M, int N,
-                               int K, int out_type, void* c, hipStream_t stream);
+                               int K, int out_type, void* c, void* ws, hipStream_t stream);
 hipError_t launch_gemm16_weight(const void* dc, const void* a, int type, const int32_t* offsets, int E, int M, int N,
-                                int K, int out_type, void* c, hipStream_t stream);
+                                int K, int out_type, void* c, void* ws, hipStream_t stream);
+
+size_t gemm16_workspace_bytes(int M, int E, int N, int K);
+// Both gradients, or one where the other's output is null.
+size_t gemm16_backward_workspace_bytes(int M, int E, int N, int K);
+hipError_t launch_gemm16_backward(const void* dc, const void* a, const void* w, int type, const int32_t* offsets, int E,
+                                  int M, int N, int K, int da_type, void* da, int dw_type, void* dw, void* ws,
+                                  hipStream_t stream);
 
 // SwiGLU and its gradients over n values, a multiple of eight (k_swiglu.hip).
 hipError_t launch_swiglu(const void* gate, const void* up, int type, size_t n, void* h, hipStream_t stream);
 hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* up, int type, size_t n, void* dgate,
                                   void* dup, hipStream_t stream);
 
-// Low-rank adapters beside a projection (k_lora.hip).  base may be null or y (dx); dx, da, db may be null.
+// Low-rank adapters beside a projection (k_lora_*.hip).  base may be null or y (dx); dx, da, db may be null.
 size_t lora_workspace_bytes(int M, int rank);
 hipError_t launch_lora(const void* x, const void* a, const void* b, const float* scales, const int32_t* offsets,
                        const int32_t* slot_row, const int32_t* row_slot, int E, int M, int K, int N, int rank, int type,

@@ -1,4 +1,4 @@
-// Device code of the low-rank adapters (k_lora.hip):
+// Device code of the low-rank adapters (k_lora_*.hip):
 //   forward   h = A_e x,  y = base + s_e B_e h
 //   backward  dh = B_e^T dy,  dx = base + s_e A_e^T dh,  dA_e = s_e dh^T x,  dB_e = s_e dy^T h
 // over the rows of adapter e, which the plan (zinc_moe_sort of the rows' adapter ids) lists.  "Position" is
@@ -52,9 +52,44 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7F800000u ? b : 0u;
 }
 
+// Rows in whole 128-byte lines.  As an MFMA operand lane l of 16 holds row l's pieces q and q + 4 (16 bytes
+// each, q its quarter of the wave); a load of piece q + 4 (l / 8) of row l % 8, and one of row 8 + l % 8, take
+// two such quarters of 8 rows each, which is 128 bytes a row.  The lower lanes' second load and the upper
+// lanes' first then change places; to store, the same again.  (8192 x 11008 read and written by 64-byte
+// pieces 95 us, by 128 75, by 256 and 1024 74.)
+__device__ __forceinline__ void trade_lines(i16x8_t& first, i16x8_t& second) {
+  const bool low = (threadIdx.x & 8) == 0;
+  const i32x4_t x = __builtin_bit_cast(i32x4_t, first), y = __builtin_bit_cast(i32x4_t, second);
+  i32x4_t a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int give = low ? y[i] : x[i];
+    const int get = __builtin_amdgcn_update_dpp(give, give, 0x128, 0xF, 0xF, false);   // row_ror:8
+    a[i] = low ? x[i] : get;
+    b[i] = low ? get : y[i];
+  }
+  first = __builtin_bit_cast(i16x8_t, a);
+  second = __builtin_bit_cast(i16x8_t, b);
+}
+
+// Four values of f: the sum of their parts in order, four parts in flight.
+__device__ __forceinline__ f32x4_t sum_parts(const float* from, int splits, size_t stride) {
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(from);
+  for (int q = 1; q < splits; q += 4) {
+    f32x4_t t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t[i] = *reinterpret_cast<const f32x4_t*>(from + (q + i < splits ? q + i : 0) * stride);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (q + i < splits) v += t[i];
+  }
+  return v;
+}
+
 // ---------------------------------------------------------------- the first products
 // parts[split][position][j] = sum over the split's columns c of z[row][c] w[j][c], or w[c][j] (W_T), j < rank.
-// A workgroup takes 16 RT rows of one adapter and a part of the columns, its four waves 32 columns in turn;
+// A workgroup takes 16 RT rows of one adapter and a part of the columns, its four waves 32 or 64 columns in turn;
 // their sums are joined in LDS.  w is the MFMA's row operand: a lane holds four neighbouring j of one row.
 struct ShrinkArgs {
   LoraPlan plan;
@@ -66,70 +101,112 @@ struct ShrinkArgs {
 
 template <typename T, int JT, int RT, bool W_T>
 struct Shrink {
-  static constexpr int TM = 16 * RT;
-  // LDS: the waves' sums; W_T: before that each wave's 32 x rank of w
+  static constexpr int kTiles = JT, TM = 16 * RT;
+  static constexpr int KS = JT <= 4 ? 2 : 1, COLS = 32 * KS;   // columns of a wave's step
+  static constexpr int STAGE = COLS * JT * 16 * 2 + 64;        // bytes
+  // LDS: the waves' sums; W_T: before that each wave's COLS x rank of w
   static size_t smem_bytes() {
-    const size_t sums = 3 * (size_t)RT * JT * 1024, stage = W_T ? 4 * (size_t)(32 * JT * 16 * 2 + 64) : 0;
+    const size_t sums = 3 * (size_t)RT * JT * 1024, stage = W_T ? 4 * (size_t)STAGE : 0;
     return sums > stage ? sums : stage;
   }
 
-  static __device__ __forceinline__ void run(const ShrinkArgs& s, uint8_t* smem) {
+  static __device__ __forceinline__ void run(const ShrinkArgs& s, int block, uint8_t* smem) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, quad = lane >> 4;
-    const int tile = blockIdx.x / s.splits, split = blockIdx.x - tile * s.splits;
+    const int tile = block / s.splits, split = block - tile * s.splits;
     const RowTile rt = find_tile<TM>(s.plan.offsets, s.plan.E, s.plan.M, tile);
     if (rt.rows <= 0) return;
     const int C = s.C, rank = s.rank;
-    const int c0 = split * s.each, c1 = min(C, c0 + s.each);
-    const T* z[RT];
+    const int c1 = min(C, (split + 1) * s.each);
+    const int h8 = l16 >> 3, l8 = l16 & 7;
+    // the rows that the lane loads: its own, or (KS 2, in whole lines) l8 and 8 + l8 of each tile
+    const T* z[RT][KS];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int at = i * 16 + l16;
-      const int row = at < rt.rows ? row_at(s.plan, rt.first + at) : -1;
-      z[i] = row < 0 ? nullptr : static_cast<const T*>(s.z) + (size_t)row * C;
-    }
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int at = i * 16 + (KS == 2 ? 8 * k + l8 : l16);
+        const int row = at < rt.rows ? row_at(s.plan, rt.first + at) : -1;
+        z[i][k] = row < 0 ? nullptr : static_cast<const T*>(s.z) + (size_t)row * C;
+      }
     const T* w = static_cast<const T*>(s.w) + (size_t)rt.expert * rank * C;
-    uint8_t* stage = smem + wave * (32 * JT * 16 * 2 + 64);
+    uint8_t* stage = smem + wave * STAGE;
+
+    // a step's operands, on their way while the step before is multiplied
+    struct Step {
+      i16x8_t z[RT][KS], w[JT][KS];
+    };
+    auto load = [&](int c, Step& d) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int at = c + 8 * quad + (KS == 2 ? 32 * h8 : 0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) d.z[i][k] = at < c1 && z[i][k] ? load16(z[i][k] + at) : i16x8_t{};
+        if constexpr (!W_T) {
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const int n = j * 16 + (KS == 2 ? 8 * k + l8 : l16);
+            d.w[j][k] = at < c1 && n < rank ? load16(w + (size_t)n * C + at) : i16x8_t{};
+          }
+        } else {   // COLS rows of w, one after the other
+          const int bytes = (min(c1, c + COLS) - c) * rank * 2;
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const int b = ((k * JT + j) * 64 + lane) * 16;
+            d.w[j][k] = b < bytes ? load16(reinterpret_cast<const uint8_t*>(w + (size_t)c * rank) + b) : i16x8_t{};
+          }
+        }
+      }
+    };
     f32x4_t acc[RT][JT] = {};
-    for (int c = c0 + wave * 32; c < c1; c += 128) {
-      const int at = c + 8 * quad;
-      const bool in = at < C;
-      i16x8_t zf[RT], wf[JT];
+    auto multiply = [&](Step& d) {
+      if constexpr (KS == 2) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) zf[i] = in && z[i] ? load16(z[i] + at) : i16x8_t{};
-      if constexpr (!W_T) {
+        for (int i = 0; i < RT; ++i) trade_lines(d.z[i][0], d.z[i][1]);
+        if constexpr (!W_T) {
 #pragma unroll
-        for (int j = 0; j < JT; ++j)
-          wf[j] = in && j * 16 + l16 < rank ? load16(w + (size_t)(j * 16 + l16) * C + at) : i16x8_t{};
-      } else {
-        // 32 rows of w, one after the other, to LDS; zeros behind the last
-        const int bytes = (min(C, c + 32) - c) * rank * 2, all = 32 * rank * 2;
-        i16x8_t v[JT];
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const int b = (j * 64 + lane) * 16;
-          v[j] = b < bytes ? load16(reinterpret_cast<const uint8_t*>(w + (size_t)c * rank) + b) : i16x8_t{};
+          for (int j = 0; j < JT; ++j) trade_lines(d.w[j][0], d.w[j][1]);
         }
+      }
+      if constexpr (W_T) {   // by way of LDS; zeros behind the last row
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const int b = (j * 64 + lane) * 16;
-          if (b < all) *reinterpret_cast<i16x8_t*>(stage + b) = v[j];
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const int b = ((k * JT + j) * 64 + lane) * 16;
+            if (b < COLS * rank * 2) *reinterpret_cast<i16x8_t*>(stage + b) = d.w[j][k];
+          }
         __builtin_amdgcn_wave_barrier();
         const uint8_t* from = stage + (8 * quad + (l16 >> 2)) * rank * 2 + (l16 & 3) * 8;
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          // (columns from the rank on are the next row's, or what lies behind: their sums are not stored)
-          const i16x4_t lo = read_turned(from + j * 32), hi = read_turned(from + 4 * rank * 2 + j * 32);
-          wf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            // (columns from the rank on are the next row's, or what lies behind: their sums are not stored)
+            const uint8_t* at = from + k * 64 * rank + j * 32;
+            const i16x4_t lo = read_turned(at), hi = read_turned(at + 8 * rank);
+            d.w[j][k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
         __builtin_amdgcn_wave_barrier();
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int j = 0; j < JT; ++j) acc[i][j] = mfma16(wf[j], zf[i], acc[i][j], T{});
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) acc[i][j] = mfma16(d.w[j][k], d.z[i][k], acc[i][j], T{});
+    };
+    Step d[2];
+    int c = split * s.each + wave * COLS;
+    if (c < c1) load(c, d[0]);
+    for (; c < c1; c += 8 * COLS) {
+      if (c + 4 * COLS < c1) load(c + 4 * COLS, d[1]);
+      multiply(d[0]);
+      if (c + 4 * COLS >= c1) break;
+      if (c + 8 * COLS < c1) load(c + 8 * COLS, d[0]);
+      multiply(d[1]);
     }
+
     f32x4_t* sums = reinterpret_cast<f32x4_t*>(smem);
     if constexpr (W_T) __syncthreads();
     if (wave) {
@@ -158,7 +235,8 @@ struct Shrink {
 
 // ---------------------------------------------------------------- the second products
 // y[row][n] = base[row][n] + s_e sum_j f[position][j] w[n][j], or w[j][n] (W_T); y's rows without an adapter
-// are base's.  A workgroup takes 16 RT rows of one adapter and kSpan columns, a wave 32 columns in turn.
+// are base's.  A workgroup takes 16 RT rows of one adapter and `span` columns, a wave 32 or 64 columns in turn; the
+// operands of the next are on their way while one is multiplied (before y is stored, which may be base).
 struct ExpandArgs {
   LoraPlan plan;
   const float* parts;
@@ -167,69 +245,114 @@ struct ExpandArgs {
   const float* scales;   // may be null: ones
   const void* base;      // may be null: zeros
   void* y;
-  int row_tiles;   // of the rows with adapters; behind them workgroups for those without
+  int span;            // columns a workgroup, a multiple of 256
+  int row_tiles;       // of the rows with adapters; behind them workgroups for those without
+  int spans;           // of a row
 };
 
-constexpr int kSpan = 512, kCopied = 64;   // columns and, of rows without an adapter, rows a workgroup
+constexpr int kCopied = 64;   // rows without an adapter that a workgroup copies
 
-template <typename T, int JT, int RT, bool W_T>
+template <typename T, int JT, int RT, bool W_T, int CP = JT <= 4 ? 2 : 1>
 struct Expand {
-  static constexpr int TM = 16 * RT, KT = (JT + 1) / 2;
+  static constexpr int kTiles = JT, TM = 16 * RT, KT = (JT + 1) / 2;
+  static constexpr int COLS = 32 * CP;   // columns of a wave's step
   static constexpr int STRIDE = JT * 16 + 4;   // floats a row of f, in LDS
-  // LDS: f's rows, their exponents; W_T: each wave's 32 columns of w, [rank][32]
-  static size_t smem_bytes() { return (size_t)TM * STRIDE * 4 + TM * 4 + (W_T ? 4 * (size_t)KT * 32 * 64 : 0); }
+  static constexpr int STAGE = KT * 32 * COLS * 2;   // bytes
+  // LDS: f's rows, their exponents; W_T: each wave's COLS columns of w, [rank][COLS]
+  static size_t smem_bytes() { return (size_t)TM * STRIDE * 4 + TM * 4 + (W_T ? 4 * (size_t)STAGE : 0); }
 
-  static __device__ __forceinline__ void copy_rows(const ExpandArgs& s, int first) {
-    const int n = blockIdx.y * kSpan + (threadIdx.x & 63) * 8;
-    if (n >= s.N) return;
+  static __device__ __forceinline__ void copy_rows(const ExpandArgs& s, int first, int span) {
+    const int end = min(s.N, (span + 1) * s.span);
     for (int row = first + (threadIdx.x >> 6); row < min(s.plan.M, first + kCopied); row += 4) {
       const int at = s.plan.slot_row[row];
       if (at >= 0 && at < s.plan.M) continue;
-      const size_t to = (size_t)row * s.N + n;
-      *reinterpret_cast<i16x8_t*>(static_cast<T*>(s.y) + to) =
-          s.base ? load16(static_cast<const T*>(s.base) + to) : i16x8_t{};
+      for (int n = span * s.span + (threadIdx.x & 63) * 8; n < end; n += 512) {
+        const size_t to = (size_t)row * s.N + n;
+        *reinterpret_cast<i16x8_t*>(static_cast<T*>(s.y) + to) =
+            s.base ? load16(static_cast<const T*>(s.base) + to) : i16x8_t{};
+      }
     }
   }
 
-  static __device__ __forceinline__ void run(const ExpandArgs& s, uint8_t* smem) {
+  static __device__ __forceinline__ void run(const ExpandArgs& s, int block, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, quad = lane >> 4;
-    const int tile = blockIdx.x, span = blockIdx.y;
+    const int tile = block / s.spans, span = block - tile * s.spans;
     if (tile >= s.row_tiles) {
-      copy_rows(s, (tile - s.row_tiles) * kCopied);
+      copy_rows(s, (tile - s.row_tiles) * kCopied, span);
       return;
     }
     const RowTile rt = find_tile<TM>(s.plan.offsets, s.plan.E, s.plan.M, tile);
     if (rt.rows <= 0) return;
-    const int N = s.N, rank = s.rank;
+    const int N = s.N, rank = s.rank, end = min(N, (span + 1) * s.span);
+    const T* w = static_cast<const T*>(s.w) + (size_t)rt.expert * N * rank;
+    const T* base = static_cast<const T*>(s.base);
+    T* y = static_cast<T*>(s.y);
+    uint8_t* stage = smem + TM * STRIDE * 4 + TM * 4 + wave * STAGE;
+    int rows[RT][CP];   // that the lane loads and stores: its own, or (CP 2, in whole lines) l8 and 8 + l8 of a tile
+    const int h8 = l16 >> 3, l8 = l16 & 7;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < CP; ++c) {
+        const int at = i * 16 + (CP == 2 ? 8 * c + l8 : l16);
+        rows[i][c] = at < rt.rows ? row_at(s.plan, rt.first + at) : -1;
+      }
+    struct Step {
+      i16x8_t w[CP * 2][KT], base[RT][CP];
+    };
+    auto load = [&](int n0, Step& d) {
+      // MFMA row 4 q + r of tile j is column 32 (j / 2) + 8 q + 4 (j % 2) + r, so that a lane holds eight neighbours
+#pragma unroll
+      for (int j = 0; j < CP * 2; ++j)
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          if constexpr (!W_T) {
+            const int n = n0 + 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3), at = k * 32 + 8 * quad;
+            d.w[j][k] = n < N && at < rank ? load16(w + (size_t)n * rank + at) : i16x8_t{};
+          } else {   // COLS columns of w's rows
+            constexpr int EACH = COLS / 8;
+            const int at = (j * KT + k) * (64 / EACH) + lane / EACH, n = n0 + (lane % EACH) * 8;
+            d.w[j][k] = at < rank && n < N ? load16(w + (size_t)at * N + n) : i16x8_t{};
+          }
+        }
+      const int n = n0 + 8 * quad + (CP == 2 ? 32 * h8 : 0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+          d.base[i][c] = base && rows[i][c] >= 0 && n < N ? load16(base + (size_t)rows[i][c] * N + n) : i16x8_t{};
+    };
+    Step d[2];
+    int n0 = span * s.span + wave * COLS;
+    if (n0 < end) load(n0, d[0]);   // (on its way while f is taken)
+
     float* f = reinterpret_cast<float*>(smem);
     int* lifts = reinterpret_cast<int*>(f + TM * STRIDE);
     for (int i = tid * 4; i < TM * JT * 16; i += 1024) {
       const int m = i / (JT * 16), j = i - m * (JT * 16);
       f32x4_t v = {};
-      if (m < rt.rows && j < rank) {
-        const float* at = s.parts + (size_t)(rt.first + m) * rank + j;
-        v = *reinterpret_cast<const f32x4_t*>(at);
-        for (int p = 1; p < s.splits; ++p)
-          v += *reinterpret_cast<const f32x4_t*>(at + (size_t)p * s.plan.M * rank);
-      }
+      if (m < rt.rows && j < rank)
+        v = sum_parts(s.parts + (size_t)(rt.first + m) * rank + j, s.splits, (size_t)s.plan.M * rank);
       *reinterpret_cast<f32x4_t*>(f + m * STRIDE + j) = v;
     }
     __syncthreads();
-    if (tid < TM) {
-      uint32_t top = 0;
-      for (int j = 0; j < JT * 16; ++j) top = max(top, finite_bits(f[tid * STRIDE + j]));
-      lifts[tid] = lift(top, T{});
+    if constexpr (!__is_same(T, __bf16)) {   // four threads a row
+      if (tid < TM * 4) {
+        uint32_t top = 0;
+        for (int j = tid & 3; j < JT * 16; j += 4) top = max(top, finite_bits(f[(tid >> 2) * STRIDE + j]));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+        if ((tid & 3) == 0) lifts[tid >> 2] = lift(top, T{});
+      }
+      __syncthreads();
     }
-    __syncthreads();
     const float scale = s.scales ? s.scales[rt.expert] : 1.0f;
     i16x8_t fh[RT][KT], fl[RT][KT];
     float back[RT];
-    T* y[RT];
-    const T* base[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int m = i * 16 + l16, e = lifts[m];
+      const int m = i * 16 + l16, e = __is_same(T, __bf16) ? 0 : lifts[m];
       const float up = power(e);
       back[i] = power(-e);
 #pragma unroll
@@ -243,73 +366,69 @@ struct Expand {
         fh[i][k] = *reinterpret_cast<i16x8_t*>(hi);
         fl[i][k] = *reinterpret_cast<i16x8_t*>(lo);
       }
-      const int row = m < rt.rows ? row_at(s.plan, rt.first + m) : -1;
-      y[i] = row < 0 ? nullptr : static_cast<T*>(s.y) + (size_t)row * N;
-      base[i] = row < 0 || !s.base ? nullptr : static_cast<const T*>(s.base) + (size_t)row * N;
     }
-    const T* w = static_cast<const T*>(s.w) + (size_t)rt.expert * N * rank;
-    uint8_t* stage = smem + TM * STRIDE * 4 + TM * 4 + wave * KT * 32 * 64;
-    const int end = min(N, (span + 1) * kSpan);
-    for (int n0 = span * kSpan + wave * 32; n0 < end; n0 += 128) {
-      // MFMA row 4 q + r of tile j is column 8 q + 4 j + r, so that a lane holds eight neighbours
-      i16x8_t wf[2][KT];
-      if constexpr (!W_T) {
+
+    auto multiply = [&](int n0, Step& d) {
+      if constexpr (W_T) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = n0 + 8 * (l16 >> 2) + 4 * j + (l16 & 3);
-#pragma unroll
-          for (int k = 0; k < KT; ++k) {
-            const int at = k * 32 + 8 * quad;
-            wf[j][k] = n < N && at < rank ? load16(w + (size_t)n * rank + at) : i16x8_t{};
-          }
-        }
-      } else {
-        i16x8_t v[KT * 2];
-#pragma unroll
-        for (int i = 0; i < KT * 2; ++i) {
-          const int j = i * 16 + (lane >> 2), n = n0 + (lane & 3) * 8;
-          v[i] = j < rank && n < N ? load16(w + (size_t)j * N + n) : i16x8_t{};
-        }
-#pragma unroll
-        for (int i = 0; i < KT * 2; ++i) *reinterpret_cast<i16x8_t*>(stage + (i * 64 + lane) * 16) = v[i];
+        for (int i = 0; i < KT * CP * 2; ++i)
+          *reinterpret_cast<i16x8_t*>(stage + (i * 64 + lane) * 16) = d.w[i / KT][i % KT];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < CP * 2; ++j)
 #pragma unroll
           for (int k = 0; k < KT; ++k) {
-            const uint8_t* from = stage + (k * 32 + 8 * quad + (l16 >> 2)) * 64 + (l16 & 3) * 16 + j * 8;
-            const i16x4_t lo = read_turned(from), hi = read_turned(from + 256);
-            wf[j][k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            const uint8_t* from =
+                stage + (k * 32 + 8 * quad + (l16 >> 2)) * COLS * 2 + (j >> 1) * 64 + (l16 & 3) * 16 + (j & 1) * 8;
+            const i16x4_t lo = read_turned(from), hi = read_turned(from + 4 * COLS * 2);
+            d.w[j][k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           }
         __builtin_amdgcn_wave_barrier();
       }
-      const int n = n0 + 8 * quad;
+      const int n = n0 + 8 * quad + (CP == 2 ? 32 * h8 : 0);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        float v[8] = {};
-        const bool in = y[i] && n < N;
-        if (in && base[i]) load8(base[i] + n, v);
+        if constexpr (CP == 2) trade_lines(d.base[i][0], d.base[i][1]);
+        i16x8_t out[CP];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          f32x4_t acc = {};
+        for (int c = 0; c < CP; ++c) {
+          typedef T T8 __attribute__((ext_vector_type(8)));
+          const T8 b = __builtin_bit_cast(T8, d.base[i][c]);
+          T8 o;
 #pragma unroll
-          for (int k = 0; k < KT; ++k) {
-            acc = mfma16(wf[j][k], fl[i][k], acc, T{});
-            acc = mfma16(wf[j][k], fh[i][k], acc, T{});
+          for (int j = 0; j < 2; ++j) {
+            f32x4_t acc = {};
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+              acc = mfma16(d.w[2 * c + j][k], fl[i][k], acc, T{});
+              acc = mfma16(d.w[2 * c + j][k], fh[i][k], acc, T{});
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[4 * j + r] = (T)fmaf(scale, acc[r] * back[i], (float)b[4 * j + r]);
           }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[4 * j + r] = fmaf(scale, acc[r] * back[i], v[4 * j + r]);
+          out[c] = __builtin_bit_cast(i16x8_t, o);
         }
-        if (in) store8(y[i] + n, v);
+        if constexpr (CP == 2) trade_lines(out[0], out[1]);
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+          if (rows[i][c] >= 0 && n < N) *reinterpret_cast<i16x8_t*>(y + (size_t)rows[i][c] * N + n) = out[c];
       }
+    };
+    for (; n0 < end; n0 += 8 * COLS) {
+      if (n0 + 4 * COLS < end) load(n0 + 4 * COLS, d[1]);
+      multiply(n0, d[0]);
+      if (n0 + 4 * COLS >= end) break;
+      if (n0 + 8 * COLS < end) load(n0 + 8 * COLS, d[0]);
+      multiply(n0 + 4 * COLS, d[1]);
     }
   }
 };
 
 // ---------------------------------------------------------------- the adapters' gradients
 // out[c][j] (or out[j][c], J_FIRST) = s_e sum over the adapter's positions p of z[row(p)][c] f[p][j].
-// A workgroup takes 64 columns of one adapter and a part of its rows, 64 at a time: z's rows and f's two
-// terms go to LDS and both operands are read transposed.  Each wave has 16 columns.
+// A workgroup takes 128 columns of one adapter and a part of its rows, 64 at a time: z's rows and f's two
+// terms go to LDS and both operands are read transposed; the next 64 rows are on their way meanwhile.  Each
+// wave has 32 columns.
 struct LoraGradArgs {
   LoraPlan plan;
   const void* z;      // [M][C]
@@ -322,51 +441,58 @@ struct LoraGradArgs {
 
 template <typename T, int JT, bool J_FIRST>
 struct LoraGrad {
-  static constexpr int FROW = JT * 32;   // bytes
-  static size_t smem_bytes() { return 64 * 128 + 2 * 64 * FROW + 64; }
+  static constexpr int COLS = 128, FROW = JT * 32;   // bytes a row of f's terms
+  static size_t smem_bytes() { return 64 * COLS * 2 + 2 * 64 * FROW + 64; }
 
-  static __device__ __forceinline__ void run(const LoraGradArgs& s, uint8_t* smem) {
+  static __device__ __forceinline__ void run(const LoraGradArgs& s, int block, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, quad = lane >> 4;
-    const int col_tiles = (s.C + 63) / 64;
-    const int e = blockIdx.x / (col_tiles * s.splits), in = blockIdx.x - e * col_tiles * s.splits;
-    const int split = in / col_tiles, c0 = (in - split * col_tiles) * 64;
+    const int col_tiles = (s.C + COLS - 1) / COLS;
+    const int e = block / (col_tiles * s.splits), in = block - e * col_tiles * s.splits;
+    const int split = in / col_tiles, c0 = (in - split * col_tiles) * COLS;
     const int lo = min(max(s.plan.offsets[e], 0), s.plan.M), hi = min(max(s.plan.offsets[e + 1], lo), s.plan.M);
     const int each = ((hi - lo + s.splits - 1) / s.splits + 63) / 64 * 64;
     const int p0 = min(hi, lo + split * each), p1 = min(hi, p0 + each);
     const int rank = s.rank;
-    uint8_t *zt = smem, *fh = smem + 64 * 128, *fl = fh + 64 * FROW;
+    uint8_t *zt = smem, *fh = smem + 64 * COLS * 2, *fl = fh + 64 * FROW;
     uint32_t* tops = reinterpret_cast<uint32_t*>(fl + 64 * FROW);
-    f32x4_t acc[JT] = {};
-    int lifted = 100;   // the sums are of f times 2^lifted
-    for (int p = p0; p < p1; p += 64) {
+    auto turn = [](int row) { return 2 * ((row & 3) + 4 * ((row >> 3) & 1)); };   // of a row's 16 pieces
+
+    i16x8_t zv[4];
+    f32x4_t fv[JT];
+    const int zrow = tid >> 4, zc = c0 + (tid & 15) * 8;   // rows zrow, + 16, + 32, + 48
+    int rows[4];   // of the step that is loaded next
+    auto load_rows = [&](int p) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = i * 32 + (tid >> 3), c = c0 + (tid & 7) * 8;
-        const int row = p + at < p1 ? row_at(s.plan, p + at) : -1;
-        const i16x8_t v =
-            row >= 0 && c < s.C ? load16(static_cast<const T*>(s.z) + (size_t)row * s.C + c) : i16x8_t{};
-        *reinterpret_cast<i16x8_t*>(zt + at * 128 + (((tid & 7) ^ (2 * (((at >> 1) & 1) + 2 * ((at >> 3) & 1)))) << 4)) = v;
+      for (int i = 0; i < 4; ++i) {
+        const int at = p + i * 16 + zrow;
+        rows[i] = at < p1 ? row_at(s.plan, at) : -1;
       }
-      float v[JT * 4];
-      uint32_t top = 0;
+    };
+    auto load = [&](int p) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        zv[i] = rows[i] >= 0 && zc < s.C ? load16(static_cast<const T*>(s.z) + (size_t)rows[i] * s.C + zc) : i16x8_t{};
+      load_rows(p + 64);
 #pragma unroll
       for (int i = 0; i < JT; ++i) {
-        const int at = (i * 256 + tid) / (JT * 4), j = ((i * 256 + tid) % (JT * 4)) * 4;
-        f32x4_t t = {};
-        if (p + at < p1 && j < rank && row_at(s.plan, p + at) >= 0) {
-          const float* from = s.f + (size_t)(p + at) * rank + j;
-          t = *reinterpret_cast<const f32x4_t*>(from);
-          for (int q = 1; q < s.f_splits; ++q)
-            t += *reinterpret_cast<const f32x4_t*>(from + (size_t)q * s.plan.M * rank);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[i * 4 + r] = t[r];
-          top = max(top, finite_bits(t[r]));
-        }
+        const int at = p + (i * 256 + tid) / (JT * 4), j = ((i * 256 + tid) % (JT * 4)) * 4;
+        fv[i] = f32x4_t{};
+        if (at < p1 && j < rank)   // (f of a position without a row is zero)
+          fv[i] = sum_parts(s.f + (size_t)at * rank + j, s.f_splits, (size_t)s.plan.M * rank);
       }
-      if constexpr (sizeof(T) == 2 && !__is_same(T, __bf16)) {
+    };
+    f32x4_t acc[2][JT] = {};
+    int lifted = 100;   // the sums are of f times 2^lifted
+    load_rows(p0);
+    if (p0 < p1) load(p0);
+    for (int p = p0; p < p1; p += 64) {
+      if constexpr (!__is_same(T, __bf16)) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < JT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = max(top, finite_bits(fv[i][r]));
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
         if (lane == 0) tops[wave] = top;
@@ -377,9 +503,11 @@ struct LoraGrad {
           // (sums so far are zero while lifted is 100, or were of values that this leaves in range)
           const float by = up - lifted < -126 ? 0.0f : power(up - lifted);
 #pragma unroll
-          for (int j = 0; j < JT; ++j)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] *= by;
+            for (int j = 0; j < JT; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[c][j][r] *= by;
           lifted = up;
         }
       } else {
@@ -387,14 +515,20 @@ struct LoraGrad {
       }
       const float up = power(lifted);
 #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = i * 16 + zrow;
+        *reinterpret_cast<i16x8_t*>(zt + at * COLS * 2 + (((tid & 15) ^ turn(at)) << 4)) = zv[i];
+      }
+#pragma unroll
       for (int i = 0; i < JT; ++i) {
         const int at = (i * 256 + tid) / (JT * 4), j = ((i * 256 + tid) % (JT * 4)) * 4;
         T h4[4], l4[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) two_terms(v[i * 4 + r] * up, h4[r], l4[r]);
+        for (int r = 0; r < 4; ++r) two_terms(fv[i][r] * up, h4[r], l4[r]);
         *reinterpret_cast<i16x4_t*>(fh + at * FROW + j * 2) = *reinterpret_cast<i16x4_t*>(h4);
         *reinterpret_cast<i16x4_t*>(fl + at * FROW + j * 2) = *reinterpret_cast<i16x4_t*>(l4);
       }
+      if (p + 64 < p1) load(p + 64);
       __syncthreads();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -403,19 +537,24 @@ struct LoraGrad {
           const i16x4_t x = read_turned(a), y = read_turned(a + 4 * stride);
           return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         };
-        const int turn = 2 * (((row >> 1) & 1) + 2 * ((row >> 3) & 1));
-        const i16x8_t zf =
-            two(zt + row * 128 + (((2 * wave + ((l16 & 3) >> 1)) ^ turn) << 4) + (l16 & 1) * 8, 128);
+        i16x8_t zf[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          zf[c] = two(zt + row * COLS * 2 + (((4 * wave + 2 * c + ((l16 & 3) >> 1)) ^ turn(row)) << 4) + (l16 & 1) * 8,
+                      COLS * 2);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           const int at = row * FROW + j * 32 + (l16 & 3) * 8;
           const i16x8_t a = two(fl + at, FROW), b = two(fh + at, FROW);
-          if constexpr (J_FIRST) {
-            acc[j] = mfma16(zf, a, acc[j], T{});
-            acc[j] = mfma16(zf, b, acc[j], T{});
-          } else {
-            acc[j] = mfma16(a, zf, acc[j], T{});
-            acc[j] = mfma16(b, zf, acc[j], T{});
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (J_FIRST) {
+              acc[c][j] = mfma16(zf[c], a, acc[c][j], T{});
+              acc[c][j] = mfma16(zf[c], b, acc[c][j], T{});
+            } else {
+              acc[c][j] = mfma16(a, zf[c], acc[c][j], T{});
+              acc[c][j] = mfma16(b, zf[c], acc[c][j], T{});
+            }
           }
         }
       }
@@ -424,22 +563,24 @@ struct LoraGrad {
     const float back = power(-lifted);
     const float scale = s.scales ? s.scales[e] : 1.0f;
 #pragma unroll
-    for (int j = 0; j < JT; ++j) {
-      // a lane's four sums: J_FIRST four neighbouring c of one j, else four j of one c
-      const int c = c0 + wave * 16 + (J_FIRST ? 4 * quad : l16), at = j * 16 + (J_FIRST ? l16 : 4 * quad);
-      if (c >= s.C || at >= rank) continue;
-      const size_t to = J_FIRST ? ((size_t)e * rank + at) * s.C + c : ((size_t)e * s.C + c) * rank + at;
-      f32x4_t v = acc[j] * back;
-      if (s.splits > 1) {
-        *reinterpret_cast<f32x4_t*>(static_cast<float*>(s.out) + (size_t)split * s.plan.E * rank * s.C + to) = v;
-      } else {
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        T4 o;
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = (T)(scale * v[r]);
-        *reinterpret_cast<T4*>(static_cast<T*>(s.out) + to) = o;
+      for (int j = 0; j < JT; ++j) {
+        // a lane's four sums: J_FIRST four neighbouring c of one j, else four j of one c
+        const int c = c0 + wave * 32 + k * 16 + (J_FIRST ? 4 * quad : l16), at = j * 16 + (J_FIRST ? l16 : 4 * quad);
+        if (c >= s.C || at >= rank) continue;
+        const size_t to = J_FIRST ? ((size_t)e * rank + at) * s.C + c : ((size_t)e * s.C + c) * rank + at;
+        const f32x4_t v = acc[k][j] * back;
+        if (s.splits > 1) {
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(s.out) + (size_t)split * s.plan.E * rank * s.C + to) = v;
+        } else {
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          T4 o;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] = (T)(scale * v[r]);
+          *reinterpret_cast<T4*>(static_cast<T*>(s.out) + to) = o;
+        }
       }
-    }
   }
 };
 

@@ -120,6 +120,41 @@ def test_product_gradients(kind, wide, rows, E, N, K):
     assert none is None and torch.equal(only_w, dw)
 
 
+# many units of the largest tile (dealt out from queues, both gradients in one launch), more experts than XCDs
+# and not a multiple of them, many small experts, and few units with a long summed dimension (in parts)
+LARGE = [(30000, 20, 1032, 1544), (24000, 3, 2056, 1032), (12000, 1, 3096, 1032), (3000, 1000, 24, 40), (33, 1, 136, 8200),
+         (70, 2, 8200, 72), (9000, 1, 72, 136), (20000, 2, 264, 64)]
+
+
+@pytest.mark.parametrize("kind,wide", [("bf16", False), ("f16", True)])
+@pytest.mark.parametrize("rows,E,N,K", LARGE)
+def test_products_of_many_and_of_few_units(kind, wide, rows, E, N, K):
+    rng = np.random.default_rng(rows + N)
+    a, w, off = activations(rng, rows, K, kind), normal(rng, E, N, K, kind=kind, size=0.1), ranges(rng, rows, E)
+    dc = normal(rng, rows, N, kind=kind)
+    out = "f32" if wide else kind
+    t = TYPES[out][0]
+    c, da = (torch.full((rows, n), -3.0, dtype=t, device=DEV) for n in (N, K))
+    Z.zinc_moe_gemm(a, w, dev(off), out=c)
+    _, dw = Z.zinc_moe_gemm_backward(dc, a, w, dev(off), da=da, dw_dtype=t)
+    ah, wh, dch = host(a), host(w), host(dc)
+    am, wm, dm = np.abs(ah), np.abs(wh), np.abs(dch)
+    close(c, R.moe_gemm(ah, wh, off, np.full((rows, N), -3.0)),
+          sums(K) * R.moe_gemm(am, wm, off, np.zeros((rows, N))), out, "c")
+    want_a, want_w = R.moe_gemm_backward(dch, ah, wh, off, np.full((rows, K), -3.0))
+    size_a, size_w = R.moe_gemm_backward(dm, am, wm, off, np.zeros((rows, K)))
+    close(da, want_a, sums(N) * size_a, out, "da")
+    close(dw, want_w, sums(rows) * size_w, out, "dw")
+    alone = Z.zinc_moe_gemm_backward(dc, a, w, dev(off), da_dtype=t, want_dw=False)[0]
+    assert torch.equal(alone[off[0]:off[-1]], da[off[0]:off[-1]])
+    assert torch.equal(Z.zinc_moe_gemm_backward(dc, a, w, dev(off), dw_dtype=t, want_da=False)[1], dw)
+    # the rows in other places of the same call
+    for _ in range(2):
+        again = torch.full_like(c, -3.0)
+        Z.zinc_moe_gemm(a, w, dev(off), out=again)
+        assert torch.equal(again, c)
+
+
 @pytest.mark.parametrize("rows,E", [(1, 1), (40, 3), (700, 2), (2000, 3)])
 def test_products_keep_nan_in_its_place(rows, E):
     """Rows outside the ranges, other experts' rows and weights, and what lies behind a row's end add nothing."""
