@@ -37,6 +37,22 @@ __device__ __forceinline__ i16x4_t read_turned(const uint8_t* lds) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)lds);
 }
 
+// Rows in whole 128-byte lines.  As an MFMA operand lane l of 16 holds row l's pieces q and q + 4 (16 bytes
+// each, q its quarter of the wave); a load of piece q + 4 (l / 8) of row l % 8, and one of row 8 + l % 8, take
+// two such quarters of 8 rows each, which is 128 bytes a row.  The lower lanes' second load and the upper
+// lanes' first then change places; to store, the same again.  (8192 x 11008 values read and written by 64-byte
+// pieces 95 us, by 128 75, by 256 and 1024 74.)
+__device__ __forceinline__ void trade_lines(i32x4_t& first, i32x4_t& second) {
+  const bool low = (threadIdx.x & 8) == 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = first[i], y = second[i], give = low ? y : x;
+    const int get = __builtin_amdgcn_update_dpp(give, give, 0x128, 0xF, 0xF, false);   // row_ror:8
+    first[i] = low ? x : get;
+    second[i] = low ? get : y;
+  }
+}
+
 struct Gemm16Args {
   const void* p;    // a, or dc
   const void* q;    // w, or a
@@ -55,18 +71,21 @@ struct Gemm16 {
   static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
   static constexpr bool P_T = F == kWeight, Q_T = F != kForward;   // summed over rows of the matrix
   // Columns of two neighbouring 16-wide tiles taken in turns of four, so that a lane's sums are eight
-  // neighbours.  The transposing reads would meet two to a bank so; their lanes hold two times four.
+  // neighbours.  The transposing reads would meet two to a bank so; their lanes hold two times four, and trade them
+  // where 16-bit outputs are stored.
   static constexpr bool WIDE = !Q_T;
   static constexpr int PI = TM / 8 / WAVES, QI = TN / 8 / WAVES, COPIES = PI + QI;   // copies a wave, a step
   static constexpr int BUFFER = (TM + TN) * 128;
   static constexpr int NBUF = BUFFERS;
   static constexpr int BAND = 8;   // row tiles walked per column
-  // fp32 gradients of the weights are stored past the caches
-  static constexpr bool STREAMED = F == kWeight && sizeof(O) == 4;
+  // Large tiles' outputs are stored past the caches, in whole lines: 32768 rows of 64 experts, 768 x 2048, dw in fp32
+  // 143 us, in lines that the caches hold 180, in half lines 166 and 183 (half as much again is written); da
+  // 118 and 131.
+  static constexpr bool STREAMED = TN == 256;
   // workgroups a CU holds by registers
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
   static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 4 == 0, "whole copies");
-  static_assert(MT >= 4 && NT % 2 == 0, "tile shape");
+  static_assert(MT >= 4 && (NT == 2 || NT == 4), "tile shape");
   static_assert((!P_T || WAVES * (512 / TM) % 16 == 0) && (!Q_T || WAVES * (512 / TN) % 16 == 0),
                 "a lane's turn is the same in all of its copies");
 
@@ -400,32 +419,50 @@ struct Gemm16 {
     const size_t first = F == kWeight ? (size_t)cu.expert * g.N + cu.p0 : (size_t)cu.first;
     const Buffer c = tile_buffer(static_cast<const uint8_t*>(g.c) + (cu.split * g.part + first * cols) * sizeof(O),
                                  rows * cols * (int)sizeof(O));
-    constexpr int NT_STORE = STREAMED ? 2 : 0;
-    const int n0 = cu.q0 + wn * (TN / WN), at = (wm * (TM / WM) + l16) * cols;
+    constexpr int AUX = STREAMED ? 2 : 0;
+    const int n0 = cu.q0 + wn * (TN / WN), m0 = wm * (TM / WM), h8 = l16 >> 3, l8 = l16 & 7;
+    auto put = [&](i32x4_t v, int row, int n) {
+      __builtin_amdgcn_raw_buffer_store_b128(v, c, n < cols ? (row * cols + n) * (int)sizeof(O) : 0x7FFFFFF0, 0, AUX);
+    };
+    // Two 16-byte pieces of a row, from columns n and m on, as whole lines of two rows.
+    auto put_two = [&](i32x4_t first, i32x4_t second, int i, int n, int m) {
+      trade_lines(first, second);
+      put(first, m0 + i * 16 + l8, n0 + (h8 ? m : n));
+      put(second, m0 + i * 16 + 8 + l8, n0 + (h8 ? m : n));
+    };
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
+      if constexpr (sizeof(O) == 4) {
 #pragma unroll
-      for (int j = 0; j < NT; j += WIDE ? 2 : 1) {
-        const int n = n0 + j * 16 + (WIDE ? 8 : 4) * quad;
-        const int off = n < cols ? (at + i * 16 * cols + n) * (int)sizeof(O) : 0x7FFFFFF0;
-        if constexpr (sizeof(O) == 4) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, acc[i][j]), c, off, 0, NT_STORE);
-          if constexpr (WIDE)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, acc[i][j + 1]), c, off + 16, 0, NT_STORE);
-        } else if constexpr (WIDE) {
+        for (int j = 0; j < NT; j += 2)
+          put_two(__builtin_bit_cast(i32x4_t, acc[i][j]), __builtin_bit_cast(i32x4_t, acc[i][j + 1]), i,
+                  16 * j + (WIDE ? 8 : 4) * quad, WIDE ? 16 * j + 8 * quad + 4 : 16 * j + 16 + 4 * quad);
+      } else {
+        i32x4_t v[NT / 2];
+        const int at = WIDE ? 8 * quad : 16 * (quad & 1) + 8 * (quad >> 1);
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
           typedef O O8 __attribute__((ext_vector_type(8)));
           O8 o;
 #pragma unroll
           for (int r = 0; r < 8; ++r) o[r] = (O)acc[i][j + (r >> 2)][r & 3];
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, o), c, off, 0, NT_STORE);
-        } else {
-          typedef O O4 __attribute__((ext_vector_type(4)));
-          typedef int i32x2_t __attribute__((ext_vector_type(2)));
-          O4 o;
+          v[j / 2] = __builtin_bit_cast(i32x4_t, o);
+          if constexpr (!WIDE) {
+            // columns 4 q .. + 3 of the tiles j and j + 1 to 8 (q / 2) .. + 7 of tile j + q % 2: quarters 1 and 3 of
+            // the one change places with 0 and 2 of the other
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = (O)acc[i][j][r];
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2_t, o), c, off, 0, NT_STORE);
+            for (int d = 0; d < 2; ++d) {
+              const auto both =
+                  __builtin_amdgcn_permlane16_swap((uint32_t)v[j / 2][d], (uint32_t)v[j / 2][2 + d], false, false);
+              v[j / 2][d] = (int)both[0];
+              v[j / 2][2 + d] = (int)both[1];
+            }
+          }
         }
+        if constexpr (NT == 4)
+          put_two(v[0], v[1], i, at, 32 + at);
+        else
+          put(v[0], m0 + i * 16 + l16, n0 + at);
       }
     }
   }

@@ -1,6 +1,7 @@
 // Both gradients of a 16-bit product by expert.  Where both are many units of the largest tile, one launch
 // computes them: a workgroup that finds no more units of da goes on with those of dw, the experts with most
-// rows first, so the last round of the one and the stores of the other are work for the same CUs.
+// rows first, so the last round of the one is work for the same CUs (32768 rows of 64 experts, 768 x 2048, dw in
+// fp32, operands from HBM: 310 us, in two launches 323; where every second workgroup begins with dw 330).
 #include "gemm16_launch.hpp"
 
 namespace zinc {

@@ -66,9 +66,9 @@ hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, co
   const size_t part = lora_part_bytes(M, rank);
   float* parts_a = reinterpret_cast<float*>(at + 2 * part);
   float* parts_b = reinterpret_cast<float*>(at + 2 * part + grad_bytes(M, E, rank, K));
-  const ShrinkArgs h = shrink_of(plan, x, a, K, rank, reinterpret_cast<float*>(at));
-  const ShrinkArgs dh = shrink_of(plan, dy, b, N, rank, reinterpret_cast<float*>(at + part));
-  const ExpandArgs ex = expand_of(kSecondTurned, dh, a, K, scales, base, dx);
+  const ShrinkArgs h = shrink_of(false, plan, x, a, K, rank, reinterpret_cast<float*>(at));
+  const ShrinkArgs dh = shrink_of(false, plan, dy, b, N, rank, reinterpret_cast<float*>(at + part));
+  const ExpandArgs ex = expand_of(false, dh, a, K, scales, base, dx);
   const int sa = grad_splits(M, E, K), sb = grad_splits(M, E, N);
   const LoraGradArgs ga{plan, x, dh.parts, dh.splits, rank, K, scales, sa, sa > 1 ? static_cast<void*>(parts_a) : da};
   const LoraGradArgs gb{plan, dy, h.parts, h.splits, rank, N, scales, sb, sb > 1 ? static_cast<void*>(parts_b) : db};
@@ -85,7 +85,7 @@ hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, co
     hipError_t e = allow_lds<H>(reinterpret_cast<const void*>(&k_lora_firsts<H, DH>), kLds);
     if (e == hipSuccess) e = allow_lds<DX>(reinterpret_cast<const void*>(&k_lora_seconds<DX, DA, DB>), kLds);
     if (e != hipSuccess) return e;
-    const long long h_blocks = M && db ? shrink_blocks(h) : 0, dh_blocks = M && (dx || da) ? shrink_blocks(dh) : 0;
+    const long long h_blocks = M && db ? shrink_blocks(false, h) : 0, dh_blocks = M && (dx || da) ? shrink_blocks(false, dh) : 0;
     if (h_blocks + dh_blocks) {
       hipLaunchKernelGGL((k_lora_firsts<H, DH>), dim3((unsigned)(h_blocks + dh_blocks)), dim3(256), first, stream, h, dh,
                          (int)h_blocks);

@@ -9,7 +9,7 @@
 namespace zinc {
 namespace {
 
-template <typename T>
+template <typename T, bool STREAMED>
 __global__ __launch_bounds__(256) void k_swiglu(const T* __restrict__ gate, const T* __restrict__ up, size_t n,
                                                 T* __restrict__ h) {
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (size_t)gridDim.x * 2048) {
@@ -21,11 +21,11 @@ __global__ __launch_bounds__(256) void k_swiglu(const T* __restrict__ gate, cons
       const Sigmoid s = sigmoid(g[r]);
       v[r] = (u[r] * s.factor) * (g[r] * s.value) * s.factor;
     }
-    store8(h + i, v);
+    store8<STREAMED>(h + i, v);
   }
 }
 
-template <typename T>
+template <typename T, bool STREAMED>
 __global__ __launch_bounds__(256) void k_swiglu_backward(const T* __restrict__ dh, const T* __restrict__ gate,
                                                          const T* __restrict__ up, size_t n, T* __restrict__ dgate,
                                                          T* __restrict__ dup) {
@@ -41,27 +41,42 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(const T* __restrict__ d
       dg[r] = (d[r] * s.factor * slope) * (u[r] * s.factor);
       du[r] = (d[r] * s.factor) * (g[r] * s.value) * s.factor;
     }
-    store8(dgate + i, dg);
-    store8(dup + i, du);
+    store8<STREAMED>(dgate + i, dg);
+    store8<STREAMED>(dup + i, du);
   }
 }
 
+// Outputs that the last-level cache (256 MB) does not hold beside the inputs are stored past the caches: 8192 x
+// 11008 bf16 98.0 us against 99.4, its gradients 168.6 against 170.5.
 template <typename T>
 void forward(const void* gate, const void* up, size_t n, void* h, unsigned blocks, hipStream_t stream) {
-  hipLaunchKernelGGL(k_swiglu<T>, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(gate),
-                     static_cast<const T*>(up), n, static_cast<T*>(h));
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(gate),
+                       static_cast<const T*>(up), n, static_cast<T*>(h));
+  };
+  if (3 * n * sizeof(T) > (256u << 20))
+    run(k_swiglu<T, true>);
+  else
+    run(k_swiglu<T, false>);
 }
 template <typename T>
 void backward(const void* dh, const void* gate, const void* up, size_t n, void* dgate, void* dup, unsigned blocks,
               hipStream_t stream) {
-  hipLaunchKernelGGL(k_swiglu_backward<T>, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(dh),
-                     static_cast<const T*>(gate), static_cast<const T*>(up), n, static_cast<T*>(dgate),
-                     static_cast<T*>(dup));
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, static_cast<const T*>(dh),
+                       static_cast<const T*>(gate), static_cast<const T*>(up), n, static_cast<T*>(dgate),
+                       static_cast<T*>(dup));
+  };
+  if (5 * n * sizeof(T) > (256u << 20))
+    run(k_swiglu_backward<T, true>);
+  else
+    run(k_swiglu_backward<T, false>);
 }
 
+// One round of 2048 values a workgroup (8192 x 11008: 99.4 us; eight rounds 102 - 105).
 unsigned blocks_for(size_t n) {
   const size_t blocks = (n + 2047) / 2048;
-  return (unsigned)(blocks < 8192 ? blocks : 8192);
+  return (unsigned)(blocks < 65536 ? blocks : 65536);
 }
 
 }  // namespace

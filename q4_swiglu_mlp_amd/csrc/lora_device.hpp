@@ -52,24 +52,12 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7F800000u ? b : 0u;
 }
 
-// Rows in whole 128-byte lines.  As an MFMA operand lane l of 16 holds row l's pieces q and q + 4 (16 bytes
-// each, q its quarter of the wave); a load of piece q + 4 (l / 8) of row l % 8, and one of row 8 + l % 8, take
-// two such quarters of 8 rows each, which is 128 bytes a row.  The lower lanes' second load and the upper
-// lanes' first then change places; to store, the same again.  (8192 x 11008 read and written by 64-byte
-// pieces 95 us, by 128 75, by 256 and 1024 74.)
+// trade_lines of operands as the MFMAs take them.
 __device__ __forceinline__ void trade_lines(i16x8_t& first, i16x8_t& second) {
-  const bool low = (threadIdx.x & 8) == 0;
-  const i32x4_t x = __builtin_bit_cast(i32x4_t, first), y = __builtin_bit_cast(i32x4_t, second);
-  i32x4_t a, b;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int give = low ? y[i] : x[i];
-    const int get = __builtin_amdgcn_update_dpp(give, give, 0x128, 0xF, 0xF, false);   // row_ror:8
-    a[i] = low ? x[i] : get;
-    b[i] = low ? get : y[i];
-  }
-  first = __builtin_bit_cast(i16x8_t, a);
-  second = __builtin_bit_cast(i16x8_t, b);
+  i32x4_t x = __builtin_bit_cast(i32x4_t, first), y = __builtin_bit_cast(i32x4_t, second);
+  trade_lines(x, y);
+  first = __builtin_bit_cast(i16x8_t, x);
+  second = __builtin_bit_cast(i16x8_t, y);
 }
 
 // Four values of f: the sum of their parts in order, four parts in flight.
@@ -246,11 +234,12 @@ struct ExpandArgs {
   const void* base;      // may be null: zeros
   void* y;
   int span;            // columns a workgroup, a multiple of 256
-  int row_tiles;       // of the rows with adapters; behind them workgroups for those without
+  int row_tiles;       // of the rows with adapters
   int spans;           // of a row
+  int copies;          // before them: groups of kCopied rows, of which those without an adapter are copied
 };
 
-constexpr int kCopied = 64;   // rows without an adapter that a workgroup copies
+constexpr int kCopied = 64;
 
 template <typename T, int JT, int RT, bool W_T, int CP = JT <= 4 ? 2 : 1>
 struct Expand {
@@ -258,18 +247,39 @@ struct Expand {
   static constexpr int COLS = 32 * CP;   // columns of a wave's step
   static constexpr int STRIDE = JT * 16 + 4;   // floats a row of f, in LDS
   static constexpr int STAGE = KT * 32 * COLS * 2;   // bytes
+  // Many rows of base and y pass the caches by, where they move in whole lines: 8192 x 11008, rank 64 92 us
+  // through the caches, 88 with y past them, 84 with both; rank 16 76, 71 and 67.
+  static constexpr bool STREAMED = CP == 2 && RT > 1;
+  static __device__ __forceinline__ i16x8_t load_base(const T* p) {
+    if constexpr (STREAMED)
+      return __builtin_nontemporal_load(reinterpret_cast<const i16x8_t*>(p));
+    else
+      return load16(p);
+  }
   // LDS: f's rows, their exponents; W_T: each wave's COLS columns of w, [rank][COLS]
   static size_t smem_bytes() { return (size_t)TM * STRIDE * 4 + TM * 4 + (W_T ? 4 * (size_t)STAGE : 0); }
 
+  // Of kCopied rows those without an adapter; a wave takes a quarter of them, four at a time.
   static __device__ __forceinline__ void copy_rows(const ExpandArgs& s, int first, int span) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int at = first + lane < s.plan.M ? s.plan.slot_row[first + lane] : 0;
+    uint32_t left = (uint32_t)(__ballot(at < 0 || at >= s.plan.M) >> (16 * wave)) & 0xFFFFu;
     const int end = min(s.N, (span + 1) * s.span);
-    for (int row = first + (threadIdx.x >> 6); row < min(s.plan.M, first + kCopied); row += 4) {
-      const int at = s.plan.slot_row[row];
-      if (at >= 0 && at < s.plan.M) continue;
-      for (int n = span * s.span + (threadIdx.x & 63) * 8; n < end; n += 512) {
-        const size_t to = (size_t)row * s.N + n;
-        *reinterpret_cast<i16x8_t*>(static_cast<T*>(s.y) + to) =
-            s.base ? load16(static_cast<const T*>(s.base) + to) : i16x8_t{};
+    while (left) {
+      int rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rows[i] = left ? first + 16 * wave + (int)__builtin_ctz(left) : -1;
+        left &= left - 1;   // (0 stays 0)
+      }
+      for (int c = span * s.span + lane * 8; c < end; c += 512) {
+        i16x8_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = rows[i] >= 0 && s.base ? load16(static_cast<const T*>(s.base) + (size_t)rows[i] * s.N + c) : i16x8_t{};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (rows[i] >= 0) *reinterpret_cast<i16x8_t*>(static_cast<T*>(s.y) + (size_t)rows[i] * s.N + c) = v[i];
       }
     }
   }
@@ -278,11 +288,11 @@ struct Expand {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, quad = lane >> 4;
     const int tile = block / s.spans, span = block - tile * s.spans;
-    if (tile >= s.row_tiles) {
-      copy_rows(s, (tile - s.row_tiles) * kCopied, span);
+    if (tile < s.copies) {
+      copy_rows(s, tile * kCopied, span);
       return;
     }
-    const RowTile rt = find_tile<TM>(s.plan.offsets, s.plan.E, s.plan.M, tile);
+    const RowTile rt = find_tile<TM>(s.plan.offsets, s.plan.E, s.plan.M, tile - s.copies);
     if (rt.rows <= 0) return;
     const int N = s.N, rank = s.rank, end = min(N, (span + 1) * s.span);
     const T* w = static_cast<const T*>(s.w) + (size_t)rt.expert * N * rank;
@@ -321,7 +331,8 @@ struct Expand {
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int c = 0; c < CP; ++c)
-          d.base[i][c] = base && rows[i][c] >= 0 && n < N ? load16(base + (size_t)rows[i][c] * N + n) : i16x8_t{};
+          d.base[i][c] =
+              base && rows[i][c] >= 0 && n < N ? load_base(base + (size_t)rows[i][c] * N + n) : i16x8_t{};
     };
     Step d[2];
     int n0 = span * s.span + wave * COLS;
@@ -411,7 +422,8 @@ struct Expand {
         if constexpr (CP == 2) trade_lines(out[0], out[1]);
 #pragma unroll
         for (int c = 0; c < CP; ++c)
-          if (rows[i][c] >= 0 && n < N) *reinterpret_cast<i16x8_t*>(y + (size_t)rows[i][c] * N + n) = out[c];
+          if (rows[i][c] >= 0 && n < N)
+            store_vector<STREAMED>(reinterpret_cast<i16x8_t*>(y + (size_t)rows[i][c] * N + n), out[c]);
       }
     };
     for (; n0 < end; n0 += 8 * COLS) {

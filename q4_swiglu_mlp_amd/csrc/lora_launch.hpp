@@ -9,22 +9,22 @@ namespace zinc {
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Row tiles of 16 a workgroup takes: one where adapters have few rows, else as many as the registers hold
-// with two workgroups a CU.  8192 rows, eight adapters, 4096 to 11008, us: the second product of rank 16 74
-// with two, 80 with four, 75 with one; of rank 32 78 and 81; of rank 64 104 with two, 91 with four, but 101 and 115
-// where its matrix is turned (dx); the first of rank 16 15 - 17 with any, of rank 64 27 with two, 40 with one.
-enum LoraProduct { kFirst, kSecond, kSecondTurned };
-inline int lora_row_tiles(int M, int E, int rank, LoraProduct p) {
+// with two workgroups a CU.  8192 rows, eight adapters, 4096 to 11008, us: the second product through the
+// caches of rank 16 74 with two, 80 with four, 75 with one; of rank 32 78 and 81; of rank 64 104 with two, 91 with
+// four, but 101 and 115 where its matrix is turned (dx); the first of rank 16 15 - 17 with any, of rank 64 27 with two, 40 with one.
+// Of the forward call's first product, 23 with four in one workgroup a CU.
+inline int lora_row_tiles(int M, int E, int rank, bool forward) {
   if (M / E <= 24 || rank > 128) return 1;
-  return p == kSecond && rank > 32 && rank <= 64 ? 4 : 2;
+  return forward && rank > 32 && rank <= 64 ? 4 : 2;
 }
 
 // Rows times splits of the first products' parts, at most, wherever there is more than one.
 constexpr int kPartRows = 16384;
 
 // Parts of the columns in a first product: enough for two workgroups a CU, of 512 columns or more.
-inline int shrink_splits(int M, int E, int rank, int C) {
+inline int shrink_splits(int M, int E, int rank, int C, bool forward) {
   if (M == 0) return 1;
-  const long long tiles = max_row_tiles(M, E, 16 * lora_row_tiles(M, E, rank, kFirst));
+  const long long tiles = max_row_tiles(M, E, 16 * lora_row_tiles(M, E, rank, forward));
   long long s = 512 / (tiles < 512 ? tiles : 512);
   const int by_columns = ceil_div(C, 512), by_rows = kPartRows / (M < kPartRows ? M : kPartRows);
   s = s < by_columns ? s : by_columns;
@@ -33,29 +33,31 @@ inline int shrink_splits(int M, int E, int rank, int C) {
 }
 inline size_t lora_part_bytes(int M, int rank) { return (size_t)(M > kPartRows ? M : kPartRows) * rank * 4; }
 
-inline ShrinkArgs shrink_of(const LoraPlan& plan, const void* z, const void* w, int C, int rank, float* parts) {
-  const int splits = shrink_splits(plan.M, plan.E, rank, C);
+inline ShrinkArgs shrink_of(bool forward, const LoraPlan& plan, const void* z, const void* w, int C, int rank,
+                            float* parts) {
+  const int splits = shrink_splits(plan.M, plan.E, rank, C, forward);
   return {plan, z, w, C, rank, splits, ceil_div(ceil_div(C, splits), 32) * 32, parts};
 }
-inline long long shrink_blocks(const ShrinkArgs& s) {
-  return max_row_tiles(s.plan.M, s.plan.E, 16 * lora_row_tiles(s.plan.M, s.plan.E, s.rank, kFirst)) * s.splits;
+inline long long shrink_blocks(bool forward, const ShrinkArgs& s) {
+  return max_row_tiles(s.plan.M, s.plan.E, 16 * lora_row_tiles(s.plan.M, s.plan.E, s.rank, forward)) * s.splits;
 }
 
-// Spans of the columns in a second product: 1024 columns (rank 16 74 us; 512 79, 2304 81), down to 256 where there
+// Spans of the columns in a second product: 1024 columns (rank 16 67 us, 512 columns 70; rank 64 84, 512 88, 2816 92), down to 256 where there
 // are fewer than eight workgroups a CU.
-inline ExpandArgs expand_of(LoraProduct p, const ShrinkArgs& f, const void* w, int N, const float* scales,
+inline ExpandArgs expand_of(bool forward, const ShrinkArgs& f, const void* w, int N, const float* scales,
                             const void* base, void* y) {
-  ExpandArgs s{f.plan, f.parts, f.splits, f.rank, N, w, scales, base, y, 0, 0, 0};
-  s.row_tiles = (int)max_row_tiles(f.plan.M, f.plan.E, 16 * lora_row_tiles(f.plan.M, f.plan.E, f.rank, p));
+  ExpandArgs s{f.plan, f.parts, f.splits, f.rank, N, w, scales, base, y, 0, 0, 0, 0};
+  s.row_tiles = (int)max_row_tiles(f.plan.M, f.plan.E, 16 * lora_row_tiles(f.plan.M, f.plan.E, f.rank, forward));
   const int least = ceil_div(N, 1024), most = ceil_div(N, 256);
   int spans = 2048 / (s.row_tiles ? s.row_tiles : 1);
   spans = spans < least ? least : spans > most ? most : spans;
   s.span = ceil_div(ceil_div(N, spans), 256) * 256;
   s.spans = ceil_div(N, s.span);
+  s.copies = base == y ? 0 : ceil_div(f.plan.M, kCopied);
   return s;
 }
 inline long long expand_blocks(const ExpandArgs& s) {
-  return ((long long)s.row_tiles + (s.base == s.y ? 0 : ceil_div(s.plan.M, kCopied))) * s.spans;
+  return ((long long)s.row_tiles + s.copies) * s.spans;
 }
 
 // Parts of an adapter's rows in the gradients of A and B: as many as make two workgroups a CU, of 128 rows
@@ -75,13 +77,14 @@ inline long long grad_blocks(const LoraGradArgs& s) { return (long long)s.plan.E
 
 // Workgroups a CU that a kernel's registers are held to.
 constexpr int lora_held(int JT) { return JT <= 8 ? 2 : 1; }
+constexpr int lora_forward_tiles(int JT, int R) { return R == 2 && JT == 4 ? 4 : R; }
 
 template <int V>
 struct Int {
   static constexpr int value = V;
 };
 
-// f(T, JT, R): the type, the tiles of 16 that hold the rank, and the row tiles of a first product.
+// f(T, JT, R): the type, the tiles of 16 that hold the rank, and the backward call's row tiles.
 template <typename T, int JT, typename F>
 hipError_t by_rows(bool few, F f) {
   if constexpr (JT <= 8)
@@ -98,7 +101,7 @@ hipError_t by_rank(int rank, bool few, F f) {
 }
 template <typename F>
 hipError_t by_kind(int type, int M, int E, int rank, F f) {
-  const bool few = lora_row_tiles(M, E, rank, kFirst) == 1;
+  const bool few = lora_row_tiles(M, E, rank, false) == 1;
   return type == 0 ? by_rank<_Float16>(rank, few, f) : by_rank<__bf16>(rank, few, f);
 }
 
