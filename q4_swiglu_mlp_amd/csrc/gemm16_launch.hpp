@@ -1,6 +1,8 @@
 // How a 16-bit product by expert is cut, by its sizes alone, and its launches.
 #pragma once
 
+#include <cmath>
+
 #include "gemm16_tile.hpp"
 #include "launch.hpp"
 
@@ -8,52 +10,92 @@ namespace zinc {
 
 constexpr size_t kQueueBytes = 8 * 32 * 4;
 
-// The tiles, with the workgroups of each that a CU holds, and what a step of 64 takes a CU in us: one
-// workgroup alone, and each of as many as it holds (dense 8192 x 4096 x 4096: 265, 267, 274 and 336 us;
-// 2331 rows of 7 experts, 520 x 1032, 17 steps: 29, 19, 16 and 12).
+// The tiles: workgroups a CU holds, steps a unit has at least, and what a model of the time (us) takes: a step of
+// 64 of one workgroup alone on a CU, a CU's time for one where it is full, the steps that a unit's beginning
+// costs, and the TB/s at which the chip stores outputs.
 struct Gemm16Shape {
-  int TM, TN, held;
-  double alone, full;
+  int TM, TN, held, least;
+  double alone, full, begin, stores;
 };
-constexpr Gemm16Shape kGemm16Shapes[] = {
-    {256, 256, 1, 1.5, 1.85}, {128, 256, 1, 0.9, 1.04}, {128, 128, 2, 0.72, 0.56}, {64, 128, 3, 0.47, 0.33}};
+constexpr Gemm16Shape kGemm16Shapes[] = {{256, 256, 1, 3, 1.08, 0.49, 1.54, 5.2},
+                                         {128, 256, 1, 4, 0.57, 0.96, 0.46, 6.1},
+                                         {128, 128, 2, 3, 0.65, 0.51, 1.6, 4.7},
+                                         {64, 128, 3, 3, 0.48, 0.34, 1.66, 7.7}};
 
 struct Gemm16Plan {
   int shape, splits;
-  bool queue;        // the units are more than the CUs hold at once, and uneven
+  bool queue;        // units dealt out as CUs fall free, for the launch that their queues cost
   size_t part;       // values from one part of the summed dimension to the next
 };
 
-// The cut with the least time by the figures above: rounds of units times their steps, and for more than one
-// part of the summed dimension 3 us for the launch that joins them and its traffic at 4 TB/s.  An expert's
-// last row tile counts as half full.  (Experts of uneven sizes: as if they were even.)
-inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, int cus = 256) {
-  const int used = E < M ? E : (M ? M : 1);
+// The cut with the least time by a model fitted to 4388 timings: 90 products of 1 - 256 experts of uneven sizes, 1 -
+// 30000 rows, each with its gradients, in every tile, in 1 - 16 parts, dealt out or not.  It is off by 17 % on average;
+// what it picks takes 4 % more than the best on average (da 2 %, dw 6 %), 53 % in the worst of 90.
+// Examples, us, in the order of the tiles, in one part: 32768 rows of 64 x 768 x 2048 124, 132, 150 and 173, dw in
+// fp32 178, 191, 203 and 250; 2331 of 7 x 520 x 1032 31, 21, 19 and 16; 64 of 64 x 768 x 2048 49, 34, 38 and 36,
+// and 28 in two parts of the last.  For 256 CUs.
+inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
+  constexpr int kCus = 256;
+  const bool weight = f == kWeight;
+  const int cols = f == kForward ? N : K;
+  const double used = M == 0 ? 1 : E * (1 - std::pow(1 - 1.0 / E, M));   // experts with rows, if any may have any
   const double out = f == kForward ? (double)M * N : f == kInput ? (double)M * K : (double)E * N * K;
-  const int steps = f == kWeight ? (M / used + 95) / 64 : ((f == kForward ? K : N) + 63) / 64;
+  const double read = 2.0 * M * (f == kInput ? N : K) + (weight ? 2.0 * M * N : 2.0 * used * N * K);
+  const double several = 1 - 1.0 / E;   // how far experts' sizes can differ
   Gemm16Plan best{3, 1, false, 0};
   double least = 1e30;
   for (int i = 0; i < 4; ++i) {
     const Gemm16Shape& s = kGemm16Shapes[i];
-    const int cols = f == kForward ? N : K, col_tiles = (cols + s.TN - 1) / s.TN;
-    const double row_tiles = f == kWeight ? (double)E * ((N + s.TM - 1) / s.TM)
-                                          : (M <= used ? M : (double)M / s.TM + 0.5 * used > used ? (double)M / s.TM + 0.5 * used : used);
-    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-      const int each = (steps + splits - 1) / splits;
-      if (splits > 1 && (each < 4 || (steps + each - 1) / each != splits || splits * out > (1 << 25))) continue;
-      const double units = row_tiles * col_tiles * splits, a_cu = units / cus;
-      const int at_once = a_cu >= s.held ? s.held : a_cu <= 1 ? 1 : (int)(a_cu + 0.999);
-      const double step = s.full * at_once > s.alone ? s.full * at_once : s.alone;
-      double rounds = units / (cus * (double)at_once);
-      rounds = rounds <= 1 ? 1 : (double)(long long)(rounds + 0.95);
-      const double us = rounds * (each + 2) * step + (splits > 1 ? 3 + splits * out * 8 / 4e6 : 0);
-      if (us < least) {
-        least = us;
-        best = {i, splits, units > 1.5 * cus * s.held && i < 2, ((size_t)out + 7) / 8 * 8};
+    const double col_tiles = (cols + s.TN - 1) / s.TN;
+    double row_tiles = used * ((N + s.TM - 1) / s.TM);
+    if (!weight) {   // an expert's last tile is partly filled
+      row_tiles = E == 1 ? (M + s.TM - 1) / s.TM : M / (double)s.TM + 0.77 * used;
+      if (row_tiles < used) row_tiles = used;
+    }
+    const double alone = !weight && M < used * s.TM ? 1.5 * s.alone : s.alone;   // weights that are read only once
+    const int all = weight ? 0 : ((f == kForward ? K : N) + 63) / 64;
+    const double mean = M / used / 64;   // an expert's steps in dw; the largest's 1 + 1.1 times as many
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      double steps, most;
+      if (weight) {
+        if (splits > 1 && mean / splits < 2) continue;
+        steps = mean / splits + 0.5;
+        most = (1 + 1.1 * several) * mean / splits + 0.5;
+      } else {
+        const int each = (all + splits - 1) / splits;
+        if (splits > 1 && (each < 4 || (all + each - 1) / each != splits)) continue;   // no part is empty
+        steps = most = each;
+      }
+      if (splits > 1 && splits * out > (1 << 26)) continue;
+      const double bytes = splits > 1 ? 4 : weight ? 3 : 2;   // (not by the call's types: the plan goes by sizes)
+      steps = steps < s.least ? s.least : steps;
+      most = most < s.least ? s.least : most;
+      const double units = row_tiles * col_tiles * splits, rounds = units / kCus;
+      const int c = rounds > s.held ? s.held : rounds <= 1.05 ? 1 : (int)(rounds + 0.95);   // workgroups a CU has
+      const double step = s.full * c > alone ? s.full * c : alone;
+      const double store = s.TM * s.TN * bytes * kCus / (s.stores * 1e6), work = (steps + s.begin) * step / c;
+      const double unit = s.held == 1 ? work + store
+                          : work > store ? work + 0.49 * store : store + 0.49 * work;   // others compute meanwhile
+      const double longest = (most + s.begin) * step;
+      for (int queue = 0; queue < (splits == 1 && rounds > 1 ? 2 : 1); ++queue) {
+        double us = longest + store * (rounds < 1 ? rounds : 1);
+        if (rounds > 1) {
+          us = rounds * unit;
+          if (weight && !queue) us *= 1 + 0.53 * several * (mean < 2.6 ? 0.21 : mean < 12.5 ? mean / 12.5 : 1);
+          if (!weight && !queue) us = (double)(long long)(rounds / c + 0.9) * c * unit;
+          if (us < longest) us = longest;
+        }
+        if (weight) us += (1 - used / E) * out * bytes * splits / 5.3e6;   // zeros for experts without rows
+        if (us < (read + bytes * splits * out) / 6.4e6) us = (read + bytes * splits * out) / 6.4e6;
+        if (us < 8) us = 7.2 + 0.1 * us;   // the host's time for one launch, which another adds to
+        us += (queue ? 6 : 0) + (splits > 1 ? 2.8 + (splits * 4 + 3) * out / 4.9e6 : 0);
+        if (us < least) {
+          least = us;
+          best = {i, splits, queue != 0, ((size_t)out + 7) / 8 * 8};
+        }
       }
     }
   }
-  if (best.splits > 1) best.queue = false;
   return best;
 }
 inline size_t gemm16_part_bytes(const Gemm16Plan& p) { return p.splits > 1 ? p.splits * p.part * sizeof(float) : 0; }

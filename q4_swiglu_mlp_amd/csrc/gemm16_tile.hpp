@@ -81,7 +81,7 @@ struct Gemm16 {
   // Large tiles' outputs are stored past the caches, in whole lines: 32768 rows of 64 experts, 768 x 2048, dw in fp32
   // 143 us, in lines that the caches hold 180, in half lines 166 and 183 (half as much again is written); da
   // 118 and 131.
-  static constexpr bool STREAMED = TN == 256;
+  static constexpr bool STREAMED = NT == 4;
   // workgroups a CU holds by registers
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
   static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 4 == 0, "whole copies");
@@ -142,20 +142,26 @@ struct Gemm16 {
   }
 
   // The experts with most rows first, dealt out to the XCDs' queues (each a contiguous run of the order)
-  // back and forth: 0 .. 7, 7 .. 0, ...; fewer than eight keep their order.
-  static __device__ __forceinline__ void order_experts(const Gemm16Args& g, int32_t* rows, int32_t* order) {
+  // back and forth: 0 .. 7, 7 .. 0, ...; fewer than eight keep their order.  Those without rows stand behind them.
+  // Returns how many have rows.
+  static __device__ __forceinline__ int order_experts(const Gemm16Args& g, int32_t* rows, int32_t* order) {
     for (int e = threadIdx.x; e < g.E; e += THREADS) {
       const int lo = min(max(g.offsets[e], 0), g.M);
       rows[e] = max(min(g.offsets[e + 1], g.M) - lo, 0);
     }
     __syncthreads();
-    const int whole = g.E / 8, rest = g.E % 8;
+    int reached = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int e = e0 + (threadIdx.x & 63);
+      reached += __popcll(__ballot(e < g.E && rows[e] > 0));
+    }
+    const int whole = reached / 8, rest = reached % 8;
     for (int e = threadIdx.x; e < g.E; e += THREADS) {
       const int mine = rows[e];
       int rank = 0;
       for (int o = 0; o < g.E; ++o) rank += rows[o] > mine || (rows[o] == mine && o < e);
       int at = rank;
-      if (whole) {
+      if (whole && rank < reached) {
         const int turn = rank / 8;
         auto xcd_of = [](int turn, int in) { return turn & 1 ? 7 - in : in; };
         const int xcd = xcd_of(turn, rank % 8);
@@ -165,6 +171,24 @@ struct Gemm16 {
       order[at] = e;
     }
     __syncthreads();
+    return reached;
+  }
+
+  // Zeros in dw, or in its parts, for the experts without rows, order[reached] and on, 64 KB a workgroup in turn
+  // (5.3 TB/s; 8 rows of 256 experts, 312 x 4152, both gradients 151 us, by products of no steps 312).
+  static __device__ __forceinline__ void clear_absent(const Gemm16Args& g, const int32_t* order, int reached) {
+    constexpr int kChunk = 4096;   // of 16 bytes
+    const size_t pieces = (size_t)g.N * g.K * sizeof(O) / 16;
+    const int chunks = (int)((pieces + kChunk - 1) / kChunk);
+    const long long all = (long long)(g.E - reached) * chunks * g.splits;
+    for (long long u = blockIdx.x; u < all; u += gridDim.x) {
+      const int at = (int)(u / chunks), split = at / (g.E - reached);
+      const size_t first = (size_t)(u - (long long)at * chunks) * kChunk;
+      const size_t expert = order[reached + at - split * (g.E - reached)];
+      i32x4_t* to = reinterpret_cast<i32x4_t*>(static_cast<O*>(g.c) + split * g.part + expert * g.N * g.K) + first;
+      const int n = (int)(pieces - first < kChunk ? pieces - first : kChunk);
+      for (int i = threadIdx.x; i < n; i += THREADS) __builtin_nontemporal_store(i32x4_t{0, 0, 0, 0}, to + i);
+    }
   }
 
   static __device__ __forceinline__ void run(const Gemm16Args& g, uint8_t* smem) {
@@ -178,8 +202,9 @@ struct Gemm16 {
     int32_t* ends = starts + g.E + 1;
     int row_tiles = 0, total;
     if constexpr (F == kWeight) {
-      order_experts(g, starts, ends);
-      total = g.E * ((g.N + TM - 1) / TM) * col_tiles * g.splits;
+      const int reached = order_experts(g, starts, ends);
+      clear_absent(g, ends, reached);
+      total = reached * ((g.N + TM - 1) / TM) * col_tiles * g.splits;
     } else {
       row_tiles = make_tables<TM>(g, starts, ends);
       __syncthreads();
