@@ -26,6 +26,7 @@ struct Gemm16Plan {
   int shape, splits;
   bool queue;        // units dealt out as CUs fall free, for the launch that their queues cost
   size_t part;       // values from one part of the summed dimension to the next
+  double us;         // the model's time
 };
 
 // The cut with the least time by a model fitted to 4388 timings: 90 products of 1 - 256 experts of uneven sizes, 1 -
@@ -34,7 +35,8 @@ struct Gemm16Plan {
 // Examples, us, in the order of the tiles, in one part: 32768 rows of 64 x 768 x 2048 124, 132, 150 and 173, dw in
 // fp32 178, 191, 203 and 250; 2331 of 7 x 520 x 1032 31, 21, 19 and 16; 64 of 64 x 768 x 2048 49, 34, 38 and 36,
 // and 28 in two parts of the last.  For 256 CUs.
-inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
+// small: the smallest tile, in one part, dealt out in turn.
+inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small = false) {
   constexpr int kCus = 256;
   const bool weight = f == kWeight;
   const int cols = f == kForward ? N : K;
@@ -42,9 +44,9 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
   const double out = f == kForward ? (double)M * N : f == kInput ? (double)M * K : (double)E * N * K;
   const double read = 2.0 * M * (f == kInput ? N : K) + (weight ? 2.0 * M * N : 2.0 * used * N * K);
   const double several = 1 - 1.0 / E;   // how far experts' sizes can differ
-  Gemm16Plan best{3, 1, false, 0};
+  Gemm16Plan best{3, 1, false, 0, 0};
   double least = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = small ? 3 : 0; i < 4; ++i) {
     const Gemm16Shape& s = kGemm16Shapes[i];
     const double col_tiles = (cols + s.TN - 1) / s.TN;
     double row_tiles = used * ((N + s.TM - 1) / s.TM);
@@ -66,7 +68,7 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
         if (splits > 1 && (each < 4 || (all + each - 1) / each != splits)) continue;   // no part is empty
         steps = most = each;
       }
-      if (splits > 1 && splits * out > (1 << 26)) continue;
+      if (splits > 1 && (small || splits * out > (1 << 26))) continue;
       const double bytes = splits > 1 ? 4 : weight ? 3 : 2;   // (not by the call's types: the plan goes by sizes)
       steps = steps < s.least ? s.least : steps;
       most = most < s.least ? s.least : most;
@@ -77,7 +79,7 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
       const double unit = s.held == 1 ? work + store
                           : work > store ? work + 0.49 * store : store + 0.49 * work;   // others compute meanwhile
       const double longest = (most + s.begin) * step;
-      for (int queue = 0; queue < (splits == 1 && rounds > 1 ? 2 : 1); ++queue) {
+      for (int queue = 0; queue < (splits == 1 && rounds > 1 && !small ? 2 : 1); ++queue) {
         double us = longest + store * (rounds < 1 ? rounds : 1);
         if (rounds > 1) {
           us = rounds * unit;
@@ -91,7 +93,7 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K) {
         us += (queue ? 6 : 0) + (splits > 1 ? 2.8 + (splits * 4 + 3) * out / 4.9e6 : 0);
         if (us < least) {
           least = us;
-          best = {i, splits, queue != 0, ((size_t)out + 7) / 8 * 8};
+          best = {i, splits, queue != 0, ((size_t)out + 7) / 8 * 8, us};
         }
       }
     }
@@ -105,19 +107,25 @@ static __global__ void k_gemm16_queue(int32_t* queue, int first) { queue[32 * th
 
 // As many persistent workgroups as the CUs hold, a multiple of the eight XCDs.
 template <typename KERNEL>
+unsigned gemm16_blocks(const Gemm16Args& g, int shape, int cus) {
+  const int bytes = (int)KERNEL::smem_bytes(g.E), TM = kGemm16Shapes[shape].TM, TN = kGemm16Shapes[shape].TN;
+  const int cols = KERNEL::kProduct == kForward ? g.N : g.K;
+  const long long row_tiles =
+      KERNEL::kProduct == kWeight ? (long long)g.E * ((g.N + TM - 1) / TM) : max_row_tiles(g.M, g.E, TM);
+  const int held = kLds / bytes < KERNEL::HELD ? kLds / bytes : KERNEL::HELD;
+  const long long units = row_tiles * ((cols + TN - 1) / TN) * g.splits, room = (long long)cus * held;
+  return (unsigned)(((units < room ? units : room) + 7) / 8 * 8);
+}
+
+// The launch's grid and LDS, whose limit is raised for `kernel` (KERNEL's, or one that KERNEL stands for).
+template <typename KERNEL>
 hipError_t gemm16_grid(const Gemm16Args& g, const void* kernel, int shape, unsigned* grid, int* bytes) {
   *bytes = (int)KERNEL::smem_bytes(g.E);
   hipError_t e = allow_lds<KERNEL>(kernel, kLds);
   int cus = 0;
   if (e == hipSuccess) e = compute_units(&cus);
   if (e != hipSuccess) return e;
-  const int cols = KERNEL::kProduct == kForward ? g.N : g.K, TM = kGemm16Shapes[shape].TM;
-  const long long row_tiles =
-      KERNEL::kProduct == kWeight ? (long long)g.E * ((g.N + TM - 1) / TM) : max_row_tiles(g.M, g.E, TM);
-  const int held = kLds / *bytes < KERNEL::HELD ? kLds / *bytes : KERNEL::HELD, TN = kGemm16Shapes[shape].TN;
-  const long long units = row_tiles * ((cols + TN - 1) / TN) * g.splits, room = (long long)cus * held;
-  const long long blocks = units < room ? units : room;
-  *grid = (unsigned)((blocks + 7) / 8 * 8);
+  *grid = gemm16_blocks<KERNEL>(g, shape, cus);
   return hipSuccess;
 }
 

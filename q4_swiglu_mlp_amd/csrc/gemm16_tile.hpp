@@ -61,7 +61,7 @@ struct Gemm16Args {
   void* c;
   int splits;       // parts of the summed dimension, each with its own output,
   size_t part;      // this many values after the one before
-  int32_t* queue;   // the next unit of each XCD, 32 apart, from gridDim.x / 8 on; or null: dealt out in turn
+  int32_t* queue;   // the next unit of each XCD, 32 apart, from blocks / 8 on; or null: dealt out in turn
 };
 
 template <Product F, int TM, int TN, int WM, int WN, int BUFFERS, typename T, typename O>
@@ -176,12 +176,13 @@ struct Gemm16 {
 
   // Zeros in dw, or in its parts, for the experts without rows, order[reached] and on, 64 KB a workgroup in turn
   // (5.3 TB/s; 8 rows of 256 experts, 312 x 4152, both gradients 151 us, by products of no steps 312).
-  static __device__ __forceinline__ void clear_absent(const Gemm16Args& g, const int32_t* order, int reached) {
+  static __device__ __forceinline__ void clear_absent(const Gemm16Args& g, const int32_t* order, int reached, int block,
+                                                      int blocks) {
     constexpr int kChunk = 4096;   // of 16 bytes
     const size_t pieces = (size_t)g.N * g.K * sizeof(O) / 16;
     const int chunks = (int)((pieces + kChunk - 1) / kChunk);
     const long long all = (long long)(g.E - reached) * chunks * g.splits;
-    for (long long u = blockIdx.x; u < all; u += gridDim.x) {
+    for (long long u = block; u < all; u += blocks) {
       const int at = (int)(u / chunks), split = at / (g.E - reached);
       const size_t first = (size_t)(u - (long long)at * chunks) * kChunk;
       const size_t expert = order[reached + at - split * (g.E - reached)];
@@ -191,7 +192,8 @@ struct Gemm16 {
     }
   }
 
-  static __device__ __forceinline__ void run(const Gemm16Args& g, uint8_t* smem) {
+  // Workgroup `block` of `blocks`, a multiple of eight.
+  static __device__ __forceinline__ void run(const Gemm16Args& g, uint8_t* smem, int block, int blocks) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, l16 = lane & 15, quad = lane >> 4;
     // the matrices' row lengths, the output's columns
@@ -203,7 +205,7 @@ struct Gemm16 {
     int row_tiles = 0, total;
     if constexpr (F == kWeight) {
       const int reached = order_experts(g, starts, ends);
-      clear_absent(g, ends, reached);
+      clear_absent(g, ends, reached, block, blocks);
       total = reached * ((g.N + TM - 1) / TM) * col_tiles * g.splits;
     } else {
       row_tiles = make_tables<TM>(g, starts, ends);
@@ -212,8 +214,8 @@ struct Gemm16 {
     }
     // An XCD has a contiguous run of the units.  Its workgroups take them in turn, or from its queue and, when
     // that is empty, from the others': then `got` is a number from queue `from`, on its way.
-    const int per = (total + 7) / 8, stride = gridDim.x / 8, xcd = blockIdx.x & 7;
-    int from = xcd, got = blockIdx.x >> 3;
+    const int per = (total + 7) / 8, stride = blocks / 8, xcd = block & 7;
+    int from = xcd, got = block >> 3;
     auto ask = [&] {   // (one wave)
       if (g.queue && lane == 0) got = atomicAdd(g.queue + 32 * from, 1);
       if (!g.queue) got += stride;
@@ -496,7 +498,7 @@ struct Gemm16 {
 template <typename KERNEL>
 __global__ __launch_bounds__(KERNEL::THREADS) void k_gemm16(Gemm16Args g) {
   extern __shared__ __align__(16) uint8_t smem[];
-  KERNEL::run(g, smem);
+  KERNEL::run(g, smem, blockIdx.x, gridDim.x);
 }
 
 }  // namespace zinc
