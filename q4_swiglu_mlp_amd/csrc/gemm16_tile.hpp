@@ -390,6 +390,28 @@ struct Gemm16 {
       const int unit = unit_of(n);
       if (unit < 0) return;
       const Unit cu = unit_at(g, starts, ends, row_tiles, col_tiles, unit);
+      // A wave whose rows all lie behind the tile's last only copies and keeps step; its SIMD's other wave has the
+      // matrix unit to itself (8192 rows of 8 x 11008 x 4096 680 us, without 687; the gradients of 32768 of 64 x 768 x
+      // 2048 292 and 297).
+      const bool idle = WM > 1 && (F == kWeight ? g.N - cu.p0 : cu.rows) <= wm * (TM / WM);
+      if (idle) {
+        for (int k = 0; k < cu.steps; ++k, buf = after(buf)) {
+          landed(ahead);
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          const bool more = is_more;
+          if (more) {
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) copy_piece(i, buf);
+          }
+          advance();
+          if (!more) ahead = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) read_q(j, buf);
+        read_p(0, 0, buf);
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll

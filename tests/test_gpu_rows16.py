@@ -155,6 +155,45 @@ def test_products_of_many_and_of_few_units(kind, wide, rows, E, N, K):
         assert torch.equal(again, c)
 
 
+# every tile of c, of da and of dw, in one part, in parts and dealt out from queues; both gradients in one launch, one
+# after the other, and side by side
+CUTS = [(1, 1, 8, 8), (1, 1, 8, 800), (1, 2, 840, 8), (1685, 2, 8, 8), (33443, 3, 16, 8), (2777, 1, 8, 5856),
+        (11334, 1, 1704, 8), (17745, 9, 632, 8), (30758, 60, 152, 8), (34823, 1, 16, 6400), (33078, 9, 904, 8),
+        (16867, 20, 136, 240), (8931, 9, 160, 2240), (24545, 130, 192, 304), (4268, 20, 1640, 448), (210, 300, 672, 264),
+        (34950, 130, 8, 136), (2008, 1, 3040, 2336), (19076, 1, 8, 920), (636, 300, 912, 144), (9572, 9, 2056, 136),
+        (27503, 130, 392, 160), (17469, 130, 984, 288), (229, 130, 288, 928), (77, 130, 728, 144), (13234, 9, 2656, 136),
+        (150, 130, 2992, 136), (86, 130, 464, 136), (25271, 9, 1224, 144), (11663, 20, 2120, 136), (713, 300, 80, 8),
+        (269, 300, 2616, 8), (169, 300, 8, 6968), (17042, 60, 648, 688), (1, 1, 1264, 8)]
+
+
+@pytest.mark.parametrize("kind,wide", [("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("rows,E,N,K", CUTS)
+def test_every_cut(kind, wide, rows, E, N, K):
+    rng = np.random.default_rng(rows + E)
+    a, w, off = activations(rng, rows, K, kind), normal(rng, E, N, K, kind=kind, size=0.1), ranges(rng, rows, E)
+    dc = normal(rng, rows, N, kind=kind)
+    out = "f32" if wide else kind
+    t = TYPES[out][0]
+    c = torch.full((rows, N), -3.0, dtype=t, device=DEV)
+    das = [torch.full((rows, K), -3.0, dtype=t, device=DEV) for _ in range(2)]
+    dws = [torch.full((E, N, K), -3.0, dtype=t, device=DEV) for _ in range(2)]
+    Z.zinc_moe_gemm(a, w, dev(off), out=c)
+    Z.zinc_moe_gemm_backward(dc, a, w, dev(off), da=das[0], dw=dws[0])
+    Z.zinc_moe_gemm_backward(dc, a, w, dev(off), da=das[1], want_dw=False)
+    Z.zinc_moe_gemm_backward(dc, a, w, dev(off), dw=dws[1], want_da=False)
+    ah, wh, dch = host(a), host(w), host(dc)
+    am, wm, dm = np.abs(ah), np.abs(wh), np.abs(dch)
+    close(c, R.moe_gemm(ah, wh, off, np.full((rows, N), -3.0)),
+          sums(K) * R.moe_gemm(am, wm, off, np.zeros((rows, N))), out, "c")
+    want_a, want_w = R.moe_gemm_backward(dch, ah, wh, off, np.full((rows, K), -3.0))
+    size_a, size_w = R.moe_gemm_backward(dm, am, wm, off, np.zeros((rows, K)))
+    for da, dw in zip(das, dws):
+        close(da, want_a, sums(N) * size_a, out, "da")
+        close(dw, want_w, sums(rows) * size_w, out, "dw")
+        for e in range(E):
+            assert off[e] < off[e + 1] or not bool(dw[e].any())
+
+
 @pytest.mark.parametrize("rows,E", [(1, 1), (40, 3), (700, 2), (2000, 3)])
 def test_products_keep_nan_in_its_place(rows, E):
     """Rows outside the ranges, other experts' rows and weights, and what lies behind a row's end add nothing."""
@@ -628,3 +667,50 @@ def test_a_workspace_is_reused_and_its_end_kept():
         for a, b in zip(Z.zinc_lora_backward(s["dc"], *args, workspace=ws[:need]), Z.zinc_lora_backward(s["dc"], *args)):
             assert torch.equal(a, b)
         assert bool((ws[need:] == 0xAB).all())
+
+
+# c and da in parts, da and c dealt out, dw in parts, dw dealt out, both dealt out in one launch
+WITH_WORKSPACE = [(40, 1, 8, 800), (40, 2, 840, 8), (210, 300, 672, 264), (229, 130, 288, 928), (1685, 2, 8, 8),
+                  (269, 300, 2616, 8), (17042, 60, 648, 688)]
+
+
+def product_state(seed, rows, E, N, K):
+    rng = np.random.default_rng(seed)
+    return (normal(rng, rows, N, kind="bf16"), normal(rng, rows, K, kind="bf16"), normal(rng, E, N, K, kind="bf16", size=0.1),
+            dev(ranges(rng, rows, E, outside=False)))
+
+
+def products(dc, a, w, off, forward=None, backward=None):
+    return (Z.zinc_moe_gemm(a, w, off, workspace=forward),
+            *Z.zinc_moe_gemm_backward(dc, a, w, off, dw_dtype=torch.float32, workspace=backward))
+
+
+@pytest.mark.parametrize("rows,E,N,K", WITH_WORKSPACE)
+def test_products_of_graphs_that_share_a_workspace(rows, E, N, K):
+    """Two graphs on one workspace of exactly the size asked for, replayed in turn; what lies behind it is kept."""
+    need = [Z.moe_gemm_workspace_size(rows, E, N, K), Z.moe_gemm_backward_workspace_size(rows, E, N, K)]
+    assert max(need) > 0
+    ws = torch.full((max(need) + 256,), 0xAB, dtype=torch.uint8, device=DEV)
+    both = ws[:need[0]], ws[:need[1]]
+    states = [product_state(seed, rows, E, N, K) for seed in (1, 2)]
+    graphs, outs = [], []
+    for s in states:
+        products(*s)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(products(*s, *both))
+    for seed in (3, 4, 5):
+        want = []
+        for i, s in enumerate(states):
+            for t, n in zip(s, product_state(seed + 10 * i, rows, E, N, K)):
+                t.copy_(n)
+            want.append([t.clone() for t in products(*s)])
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for got, expected in zip(outs, want):
+            for a, b in zip(got, expected):
+                assert torch.equal(a, b)
+        assert bool((ws[max(need):] == 0xAB).all())
