@@ -454,10 +454,12 @@ int zinc_moe_fp8_experts(const void* w_gate, const float* gate_scales, const voi
  * no dw; offsets are cut to [0, rows] and have to ascend.  dw of an expert without rows is zeros (also
  * where rows is 0, which needs no other input).  da or dw may be NULL: it is then not computed, and w
  * (a) not read.  The result is a function of the inputs alone, run after run; which kernel takes a
- * product goes by its sizes, so a row's last bits may change with the number of rows beside it.
+ * product goes by its sizes, and by which gradients are asked for, so a row's last bits may change with the
+ * number of rows beside it, and da's (dw's) with dw (da) beside it.
  * N and K: multiples of 8 up to 65536 (else ZINC_ERR_SHAPE); rows <= 2^24, n_experts <= 1024, types as above
  * (else ZINC_ERR_ARG).  Matrices and the workspace are 16-byte aligned, offsets 4.  The size queries
- * return 0 where no workspace is needed (workspace may then be NULL) and for arguments out of range.
+ * return 0 for rows 0 (workspace may then be NULL) and for arguments out of range; the sizes are
+ * non-decreasing in rows, and at most 2^26 + 2^11 bytes.
  * No output of these calls, of SwiGLU's or the adapters' may overlap an input, another output or the
  * workspace, but for y (dx) in the place of base.
  */
@@ -520,7 +522,7 @@ int zinc_lora_backward(const void* dy, const void* x, int32_t type, int32_t M, i
  * MoE call records a HIP event pair on its stream immediately around its main
  * kernel -- the fused unit kernel for prefill and MoE; for decode, one pair
  * around the gate/up matvec and one around the down matvec; for an FP8 or 16-bit product one around
- * its main kernel (two with both gradients), for the FP8 experts one around the gate/up and one around the down
+ * its main kernel (one or two with both gradients), for the FP8 experts one around the gate/up and one around the down
  * product -- for up to `capacity` pairs.  The events are recorded without a system-scope fence
  * (hipEventDisableSystemFence), so they add no cache write-back of their own
  * to the work they bracket.  zinc_timing_collect() waits for the recorded events,

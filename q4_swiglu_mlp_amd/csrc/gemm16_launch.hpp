@@ -29,6 +29,23 @@ struct Gemm16Plan {
   double us;         // the model's time
 };
 
+// Experts with rows, if any may have any.
+inline double gemm16_used(int M, int E) { return M == 0 ? 1 : E * (1 - std::pow(1 - 1.0 / E, M)); }
+
+// Parts of the summed dimension at most (of four steps, in dw of two of the mean expert's), and values in all of them
+// (64 MB: of 300 drawn sizes with four times as many none took less).  With the rows neither falls.
+constexpr double kPartValues = 1 << 24;
+inline int gemm16_most_parts(Product f, int M, int E, int N, int K) {
+  const double most = f == kWeight ? M / gemm16_used(M, E) / 128 : ((f == kForward ? K : N) + 63) / 64 / 4;
+  return most < 1 ? 1 : most > 16 ? 16 : (int)most;
+}
+// A workspace's bytes for the parts of any product of up to M rows.
+inline size_t gemm16_part_bytes(Product f, int M, int E, int N, int K) {
+  const int parts = gemm16_most_parts(f, M, E, N, K);
+  const double out = f == kForward ? (double)M * N : f == kInput ? (double)M * K : (double)E * N * K;
+  return parts == 1 ? 0 : 4 * (size_t)(parts * out < kPartValues ? parts * out : kPartValues);
+}
+
 // The cut with the least time by a model fitted to 4388 timings: 90 products of 1 - 256 experts of uneven sizes, 1 -
 // 30000 rows, each with its gradients, in every tile, in 1 - 16 parts, dealt out or not.  It is off by 17 % on average;
 // what it picks takes 4 % more than the best on average (da 2 %, dw 6 %), 53 % in the worst of 90.
@@ -40,11 +57,13 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
   constexpr int kCus = 256;
   const bool weight = f == kWeight;
   const int cols = f == kForward ? N : K;
-  const double used = M == 0 ? 1 : E * (1 - std::pow(1 - 1.0 / E, M));   // experts with rows, if any may have any
+  const double used = gemm16_used(M, E);
   const double out = f == kForward ? (double)M * N : f == kInput ? (double)M * K : (double)E * N * K;
   const double read = 2.0 * M * (f == kInput ? N : K) + (weight ? 2.0 * M * N : 2.0 * used * N * K);
   const double several = 1 - 1.0 / E;   // how far experts' sizes can differ
+  const int parts = small ? 1 : gemm16_most_parts(f, M, E, N, K);
   Gemm16Plan best{3, 1, false, 0, 0};
+  if (M == 0) return best;   // (dw of no rows)
   double least = 1e30;
   for (int i = small ? 3 : 0; i < 4; ++i) {
     const Gemm16Shape& s = kGemm16Shapes[i];
@@ -58,17 +77,16 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
     const int all = weight ? 0 : ((f == kForward ? K : N) + 63) / 64;
     const double mean = M / used / 64;   // an expert's steps in dw; the largest's 1 + 1.1 times as many
     for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (splits > parts || (splits > 1 && splits * out > kPartValues)) break;
       double steps, most;
       if (weight) {
-        if (splits > 1 && mean / splits < 2) continue;
         steps = mean / splits + 0.5;
         most = (1 + 1.1 * several) * mean / splits + 0.5;
       } else {
         const int each = (all + splits - 1) / splits;
-        if (splits > 1 && (each < 4 || (all + each - 1) / each != splits)) continue;   // no part is empty
+        if ((all + each - 1) / each != splits) continue;   // no part is empty
         steps = most = each;
       }
-      if (splits > 1 && (small || splits * out > (1 << 26))) continue;
       const double bytes = splits > 1 ? 4 : weight ? 3 : 2;   // (not by the call's types: the plan goes by sizes)
       steps = steps < s.least ? s.least : steps;
       most = most < s.least ? s.least : most;
@@ -100,7 +118,6 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
   }
   return best;
 }
-inline size_t gemm16_part_bytes(const Gemm16Plan& p) { return p.splits > 1 ? p.splits * p.part * sizeof(float) : 0; }
 
 // The queues' first numbers, behind the units that the workgroups start with.
 static __global__ void k_gemm16_queue(int32_t* queue, int first) { queue[32 * threadIdx.x] = first; }

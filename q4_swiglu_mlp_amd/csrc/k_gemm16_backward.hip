@@ -88,9 +88,9 @@ hipError_t run_both(const Gemm16Args& a, const Gemm16Args& w, hipStream_t stream
 }  // namespace
 
 size_t gemm16_backward_workspace_bytes(int M, int E, int N, int K) {
-  const BackwardPlan p = plan_backward(M, E, N, K);
-  const size_t a = M ? gemm16_part_bytes(p.input) : 0, w = gemm16_part_bytes(p.weight);
-  return (M && (p.input.queue || a)) || p.weight.queue || w ? 2 * kQueueBytes + (a > w ? a : w) : 0;
+  if (M == 0) return 0;
+  const size_t a = gemm16_part_bytes(kInput, M, E, N, K), w = gemm16_part_bytes(kWeight, M, E, N, K);
+  return 2 * kQueueBytes + (a > w ? a : w);
 }
 
 hipError_t launch_gemm16_backward(const void* dc, const void* a, const void* w, int type, const int32_t* offsets, int E,

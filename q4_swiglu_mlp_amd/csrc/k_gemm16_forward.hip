@@ -8,9 +8,7 @@ hipError_t launch_gemm16_forward(const void* p, const void* q, int type, const i
 }
 
 size_t gemm16_workspace_bytes(int M, int E, int N, int K) {
-  if (M == 0) return 0;
-  const Gemm16Plan p = plan_gemm16(kForward, M, E, N, K);
-  return p.queue || p.splits > 1 ? kQueueBytes + gemm16_part_bytes(p) : 0;
+  return M == 0 ? 0 : kQueueBytes + gemm16_part_bytes(kForward, M, E, N, K);
 }
 
 }  // namespace zinc

@@ -105,12 +105,10 @@ def test_workspace_sizes():
     for size in (Z.moe_gemm_workspace_size, Z.moe_gemm_backward_workspace_size):
         assert size(-1, 4, 256, 256) == 0 and size(16, 0, 256, 256) == 0 and size(16, 4, 12, 256) == 0
         assert size(1 << 40, 4, 256, 256) == 0
-    # parts of the summed dimension, or queues; with rows the size may fall again, but stays below its bound
-    assert Z.moe_gemm_workspace_size(40, 1, 8, 800) > 0 and Z.moe_gemm_backward_workspace_size(1685, 2, 8, 8) > 0
-    for E, N, K in ((1, 8, 800), (1, 4096, 4096), (64, 768, 2048), (1024, 1024, 64), (1, 65536, 65536), (1, 65536, 8)):
-        for rows in (0, 1, 7, 100, 1000, 4096, 10000, 33333, 200000, 1 << 20, 1 << 24):
-            assert Z.moe_gemm_workspace_size(rows, E, N, K) <= (1 << 28) + 2048 * 16
-            assert Z.moe_gemm_backward_workspace_size(rows, E, N, K) <= (1 << 28) + 2048 * 16
+    for size in (Z.moe_gemm_workspace_size, Z.moe_gemm_backward_workspace_size):
+        for E, N, K in ((1, 8, 800), (1, 4096, 4096), (64, 768, 2048), (1024, 1024, 64), (1, 65536, 65536), (1, 65536, 8)):
+            sizes = [size(rows, E, N, K) for rows in (0, 1, 2, 7, 64, 100, 1000, 4096, 10000, 33333, 1 << 20, 1 << 24)]
+            assert sizes == sorted(sizes) and sizes[0] == 0 and 0 < sizes[1] and sizes[-1] <= (1 << 26) + (1 << 11)
 
 
 def test_a_small_workspace_is_refused():
