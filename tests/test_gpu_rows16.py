@@ -714,3 +714,96 @@ def test_products_of_graphs_that_share_a_workspace(rows, E, N, K):
             for a, b in zip(got, expected):
                 assert torch.equal(a, b)
         assert bool((ws[max(need):] == 0xAB).all())
+
+
+@pytest.mark.parametrize("rows,E,N,K", [(17042, 60, 648, 688), (1111, 7, 520, 1032), (1685, 2, 8, 8)])
+def test_gradients_of_two_types(rows, E, N, K):
+    """In one launch, side by side and apart: the 16-bit gradient is the fp32 one, rounded."""
+    s = product_state(7, rows, E, N, K)
+    wide_a, wide_w = Z.zinc_moe_gemm_backward(*s, da_dtype=torch.float32, dw_dtype=torch.float32)
+    inside = slice(int(s[3][0]), int(s[3][-1]))
+    for a_type, w_type in ((torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)):
+        da, dw = Z.zinc_moe_gemm_backward(*s, da_dtype=a_type, dw_dtype=w_type)
+        assert da.dtype == a_type and dw.dtype == w_type
+        assert torch.equal(da[inside], wide_a[inside].to(a_type)) and torch.equal(dw, wide_w.to(w_type))
+
+
+# ---------------------------------------------------------------- past 2**32 bytes
+def last_rows(rng, rows, cols, n, kind):
+    """Zeros but for the last n rows."""
+    x = torch.zeros((rows, cols), dtype=TYPES[kind][0], device=DEV)
+    x[-n:] = normal(rng, n, cols, kind=kind)
+    return x
+
+
+@pytest.mark.parametrize("N,K", [(8, 640), (640, 8)])
+def test_products_past_32_bits(N, K):
+    rng = np.random.default_rng(N)
+    rows, n = 3_600_000, 300
+    a, dc, w = last_rows(rng, rows, K, n, "bf16"), last_rows(rng, rows, N, n, "bf16"), normal(rng, 2, N, K, kind="bf16")
+    assert max(a.numel(), dc.numel()) * 2 > 1 << 32
+    off = np.array([0, rows - 200, rows], np.int32)
+    c = Z.zinc_moe_gemm(a, w, dev(off))
+    da, dw = Z.zinc_moe_gemm_backward(dc, a, w, dev(off), dw_dtype=torch.float32)
+    tail = np.array([0, n - 200, n], np.int32)
+    at, dt, wh = host(a[-n:]), host(dc[-n:]), host(w)
+    zero = lambda cols: np.zeros((n, cols))
+    close(c[-n:], R.moe_gemm(at, wh, tail, zero(N)), sums(K) * R.moe_gemm(abs(at), abs(wh), tail, zero(N)), "bf16", "c")
+    want = R.moe_gemm_backward(dt, at, wh, tail, zero(K))
+    size = R.moe_gemm_backward(abs(dt), abs(at), abs(wh), tail, zero(K))
+    close(da[-n:], want[0], sums(N) * size[0], "bf16", "da")
+    close(dw, want[1], sums(n) * size[1], "f32", "dw")   # the zeros add nothing
+    assert not bool(c[:-n].any()) and not bool(da[:-n].any())
+
+
+def test_weights_past_32_bits():
+    """The last expert's rows alone; the others' gradients are zeros."""
+    rng = np.random.default_rng(3)
+    E, N, K, n = 1024, 1040, 2048, 40
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device=DEV)
+    w[-1] = normal(rng, N, K, kind="bf16")
+    assert w.numel() * 2 > 1 << 32
+    a, dc = normal(rng, n, K, kind="bf16"), normal(rng, n, N, kind="bf16")
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = n
+    c = Z.zinc_moe_gemm(a, w, off)
+    dw = torch.full_like(w, -3.0)
+    da, _ = Z.zinc_moe_gemm_backward(dc, a, w, off, dw=dw)
+    one, ah, dh, wh = np.array([0, n], np.int32), host(a), host(dc), host(w[-1:])
+    close(c, R.moe_gemm(ah, wh, one, np.zeros((n, N))), sums(K) * R.moe_gemm(abs(ah), abs(wh), one, np.zeros((n, N))),
+          "bf16", "c")
+    want = R.moe_gemm_backward(dh, ah, wh, one, np.zeros((n, K)))
+    size = R.moe_gemm_backward(abs(dh), abs(ah), abs(wh), one, np.zeros((n, K)))
+    close(da, want[0], sums(N) * size[0], "bf16", "da")
+    close(dw[-1:], want[1], sums(n) * size[1], "bf16", "dw")
+    assert not bool(dw[:-1].any())
+
+
+def test_rows_past_32_bits():
+    """SwiGLU and the adapters: the last rows as alone."""
+    rng = np.random.default_rng(5)
+    rows, cols, n, rank, K = 300_000, 8192, 40, 16, 64
+    gate, up, base = (last_rows(rng, rows, cols, n, "bf16") for _ in range(3))
+    assert gate.numel() * 2 > 1 << 32
+    assert torch.equal(Z.zinc_swiglu(gate, up)[-n:], Z.zinc_swiglu(gate[-n:], up[-n:]))
+    for got, want in zip(Z.zinc_swiglu_backward(base, gate, up), Z.zinc_swiglu_backward(base[-n:], gate[-n:], up[-n:])):
+        assert torch.equal(got[-n:], want)
+    x = last_rows(rng, rows, K, n, "bf16")
+    a, b = normal(rng, 2, rank, K, kind="bf16"), normal(rng, 2, cols, rank, kind="bf16", size=0.1)
+    ids = np.full(rows, -1)
+    ids[-n:] = rng.integers(-1, 2, n)
+    y = Z.zinc_lora(x, a, b, None, *plan_of(ids, 2), base=base)
+    want = Z.zinc_lora(x[-n:].contiguous(), a, b, None, *plan_of(ids[-n:], 2), base=base[-n:].contiguous())
+    assert torch.equal(y[-n:], want) and not bool(y[:-n].any())
+    # gradients, with the wide matrix as x
+    wide, tall = b.transpose(1, 2).contiguous(), a.transpose(1, 2).contiguous()
+    back = Z.zinc_lora_backward(x, base, wide, tall, None, *plan_of(ids, 2))
+    tail = F.sort(ids[-n:].reshape(-1, 1).astype(np.int32), 2)
+    args = [host(t) for t in (x[-n:], base[-n:], wide, tall)] + [np.ones(2)]
+    want = R.lora_backward(*args, tail, np.zeros((n, cols)))
+    size = R.lora_backward(*(np.abs(t) for t in args), tail, np.zeros((n, cols)))
+    each = split_off("bf16") + 4 * 2.0 ** -24
+    assert not bool(back[0][:-n].any())
+    close(back[0][-n:], want[0], (sums(K) + sums(2 * rank) + each) * size[0], "bf16", "dx")
+    close(back[1], want[1], (sums(K) + sums(2 * n + 64) + each) * size[1], "bf16", "da")
+    close(back[2], want[2], (sums(cols) + sums(2 * n + 64) + each) * size[2], "bf16", "db")
