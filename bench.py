@@ -17,7 +17,8 @@ with its RMS norm and residual, the 2048-token prefill over 32 layers) ride in
 "secondary".  ``--only staged`` instead times the fused prefill against its
 staged baseline (the intermediate in device memory) at M=256 and M=2048, and
 ``--only fp8`` the expert layer on block-scaled FP8 weights with its operators
-one by one.
+one by one, ``--only rows16`` the 16-bit products by expert, SwiGLU and the adapters
+with their gradients.
 
 Also in the line: the measured peaks of this chip (an MFMA-only loop, HBM
 stream read and copy; libzinc_peaks.so), the graphics clock and socket power
@@ -687,6 +688,8 @@ def secondary(args, torch):
         out += m384_lines(args, torch, np, Z, S, dev, t)
     if args.only == "fp8":      # its own run
         out += fp8_lines(args, torch, np, Z, S, dev, t)
+    if args.only == "rows16":   # its own run
+        out += rows16_lines(args, torch, np, Z, S, dev, t)
     return out
 
 
@@ -893,21 +896,8 @@ def decode_lines(args, torch, np, Z, S, dev, t):
     return out
 
 
-def fp8_lines(args, torch, np, Z, S, dev, t):
-    """The expert layer of the MoE workload (64 experts, top-8, 2048 -> 768) on
-    block-scaled FP8 weights, by tokens; then its operators one by one at 4096 tokens, and
-    the dense product at the headline layer's sizes.  Weights and rows are rotated past the
-    last-level cache."""
-    out = []
-    w = S.WORKLOADS["moe_e64"]
-    E, k, H, I = w.n_experts, w.top_k, w.hidden, w.inter
-    gen = torch.Generator(device=dev).manual_seed(w.seed)
-    randn = lambda *shape: torch.randn(shape, dtype=torch.bfloat16, device=dev, generator=gen)
-
-    def weight(R, C):   # E matrices [R, C]: their blocks of 128 rows follow one another
-        q, s = Z.zinc_fp8_quantize(randn(E * R, C) / C ** 0.5, 128)
-        return q.view(E, R, C), s.view(E, R // 128, C // 128)
-
+def call_timer(torch, out):
+    """timed(name, call): a line of `out` with the mean time of 100 calls; more=work adds its rate per microsecond."""
     def timed(name, fn, steps=100, **more):
         t0, i = time.perf_counter(), 0
         while i < 10 or time.perf_counter() - t0 < 0.05:
@@ -923,6 +913,25 @@ def fp8_lines(args, torch, np, Z, S, dev, t):
         out.append({"workload": name, "us_per_call": round(us, 3), **rates})
         log(f"[bench] {out[-1]}")
 
+    return timed
+
+
+def fp8_lines(args, torch, np, Z, S, dev, t):
+    """The expert layer of the MoE workload (64 experts, top-8, 2048 -> 768) on
+    block-scaled FP8 weights, by tokens; then its operators one by one at 4096 tokens, and
+    the dense product at the headline layer's sizes.  Weights and rows are rotated past the
+    last-level cache."""
+    out = []
+    w = S.WORKLOADS["moe_e64"]
+    E, k, H, I = w.n_experts, w.top_k, w.hidden, w.inter
+    gen = torch.Generator(device=dev).manual_seed(w.seed)
+    randn = lambda *shape: torch.randn(shape, dtype=torch.bfloat16, device=dev, generator=gen)
+
+    def weight(R, C):   # E matrices [R, C]: their blocks of 128 rows follow one another
+        q, s = Z.zinc_fp8_quantize(randn(E * R, C) / C ** 0.5, 128)
+        return q.view(E, R, C), s.view(E, R // 128, C // 128)
+
+    timed = call_timer(torch, out)
     sets = [weight(I, H) + weight(I, H) + weight(H, I) for _ in range(2)]
     for M, dtype in ((1, torch.bfloat16), (32, torch.bfloat16), (512, torch.bfloat16), (4096, torch.bfloat16),
                      (1, torch.float32), (512, torch.float32), (4096, torch.float32)):
@@ -969,6 +978,61 @@ def fp8_lines(args, torch, np, Z, S, dev, t):
         for dtype in (torch.bfloat16, torch.float32):
             timed(f"product {M} x {N} x {K}, {str(dtype)[6:]} output, 12 rotated weights",
                   lambda i: Z.zinc_gemm_fp8(a, sa, *weights[i % 12], dtype), tflops=2.0 * M * N * K)
+    return out
+
+
+def rows16_lines(args, torch, np, Z, S, dev, t):
+    """A training step's expert operators in bf16 (64 experts, top-8, 2048 -> 768, 4096 tokens), the same
+    product for a decode step, the headline layer's sizes by eight experts, and adapters beside its gate projection.
+    Rows and weights are rotated past the last-level cache."""
+    out = []
+    timed = call_timer(torch, out)
+    w = S.WORKLOADS["moe_e64"]
+    E, k, H, I = w.n_experts, w.top_k, w.hidden, w.inter
+    gen = torch.Generator(device=dev).manual_seed(w.seed)
+    randn = lambda *shape: torch.randn(shape, dtype=torch.bfloat16, device=dev, generator=gen)
+
+    def plans(M):
+        logits = [torch.randn((M, E), device=dev, generator=gen) for _ in range(8)]
+        return [Z.zinc_moe_sort(Z.zinc_moe_route_topk(v, k)[0], E)[0] for v in logits]
+
+    weights = [randn(E, I, H) / H ** 0.5 for _ in range(3)]
+    for M in (8, 512, 4096):
+        rows, offsets = M * k, plans(M)
+        x, dc = [randn(rows, H) for _ in range(3)], [randn(rows, I) for _ in range(3)]
+        timed(f"grouped product, {rows} rows of {E}, {I} x {H}",
+              lambda i: Z.zinc_moe_gemm(x[i % 3], weights[i % 3], offsets[i % 8]), tflops=2.0 * rows * I * H)
+        timed(f"its gradients, dw in fp32, {rows} rows",
+              lambda i: Z.zinc_moe_gemm_backward(dc[i % 3], x[i % 3], weights[i % 3], offsets[i % 8],
+                                                 dw_dtype=torch.float32), tflops=4.0 * rows * I * H)
+    up = [randn(rows, I) for _ in range(3)]
+    timed(f"SwiGLU, {rows} x {I}", lambda i: Z.zinc_swiglu(dc[i % 3], up[i % 3]), tb_s=6.0 * rows * I)
+    timed(f"its gradients, {rows} x {I}", lambda i: Z.zinc_swiglu_backward(up[(i + 1) % 3], dc[i % 3], up[i % 3]),
+          tb_s=10.0 * rows * I)
+    del x, dc, up, weights
+    N, K = 11008, 4096
+    rows, offsets = 8192, torch.arange(0, 8193, 1024, dtype=torch.int32, device=dev)
+    x, big = [randn(rows, K) for _ in range(3)], [randn(8, N, K) / K ** 0.5 for _ in range(2)]
+    timed(f"grouped product, {rows} rows of 8, {N} x {K}", lambda i: Z.zinc_moe_gemm(x[i % 3], big[i % 2], offsets),
+          tflops=2.0 * rows * N * K)
+    del big
+    scales = torch.ones(64, device=dev)
+    for M, A, r in ((32, 64, 16), (8192, 8, 64), (8192, 8, 16)):
+        ids = torch.randint(0, A, (M, 1), device=dev, generator=gen, dtype=torch.int32)
+        if M > 32:   # prompts one after the other
+            ids = (torch.arange(M, device=dev, dtype=torch.int32) // (M // A))[:, None].contiguous()
+        plan = Z.zinc_moe_sort(ids, A)
+        a, b = [randn(A, r, K) / K ** 0.5 for _ in range(3)], [randn(A, N, r) / r ** 0.5 for _ in range(3)]
+        base = [randn(M, N) for _ in range(3)]
+        timed(f"adapters, {M} rows, {A} of rank {r}, {K} -> {N}, in place",
+              lambda i: Z.zinc_lora(x[i % 3][:M], a[i % 3], b[i % 3], scales[:A], *plan, base=base[i % 3], y=base[i % 3]),
+              tb_s=2.0 * M * (K + 2 * N) + 2.0 * A * r * (K + N))
+        if M > 32:
+            grad = [randn(M, K) for _ in range(3)]
+            timed(f"their gradients, {M} rows, {A} of rank {r}",
+                  lambda i: Z.zinc_lora_backward(base[i % 3], x[i % 3], a[i % 3], b[i % 3], scales[:A], *plan,
+                                                 base=grad[i % 3], dx=grad[i % 3]),
+                  tb_s=2.0 * M * (3 * K + N) + 4.0 * A * r * (K + N))
     return out
 
 
@@ -1083,8 +1147,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=300)
     ap.add_argument("--no-secondary", action="store_true")
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--only", choices=["decode", "moe", "block", "m2048", "staged", "m384", "fp8", "peaks",
-                                       "cpu"],
+    ap.add_argument("--only", choices=["decode", "moe", "block", "m2048", "staged", "m384", "fp8", "rows16",
+                                       "peaks", "cpu"],
                     default=None,
                     help="development and profiling runs: skip the headline and run one part (a secondary line, "
                          "the measured peaks, or the full CPU oracle table including one-thread figures)")

@@ -74,11 +74,9 @@ hipError_t run_both(const Gemm16Args& a, const Gemm16Args& w, hipStream_t stream
   int bytes = 0;
   hipError_t e = gemm16_grid<Both<INPUT, WEIGHT>>(a, kernel, 0, &grid, &bytes);
   if (e != hipSuccess) return e;
-  for (int32_t* q : {a.queue, w.queue}) {
-    hipLaunchKernelGGL(k_gemm16_queue, dim3(1), dim3(8), 0, stream, q, (int)grid / 8);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  hipLaunchKernelGGL(k_gemm16_queue, dim3(1), dim3(16), 0, stream, a.queue, (int)grid / 8);   // both: w's follows
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   timing_begin(stream);
   hipLaunchKernelGGL((k_gemm16_both<INPUT, WEIGHT>), dim3(grid), dim3(INPUT::THREADS), bytes, stream, a, w);
   timing_end(stream);

@@ -42,14 +42,14 @@ inline long long shrink_blocks(bool forward, const ShrinkArgs& s) {
   return max_row_tiles(s.plan.M, s.plan.E, 16 * lora_row_tiles(s.plan.M, s.plan.E, s.rank, forward)) * s.splits;
 }
 
-// Spans of the columns in a second product: 1024 columns (rank 16 67 us, 512 columns 70; rank 64 84, 512 88, 2816 92), down to 256 where there
-// are fewer than eight workgroups a CU.
+// Spans of the columns in a second product: 1024 columns (8192 x 11008, rank 64 84 us, 512 columns 88, 768 92, 2816 92),
+// down to 256 where there are fewer than two workgroups a CU.
 inline ExpandArgs expand_of(bool forward, const ShrinkArgs& f, const void* w, int N, const float* scales,
                             const void* base, void* y) {
   ExpandArgs s{f.plan, f.parts, f.splits, f.rank, N, w, scales, base, y, 0, 0, 0, 0};
   s.row_tiles = (int)max_row_tiles(f.plan.M, f.plan.E, 16 * lora_row_tiles(f.plan.M, f.plan.E, f.rank, forward));
   const int least = ceil_div(N, 1024), most = ceil_div(N, 256);
-  int spans = 2048 / (s.row_tiles ? s.row_tiles : 1);
+  int spans = 512 / (s.row_tiles ? s.row_tiles : 1);
   spans = spans < least ? least : spans > most ? most : spans;
   s.span = ceil_div(ceil_div(N, spans), 256) * 256;
   s.spans = ceil_div(N, s.span);
