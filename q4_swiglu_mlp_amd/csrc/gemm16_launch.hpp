@@ -20,7 +20,8 @@ struct Gemm16Shape {
 constexpr Gemm16Shape kGemm16Shapes[] = {{256, 256, 1, 3, 1.08, 0.49, 1.54, 5.2},
                                          {128, 256, 1, 4, 0.57, 0.96, 0.46, 6.1},
                                          {128, 128, 2, 3, 0.65, 0.51, 1.6, 4.7},
-                                         {64, 128, 3, 3, 0.48, 0.34, 1.66, 7.7}};
+                                         {64, 128, 3, 3, 0.48, 0.34, 1.66, 7.7},
+                                         {64, 128, 2, 4, 0.2, 0.4, 0.52, 3.8}};   // the last one's, of c: three buffers
 
 struct Gemm16Plan {
   int shape, splits;
@@ -48,10 +49,10 @@ inline size_t gemm16_part_bytes(Product f, int M, int E, int N, int K) {
 
 // The cut with the least time by a model fitted to 4388 timings: 90 products of 1 - 256 experts of uneven sizes, 1 -
 // 30000 rows, each with its gradients, in every tile, in 1 - 16 parts, dealt out or not.  It is off by 17 % on average;
-// what it picks takes 4 % more than the best on average (da 2 %, dw 6 %), 53 % in the worst of 90.
-// Examples, us, in the order of the tiles, in one part: 32768 rows of 64 x 768 x 2048 124, 132, 150 and 173, dw in
-// fp32 178, 191, 203 and 250; 2331 of 7 x 520 x 1032 31, 21, 19 and 16; 64 of 64 x 768 x 2048 49, 34, 38 and 36,
-// and 28 in two parts of the last.  For 256 CUs.
+// what it picks takes 4 % more than the best on average (c 3.5 %, da 2 %, dw 5 %), 48 % in the worst of 360.
+// Examples, us, in the order of the tiles, in one part: 32768 rows of 64 x 768 x 2048 124, 132, 150 and 171, dw in
+// fp32 178, 191, 203 and 250; 2331 of 7 x 520 x 1032 31, 21, 19 and 13; 64 of 64 x 768 x 2048 49, 34, 38 and 32,
+// and 27 in two parts of the last.  For 256 CUs.
 // small: the smallest tile, in one part, dealt out in turn.
 inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small = false) {
   constexpr int kCus = 256;
@@ -66,7 +67,7 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
   if (M == 0) return best;   // (dw of no rows)
   double least = 1e30;
   for (int i = small ? 3 : 0; i < 4; ++i) {
-    const Gemm16Shape& s = kGemm16Shapes[i];
+    const Gemm16Shape& s = kGemm16Shapes[i == 3 && f == kForward ? 4 : i];
     const double col_tiles = (cols + s.TN - 1) / s.TN;
     double row_tiles = used * ((N + s.TM - 1) / s.TM);
     if (!weight) {   // an expert's last tile is partly filled
@@ -106,7 +107,8 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
           if (us < longest) us = longest;
         }
         if (weight) us += (1 - used / E) * out * bytes * splits / 5.3e6;   // zeros for experts without rows
-        if (us < (read + bytes * splits * out) / 6.4e6) us = (read + bytes * splits * out) / 6.4e6;
+        const double memory = (read + bytes * splits * out) / (rounds <= 1.05 ? 5.5e6 : 6.4e6);
+        if (us < memory) us = memory;
         if (us < 8) us = 7.2 + 0.1 * us;   // the host's time for one launch, which another adds to
         us += (queue ? 6 : 0) + (splits > 1 ? 2.8 + (splits * 4 + 3) * out / 4.9e6 : 0);
         if (us < least) {
@@ -168,7 +170,7 @@ hipError_t run_gemm16(const Gemm16Args& g, int shape, hipStream_t stream) {
   if (shape == 0) return run_gemm16<Gemm16<F, 256, 256, 2, 4, 2, T, O>>(g, 0, stream);
   if (shape == 1) return run_gemm16<Gemm16<F, 128, 256, 2, 4, 3, T, O>>(g, 1, stream);
   if (shape == 2) return run_gemm16<Gemm16<F, 128, 128, 2, 2, 2, T, O>>(g, 2, stream);
-  return run_gemm16<Gemm16<F, 64, 128, 1, 4, 2, T, O>>(g, 3, stream);
+  return run_gemm16<Gemm16<F, 64, 128, 1, 4, F == kForward ? 3 : 2, T, O>>(g, 3, stream);
 }
 
 // f(T, O) for the type codes of the operands (0 fp16, 1 bf16) and of the output (the same, or 2 fp32).

@@ -77,6 +77,12 @@ struct Gemm16 {
   static constexpr int PI = TM / 8 / WAVES, QI = TN / 8 / WAVES, COPIES = PI + QI;   // copies a wave, a step
   static constexpr int BUFFER = (TM + TN) * 128;
   static constexpr int NBUF = BUFFERS;
+  // The smallest tile's waves hold a step's fragments in full, so its buffer is free, and the next step's reads and copies
+  // on their way, from the step's start; a CU that holds one workgroup otherwise waits for each read (2331 rows of 7 x
+  // 520 x 1032: 16.3 us, so 16.1, and 12.6 with the three buffers that the forward product takes).  Over 90 products the
+  // best of all cuts takes 4 % less so; three buffers, and two workgroups a CU instead of three, cost dw 2 %, da gains 1 %
+  // with two or three.
+  static constexpr bool EAGER = NT == 2;
   static constexpr int BAND = 8;   // row tiles walked per column
   // Large tiles' outputs are stored past the caches, in whole lines: 32768 rows of 64 experts, 768 x 2048, dw in fp32
   // 143 us, in lines that the caches hold 180, in half lines 166 and 183 (half as much again is written); da
@@ -340,7 +346,8 @@ struct Gemm16 {
       const i16x4_t lo = read_turned(at + (32 * h) * width * 2), hi = read_turned(at + (32 * h + 4) * width * 2);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    i16x8_t pf[2][2], qf[NT][2];
+    constexpr int SLOTS = EAGER ? MT : 2;
+    i16x8_t pf[SLOTS][2], qf[NT][2];
     auto read_p = [&](int i, int slot, int buf) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -382,7 +389,8 @@ struct Gemm16 {
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int j = 0; j < NT; ++j) read_q(j, 0);
-    read_p(0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < (EAGER ? MT : 1); ++i) read_p(i, i, 0);
     int buf = 0;
     auto after = [](int b) { return NBUF == 2 ? b ^ 1 : b == NBUF - 1 ? 0 : b + 1; };
     constexpr int EACH = (COPIES + NT - 1) / NT;   // copies beside a column of the last two row tiles
@@ -418,6 +426,40 @@ struct Gemm16 {
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
       for (int k = 0; k < cu.steps; ++k, buf = after(buf)) {
         const int next = after(buf);
+        if constexpr (EAGER) {
+          landed(ahead);
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          const bool more = is_more;
+          if (more) {
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) copy_piece(i, buf);
+          }
+#pragma unroll
+          for (int i = 0; i < MT - 2; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < NT; ++j) acc[i][j] = mfma16(qf[j][h], pf[i][h], acc[i][j], T{});
+            read_p(i, i, next);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              acc[MT - 2][j] = mfma16(qf[j][h], pf[SLOTS - 2][h], acc[MT - 2][j], T{});
+              acc[MT - 1][j] = mfma16(qf[j][h], pf[SLOTS - 1][h], acc[MT - 1][j], T{});
+            }
+            read_q(j, next);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          read_p(MT - 2, SLOTS - 2, next);
+          read_p(MT - 1, SLOTS - 1, next);
+          advance();
+          if (!more) ahead = 0;
+          continue;
+        }
         // all columns of one row tile after the other, the next tile's fragment on its way
 #pragma unroll
         for (int i = 0; i < MT - 2; ++i) {

@@ -163,7 +163,8 @@ CUTS = [(1, 1, 8, 8), (1, 1, 8, 800), (1, 2, 840, 8), (1685, 2, 8, 8), (33443, 3
         (34950, 130, 8, 136), (2008, 1, 3040, 2336), (19076, 1, 8, 920), (636, 300, 912, 144), (9572, 9, 2056, 136),
         (27503, 130, 392, 160), (17469, 130, 984, 288), (229, 130, 288, 928), (77, 130, 728, 144), (13234, 9, 2656, 136),
         (150, 130, 2992, 136), (86, 130, 464, 136), (25271, 9, 1224, 144), (11663, 20, 2120, 136), (713, 300, 80, 8),
-        (269, 300, 2616, 8), (169, 300, 8, 6968), (17042, 60, 648, 688), (1, 1, 1264, 8)]
+        (269, 300, 2616, 8), (169, 300, 8, 6968), (17042, 60, 648, 688), (1, 1, 1264, 8),
+        (28194, 130, 200, 376), (3739, 20, 8, 3168), (17984, 130, 312, 688), (1088, 300, 160, 432)]
 
 
 @pytest.mark.parametrize("kind,wide", [("bf16", True), ("f16", False)])
@@ -671,7 +672,7 @@ def test_a_workspace_is_reused_and_its_end_kept():
 
 # c and da in parts, da and c dealt out, dw in parts, dw dealt out, both dealt out in one launch
 WITH_WORKSPACE = [(40, 1, 8, 800), (40, 2, 840, 8), (210, 300, 672, 264), (229, 130, 288, 928), (1685, 2, 8, 8),
-                  (269, 300, 2616, 8), (17042, 60, 648, 688)]
+                  (269, 300, 2616, 8), (17042, 60, 648, 688), (1088, 300, 160, 432), (3739, 20, 8, 3168)]
 
 
 def product_state(seed, rows, E, N, K):
