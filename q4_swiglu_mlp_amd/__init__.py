@@ -239,9 +239,15 @@ def _check(status: int, where: str) -> None:
 # Temporaries (y, the workspace) are allocated on the stream the call is
 # enqueued on, so the caching allocator does not hand their memory to other
 # work while that stream still uses it.
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> int | None:
@@ -686,14 +692,14 @@ class _Call:
             if not need:
                 return None, 0, None
             ws = self.empty((need,), _torch().uint8)
+            return ws.data_ptr(), need, ws
         return ws.data_ptr(), _nbytes(ws), ws
 
     def run(self, name: str, *args) -> None:
-        cuda = _torch().cuda
-        if cuda.current_device() == self.index:
+        if _torch()._C._cuda_getDevice() == self.index:
             status = getattr(lib, name)(*args, self.raw)
         else:
-            with cuda.device(self.index):
+            with _torch().cuda.device(self.index):
                 status = getattr(lib, name)(*args, self.raw)
         if status:
             _check(status, name)
@@ -997,18 +1003,18 @@ def _out_code(dtype, of, what: str) -> int:
     return _type_code(dtype, what)
 
 
-def _expert_weights(w, dtype, what: str = "w"):
-    """(experts, rows, columns) of contiguous 16-bit matrices [n_experts, N, K]."""
+def _expert_weights(w, dtype, N: int | None, K: int | None):
+    """(experts, rows, columns) of contiguous 16-bit matrices w [n_experts, N, K]; None: any multiple of eight."""
     if w is None or w.dim() != 3:
-        raise ValueError(f"{what} must be a 3-D [n_experts, N, K] tensor")
-    E, N, K = w.shape
+        raise ValueError("w must be a 3-D [n_experts, N, K] tensor")
+    E, rows, cols = w.shape
     if E < 1 or E > 1024:
-        raise ValueError(f"{what} must hold 1..1024 matrices")
-    for n in (N, K):
+        raise ValueError("w must hold 1..1024 matrices")
+    for n in (rows, cols):
         if n <= 0 or n % 8 or n > 65536:
-            raise ValueError(f"{what}'s matrices must have multiples of 8 rows and columns, at most 65536")
-    _fits(w, dtype, (E, N, K), what)
-    return E, N, K
+            raise ValueError("w's matrices must have multiples of 8 rows and columns, at most 65536")
+    _fits(w, dtype, (E, N or rows, K or cols), "w")
+    return E, rows, cols
 
 
 def zinc_moe_gemm(a, w, offsets, out_dtype=None, out=None, workspace=None, stream=None):
@@ -1017,8 +1023,7 @@ def zinc_moe_gemm(a, w, offsets, out_dtype=None, out=None, workspace=None, strea
     are left as they were."""
     torch = _torch()
     code, rows, K = _rows16(a, "a")
-    E, N, _ = _expert_weights(w, a.dtype)
-    _fits(w, a.dtype, (E, N, K), "w")
+    E, N, _ = _expert_weights(w, a.dtype, None, K)
     _fits(offsets, torch.int32, (E + 1,), "offsets")
     dtype = out_dtype or (a.dtype if out is None else out.dtype)
     out_code = _out_code(dtype, a.dtype, "out_dtype")
@@ -1040,8 +1045,7 @@ def zinc_moe_gemm_backward(dc, a, w, offsets, da_dtype=None, dw_dtype=None, da=N
     were; dw of an expert without rows is zeros."""
     torch = _torch()
     code, rows, N = _rows16(dc, "dc")
-    E, _, K = _expert_weights(w, dc.dtype)
-    _fits(w, dc.dtype, (E, N, K), "w")
+    E, _, K = _expert_weights(w, dc.dtype, N, None)
     _fits(a, dc.dtype, (rows, K), "a")
     _fits(offsets, torch.int32, (E + 1,), "offsets")
     if not want_da and not want_dw or (da is not None and not want_da) or (dw is not None and not want_dw):
