@@ -1025,7 +1025,8 @@ def rows16_lines(args, torch, np, Z, S, dev, t):
         a, b = [randn(A, r, K) / K ** 0.5 for _ in range(3)], [randn(A, N, r) / r ** 0.5 for _ in range(3)]
         base = [randn(M, N) for _ in range(3)]
         timed(f"adapters, {M} rows, {A} of rank {r}, {K} -> {N}, in place",
-              lambda i: Z.zinc_lora(x[i % 3][:M], a[i % 3], b[i % 3], scales[:A], *plan, base=base[i % 3], y=base[i % 3]),
+              lambda i: Z.zinc_lora(x[i % 3][:M], a[i % 3], b[i % 3], scales[:A], *plan, base=base[i % 3],
+                                    y=base[i % 3]),
               tb_s=2.0 * M * (K + 2 * N) + 2.0 * A * r * (K + N))
         if M > 32:
             grad = [randn(M, K) for _ in range(3)]

@@ -77,11 +77,11 @@ struct Gemm16 {
   static constexpr int PI = TM / 8 / WAVES, QI = TN / 8 / WAVES, COPIES = PI + QI;   // copies a wave, a step
   static constexpr int BUFFER = (TM + TN) * 128;
   static constexpr int NBUF = BUFFERS;
-  // The smallest tile's waves hold a step's fragments in full, so its buffer is free, and the next step's reads and copies
-  // on their way, from the step's start; a CU that holds one workgroup otherwise waits for each read (2331 rows of 7 x
-  // 520 x 1032: 16.3 us, so 16.1, and 12.6 with the three buffers that the forward product takes).  Over 90 products the
-  // best of all cuts takes 4 % less so; three buffers, and two workgroups a CU instead of three, cost dw 2 %, da gains 1 %
-  // with two or three.
+  // The smallest tile's waves hold a step's fragments in full, so its buffer is free, and the next step's reads and
+  // copies on their way, from the step's start; a CU that holds one workgroup otherwise waits for each read (2331
+  // rows of 7 x 520 x 1032: 16.3 us, so 16.1, and 12.6 with the three buffers that the forward product takes).  Over
+  // 90 products the best of all cuts takes 4 % less so; three buffers, and two workgroups a CU instead of three, cost
+  // dw 2 %, da gains 1 % with two or three.
   static constexpr bool EAGER = NT == 2;
   static constexpr int BAND = 8;   // row tiles walked per column
   // Large tiles' outputs are stored past the caches, in whole lines: 32768 rows of 64 experts, 768 x 2048, dw in fp32

@@ -1,10 +1,10 @@
 // Both gradients of a 16-bit product by expert, in one launch where that is less.  Where both are many units of the
 // largest tile, a workgroup that finds no more units of da goes on with those of dw, the experts with most
 // rows first, so the last round of the one is work for the same CUs (32768 rows of 64 experts, 768 x 2048, dw in
-// fp32, operands from HBM: 310 us, in two launches 323; where every second workgroup begins with dw 330).
+// fp32, operands from HBM: 290 us, in two launches 303; 6 % more where every second workgroup begins with dw).
 // Where both are a few units, or bound by memory, the smallest tile's workgroups for da and for dw lie side by side (47
-// rows of 16 experts, 1752 x 696: 28 us, one after the other 43; 1111 of 7, 520 x 1032, fp16: 13 and 22): by the model's
-// times, as if four fifths of the shorter were added to the longer (over 200 drawn sizes 6 % less on average).
+// rows of 16 experts, 1752 x 696: 28 us, one after the other 43; 1111 of 7, 520 x 1032, fp16: 13 and 22): by the
+// model's times, as if four fifths of the shorter were added to the longer (over 200 drawn sizes 6 % less on average).
 #include "gemm16_launch.hpp"
 
 namespace zinc {
@@ -106,7 +106,8 @@ hipError_t launch_gemm16_backward(const void* dc, const void* a, const void* w, 
     });
   }
   if (da && dw && M && p.beside) {
-    const Gemm16Args ga{dc, w, offsets, E, M, N, K, da, 1, 0, nullptr}, gw{dc, a, offsets, E, M, N, K, dw, 1, 0, nullptr};
+    const Gemm16Args ga{dc, w, offsets, E, M, N, K, da, 1, 0, nullptr};
+    const Gemm16Args gw{dc, a, offsets, E, M, N, K, dw, 1, 0, nullptr};
     return by_types(type, da_type, [&](auto t, auto oa) {
       using T = decltype(t);
       using OA = decltype(oa);

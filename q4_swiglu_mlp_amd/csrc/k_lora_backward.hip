@@ -16,8 +16,9 @@ __global__ __launch_bounds__(256, lora_held(H::kTiles)) void k_lora_firsts(Shrin
 }
 
 template <typename DX, typename DA, typename DB>
-__global__ __launch_bounds__(256, lora_held(DX::kTiles)) void k_lora_seconds(ExpandArgs dx, LoraGradArgs da, LoraGradArgs db, int a_blocks,
-                                                      int b_blocks) {
+__global__ __launch_bounds__(256, lora_held(DX::kTiles)) void k_lora_seconds(ExpandArgs dx, LoraGradArgs da,
+                                                                               LoraGradArgs db, int a_blocks,
+                                                                               int b_blocks) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int block = blockIdx.x;
   if (block < a_blocks)
@@ -85,18 +86,19 @@ hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, co
     hipError_t e = allow_lds<H>(reinterpret_cast<const void*>(&k_lora_firsts<H, DH>), kLds);
     if (e == hipSuccess) e = allow_lds<DX>(reinterpret_cast<const void*>(&k_lora_seconds<DX, DA, DB>), kLds);
     if (e != hipSuccess) return e;
-    const long long h_blocks = M && db ? shrink_blocks(false, h) : 0, dh_blocks = M && (dx || da) ? shrink_blocks(false, dh) : 0;
+    const long long h_blocks = M && db ? shrink_blocks(false, h) : 0;
+    const long long dh_blocks = M && (dx || da) ? shrink_blocks(false, dh) : 0;
     if (h_blocks + dh_blocks) {
-      hipLaunchKernelGGL((k_lora_firsts<H, DH>), dim3((unsigned)(h_blocks + dh_blocks)), dim3(256), first, stream, h, dh,
-                         (int)h_blocks);
+      hipLaunchKernelGGL((k_lora_firsts<H, DH>), dim3((unsigned)(h_blocks + dh_blocks)), dim3(256), first, stream,
+                         h, dh, (int)h_blocks);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     const long long a_blocks = da ? grad_blocks(ga) : 0, b_blocks = db ? grad_blocks(gb) : 0;
     const long long x_blocks = dx ? expand_blocks(ex) : 0;
     if (a_blocks + b_blocks + x_blocks == 0) return e;
-    hipLaunchKernelGGL((k_lora_seconds<DX, DA, DB>), dim3((unsigned)(a_blocks + b_blocks + x_blocks)), dim3(256), second,
-                       stream, ex, ga, gb, (int)a_blocks, (int)b_blocks);
+    hipLaunchKernelGGL((k_lora_seconds<DX, DA, DB>), dim3((unsigned)(a_blocks + b_blocks + x_blocks)), dim3(256),
+                       second, stream, ex, ga, gb, (int)a_blocks, (int)b_blocks);
     return hipGetLastError();
   });
   const JoinArgs ja{parts_a, sa, (size_t)rank * K, da && sa > 1 ? (size_t)E * rank * K : 0, da};

@@ -32,8 +32,8 @@ hipError_t launch_lora(const void* x, const void* a, const void* b, const float*
     hipError_t e = allow_lds<SHRINK>(reinterpret_cast<const void*>(&k_lora_shrink<SHRINK>), kLds);
     if (e == hipSuccess) e = allow_lds<EXPAND>(reinterpret_cast<const void*>(&k_lora_expand<EXPAND>), kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_lora_shrink<SHRINK>, dim3((unsigned)shrink_blocks(true, s)), dim3(256), SHRINK::smem_bytes(), stream,
-                       s);
+    hipLaunchKernelGGL(k_lora_shrink<SHRINK>, dim3((unsigned)shrink_blocks(true, s)), dim3(256), SHRINK::smem_bytes(),
+                       stream, s);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_lora_expand<EXPAND>, dim3((unsigned)expand_blocks(x2)), dim3(256), EXPAND::smem_bytes(),

@@ -37,8 +37,8 @@ __device__ __forceinline__ void two_terms(float v, T& hi, T& lo) {
   lo = (T)(__builtin_isfinite(rest) ? rest : 0.0f);   // an infinity stays one
 }
 
-// The power of two that brings values of at most `top` (the bits of a largest finite magnitude) to 2^13 and above, below
-// 2^14, as the exponent to multiply by; bf16 has fp32's range and needs none.
+// The power of two that brings values of at most `top` (the bits of a largest finite magnitude) to 2^13 and above,
+// below 2^14, as the exponent to multiply by; bf16 has fp32's range and needs none.
 __device__ __forceinline__ int lift(uint32_t top, _Float16) {
   if (top == 0) return 0;
   const int e = 13 + 127 - (int)(top >> 23);

@@ -11,7 +11,8 @@ inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // Row tiles of 16 a workgroup takes: one where adapters have few rows, else as many as the registers hold
 // with two workgroups a CU.  8192 rows, eight adapters, 4096 to 11008, us: the second product through the
 // caches of rank 16 74 with two, 80 with four, 75 with one; of rank 32 78 and 81; of rank 64 104 with two, 91 with
-// four, but 101 and 115 where its matrix is turned (dx); the first of rank 16 15 - 17 with any, of rank 64 27 with two, 40 with one.
+// four, but 101 and 115 where its matrix is turned (dx); the first of rank 16 15 - 17 with any, of rank 64 27 with
+// two, 40 with one.
 // Of the forward call's first product, 23 with four in one workgroup a CU.
 inline int lora_row_tiles(int M, int E, int rank, bool forward) {
   if (M / E <= 24 || rank > 128) return 1;
@@ -42,8 +43,8 @@ inline long long shrink_blocks(bool forward, const ShrinkArgs& s) {
   return max_row_tiles(s.plan.M, s.plan.E, 16 * lora_row_tiles(s.plan.M, s.plan.E, s.rank, forward)) * s.splits;
 }
 
-// Spans of the columns in a second product: 1024 columns (8192 x 11008, rank 64 84 us, 512 columns 88, 768 92, 2816 92),
-// down to 256 where there are fewer than two workgroups a CU.
+// Spans of the columns in a second product: 1024 columns (8192 x 11008, rank 64 84 us, 512 columns 88, 768 92,
+// 2816 92), down to 256 where there are fewer than two workgroups a CU.
 inline ExpandArgs expand_of(bool forward, const ShrinkArgs& f, const void* w, int N, const float* scales,
                             const void* base, void* y) {
   ExpandArgs s{f.plan, f.parts, f.splits, f.rank, N, w, scales, base, y, 0, 0, 0, 0};

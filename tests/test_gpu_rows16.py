@@ -164,7 +164,8 @@ CUTS = [(1, 1, 8, 8), (1, 1, 8, 800), (1, 2, 840, 8), (1685, 2, 8, 8), (33443, 3
         (27503, 130, 392, 160), (17469, 130, 984, 288), (229, 130, 288, 928), (77, 130, 728, 144), (13234, 9, 2656, 136),
         (150, 130, 2992, 136), (86, 130, 464, 136), (25271, 9, 1224, 144), (11663, 20, 2120, 136), (713, 300, 80, 8),
         (269, 300, 2616, 8), (169, 300, 8, 6968), (17042, 60, 648, 688), (1, 1, 1264, 8),
-        (28194, 130, 200, 376), (3739, 20, 8, 3168), (17984, 130, 312, 688), (1088, 300, 160, 432)]
+        (28194, 130, 200, 376), (3739, 20, 8, 3168), (17984, 130, 312, 688), (1088, 300, 160, 432),
+        (3, 1, 65536, 8), (3, 2, 8, 65536), (300, 1, 65536, 72), (300, 1024, 72, 264)]
 
 
 @pytest.mark.parametrize("kind,wide", [("bf16", True), ("f16", False)])
@@ -338,7 +339,8 @@ def adapter_ids(rng, M, E):
 
 LORA = [(1, 1, 8, 8, 8), (1, 4, 16, 264, 72), (7, 3, 8, 40, 520), (33, 64, 24, 136, 1032), (64, 1, 64, 512, 264),
         (200, 2, 16, 1032, 1040), (300, 3, 72, 264, 520), (130, 2, 128, 256, 136), (150, 2, 256, 136, 264),
-        (90, 3, 200, 72, 72), (1500, 2, 32, 520, 136), (1100, 1, 40, 72, 600)]
+        (90, 3, 200, 72, 72), (1500, 2, 32, 520, 136), (1100, 1, 40, 72, 600), (3, 1, 256, 65536, 8), (5, 2, 8, 8, 65536),
+        (130, 1, 64, 65536, 72), (200, 1024, 16, 72, 40)]
 
 
 def lora_inputs(rng, M, E, rank, K, N, kind):
