@@ -60,19 +60,26 @@ __device__ __forceinline__ void trade_lines(i16x8_t& first, i16x8_t& second) {
   second = __builtin_bit_cast(i16x8_t, y);
 }
 
-// Four values of f: the sum of their parts in order, four parts in flight.
-__device__ __forceinline__ f32x4_t sum_parts(const float* from, int splits, size_t stride) {
-  f32x4_t v = *reinterpret_cast<const f32x4_t*>(from);
-  for (int q = 1; q < splits; q += 4) {
-    f32x4_t t[4];
+// F pieces of f a thread: the sums of their parts in order; load(part, piece).  The first part and up to four more of
+// every piece are in flight at a time (1626 rows of 16 adapters of rank 128, gradients: the second launch 34 us, piece
+// by piece 50).
+template <int F, typename LOAD>
+__device__ __forceinline__ void sum_parts(f32x4_t (&v)[F], int splits, LOAD load) {
+  constexpr int G = F <= 2 ? 4 : F <= 4 ? 2 : 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      t[i] = *reinterpret_cast<const f32x4_t*>(from + (q + i < splits ? q + i : 0) * stride);
+  for (int i = 0; i < F; ++i) v[i] = load(0, i);
+  for (int q = 1; q < splits; q += G) {
+    f32x4_t t[G][F];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (q + i < splits) v += t[i];
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < F; ++i) t[g][i] = load(q + g < splits ? q + g : 0, i);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        if (q + g < splits) v[i] += t[g][i];
   }
-  return v;
 }
 
 // ---------------------------------------------------------------- the first products
@@ -340,12 +347,17 @@ struct Expand {
 
     float* f = reinterpret_cast<float*>(smem);
     int* lifts = reinterpret_cast<int*>(f + TM * STRIDE);
-    for (int i = tid * 4; i < TM * JT * 16; i += 1024) {
-      const int m = i / (JT * 16), j = i - m * (JT * 16);
-      f32x4_t v = {};
-      if (m < rt.rows && j < rank)
-        v = sum_parts(s.parts + (size_t)(rt.first + m) * rank + j, s.splits, (size_t)s.plan.M * rank);
-      *reinterpret_cast<f32x4_t*>(f + m * STRIDE + j) = v;
+    constexpr int F = (TM * JT * 16 + 1023) / 1024;
+    f32x4_t v[F];
+    sum_parts(v, s.splits, [&](int q, int i) {
+      const int m = (i * 1024 + tid * 4) / (JT * 16), j = (i * 1024 + tid * 4) - m * (JT * 16);
+      if (m >= rt.rows || j >= rank) return f32x4_t{};
+      return *reinterpret_cast<const f32x4_t*>(s.parts + (q * (size_t)s.plan.M + rt.first + m) * rank + j);
+    });
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int m = (i * 1024 + tid * 4) / (JT * 16), j = (i * 1024 + tid * 4) - m * (JT * 16);
+      if (m < TM) *reinterpret_cast<f32x4_t*>(f + m * STRIDE + j) = v[i];
     }
     __syncthreads();
     if constexpr (!__is_same(T, __bf16)) {   // four threads a row
@@ -486,13 +498,11 @@ struct LoraGrad {
       for (int i = 0; i < 4; ++i)
         zv[i] = rows[i] >= 0 && zc < s.C ? load16(static_cast<const T*>(s.z) + (size_t)rows[i] * s.C + zc) : i16x8_t{};
       load_rows(p + 64);
-#pragma unroll
-      for (int i = 0; i < JT; ++i) {
+      sum_parts(fv, s.f_splits, [&](int q, int i) {   // (f of a position without a row is zero)
         const int at = p + (i * 256 + tid) / (JT * 4), j = ((i * 256 + tid) % (JT * 4)) * 4;
-        fv[i] = f32x4_t{};
-        if (at < p1 && j < rank)   // (f of a position without a row is zero)
-          fv[i] = sum_parts(s.f + (size_t)at * rank + j, s.f_splits, (size_t)s.plan.M * rank);
-      }
+        if (at >= p1 || j >= rank) return f32x4_t{};
+        return *reinterpret_cast<const f32x4_t*>(s.f + (q * (size_t)s.plan.M + at) * rank + j);
+      });
     };
     f32x4_t acc[2][JT] = {};
     int lifted = 100;   // the sums are of f times 2^lifted
