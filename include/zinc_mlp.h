@@ -498,9 +498,9 @@ int zinc_swiglu_backward(const void* dh, const void* gate, const void* up, int32
  *   da_e = scales[e] sum_m dh[m] x[m]^T,   db_e = scales[e] sum_m dy[m] (A_e x[m])^T     over the rows of e
  * (zeros for an adapter without rows, also where M is 0).  The gradient of base is dy itself.  dx, da or db
  * may be NULL: it is then not computed.
- * A x and dh are kept in fp32; where they are operands again they are split in two 16-bit terms (16
- * bits of a value in bf16, 21 in fp16), sums are fp32 and results are rounded once.  Nothing depends on the
- * order of the GPU's work: equal inputs give equal bits.
+ * A x and dh are kept in fp32; where they are operands again they are split in 16-bit terms (three in bf16, which
+ * are the value itself, two in fp16, 22 bits of it), sums are fp32 and results are rounded once.  Nothing depends on
+ * the order of the GPU's work: equal inputs give equal bits.
  * K and N: multiples of 8 up to 65536, rank a multiple of 8 up to 256 (else ZINC_ERR_SHAPE); M <= 2^24,
  * n_adapters <= 1024 (else ZINC_ERR_ARG).  Matrices and the workspace are 16-byte aligned, scales and the
  * plan 4.  The workspace sizes are non-decreasing in M.

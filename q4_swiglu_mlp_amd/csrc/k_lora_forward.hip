@@ -10,7 +10,7 @@ __global__ __launch_bounds__(256, KERNEL::TM == 64 ? 1 : lora_held(KERNEL::kTile
 }
 
 template <typename KERNEL>
-__global__ __launch_bounds__(256, lora_held(KERNEL::kTiles)) void k_lora_expand(ExpandArgs s) {
+__global__ __launch_bounds__(256, 2) void k_lora_expand(ExpandArgs s) {
   extern __shared__ __align__(16) uint8_t smem[];
   KERNEL::run(s, blockIdx.x, smem);
 }

@@ -5,9 +5,11 @@
 // a row's place in the plan, by adapter.
 //
 // h and dh are kept in fp32 as parts of their sums ([splits][rows][rank], added in order where they are
-// read).  As operands of the second products they are two 16-bit terms, high and low: 16 bits of a value in
-// bf16, 21 in fp16, so that they cost the 16-bit results nothing.  fp16's range is not fp32's: its terms
-// are taken of h times a power of two, of the row (expand) or of all rows so far (gradients of A and B).
+// read).  As operands of the second products they are sums of 16-bit terms: three in bf16, which are all of fp32's
+// 24 bits (two, 16 bits, take 18 % less in the gradients of rank 128, 8 % of rank 64, 1 % in the rest of up to 64, but
+// sums that cancel show the rest); two in fp16, 22 bits: off by 2^-22 of a value at most, as four of the 2^-24 that
+// each addition of the sum before may be off by, of which there are eight at least.  fp16's range is not fp32's: its
+// terms are taken of h times a power of two, of the row (expand) or of all rows so far (gradients of A and B).
 #pragma once
 
 #include "gemm16_tile.hpp"
@@ -29,12 +31,18 @@ __device__ __forceinline__ int row_at(const LoraPlan& p, int position) {
 
 __device__ __forceinline__ i16x8_t load16(const void* p) { return *static_cast<const i16x8_t*>(p); }
 
-// v as two 16-bit terms.
+// v as the sum of its 16-bit terms, the largest first; what each leaves is exact.  set(term, value).
 template <typename T>
-__device__ __forceinline__ void two_terms(float v, T& hi, T& lo) {
-  hi = (T)v;
-  const float rest = v - (float)hi;
-  lo = (T)(__builtin_isfinite(rest) ? rest : 0.0f);   // an infinity stays one
+constexpr int kTerms = __is_same(T, __bf16) ? 3 : 2;
+template <typename T, typename SET>
+__device__ __forceinline__ void split_terms(float v, SET set) {
+#pragma unroll
+  for (int t = 0; t < kTerms<T>; ++t) {
+    const T term = (T)v;
+    set(t, term);
+    v -= (float)term;
+    if (t == 0) v = __builtin_isfinite(v) ? v : 0.0f;   // an infinity stays one
+  }
 }
 
 // The power of two that brings values of at most `top` (the bits of a largest finite magnitude) to 2^13 and above,
@@ -263,8 +271,13 @@ struct Expand {
     else
       return load16(p);
   }
-  // LDS: f's rows, their exponents; W_T: each wave's COLS columns of w, [rank][COLS]
-  static size_t smem_bytes() { return (size_t)TM * STRIDE * 4 + TM * 4 + (W_T ? 4 * (size_t)STAGE : 0); }
+  // f's terms, of which the four waves hold the same fragments; the last one lies in LDS where registers would spill
+  // (rank 64, four row tiles) or a SIMD would hold one wave instead of two (rank 256, 8192 rows, 4096 to 11008: the
+  // forward call 507 us, 591).
+  static constexpr int TERMS = kTerms<T>, HELD = TERMS == 3 && (RT == 4 || (JT == 16 && !W_T)) ? 2 : TERMS;
+  // LDS: f's rows, their exponents; the last term; W_T: each wave's COLS columns of w, [rank][COLS]
+  static constexpr int LAST = TM * STRIDE * 4 + TM * 4, STAGES = LAST + (HELD < TERMS ? RT * KT * 1024 : 0);
+  static size_t smem_bytes() { return STAGES + (W_T ? 4 * (size_t)STAGE : 0); }
 
   // Of kCopied rows those without an adapter; a wave takes a quarter of them, four at a time.
   static __device__ __forceinline__ void copy_rows(const ExpandArgs& s, int first, int span) {
@@ -305,7 +318,7 @@ struct Expand {
     const T* w = static_cast<const T*>(s.w) + (size_t)rt.expert * N * rank;
     const T* base = static_cast<const T*>(s.base);
     T* y = static_cast<T*>(s.y);
-    uint8_t* stage = smem + TM * STRIDE * 4 + TM * 4 + wave * STAGE;
+    uint8_t *stage = smem + STAGES + wave * STAGE, *last = smem + LAST + lane * 16;
     int rows[RT][CP];   // that the lane loads and stores: its own, or (CP 2, in whole lines) l8 and 8 + l8 of a tile
     const int h8 = l16 >> 3, l8 = l16 & 7;
 #pragma unroll
@@ -371,7 +384,7 @@ struct Expand {
       __syncthreads();
     }
     const float scale = s.scales ? s.scales[rt.expert] : 1.0f;
-    i16x8_t fh[RT][KT], fl[RT][KT];
+    i16x8_t ft[HELD][RT][KT];
     float back[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -380,16 +393,20 @@ struct Expand {
       back[i] = power(-e);
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
-        T hi[8], lo[8];
+        T terms[TERMS][8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const int j = k * 32 + 8 * quad + r;
-          two_terms(j < JT * 16 ? f[m * STRIDE + j] * up : 0.0f, hi[r], lo[r]);
+          split_terms<T>(j < JT * 16 ? f[m * STRIDE + j] * up : 0.0f, [&](int t, T v) { terms[t][r] = v; });
         }
-        fh[i][k] = *reinterpret_cast<i16x8_t*>(hi);
-        fl[i][k] = *reinterpret_cast<i16x8_t*>(lo);
+#pragma unroll
+        for (int t = 0; t < HELD; ++t) ft[t][i][k] = *reinterpret_cast<i16x8_t*>(terms[t]);
+        if constexpr (HELD < TERMS)
+          if (i % 4 == wave)
+            *reinterpret_cast<i16x8_t*>(last + (i * KT + k) * 1024) = *reinterpret_cast<i16x8_t*>(terms[HELD]);
       }
     }
+    if constexpr (HELD < TERMS) __syncthreads();
 
     auto multiply = [&](int n0, Step& d) {
       if constexpr (W_T) {
@@ -412,7 +429,12 @@ struct Expand {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         if constexpr (CP == 2) trade_lines(d.base[i][0], d.base[i][1]);
-        i16x8_t out[CP];
+        i16x8_t out[CP], fl[KT];
+        if constexpr (HELD < TERMS) {
+          asm volatile("" ::: "memory");   // (read here each time, not held from before the loop)
+#pragma unroll
+          for (int k = 0; k < KT; ++k) fl[k] = *reinterpret_cast<const i16x8_t*>(last + (i * KT + k) * 1024);
+        }
 #pragma unroll
         for (int c = 0; c < CP; ++c) {
           typedef T T8 __attribute__((ext_vector_type(8)));
@@ -422,10 +444,10 @@ struct Expand {
           for (int j = 0; j < 2; ++j) {
             f32x4_t acc = {};
 #pragma unroll
-            for (int k = 0; k < KT; ++k) {
-              acc = mfma16(d.w[2 * c + j][k], fl[i][k], acc, T{});
-              acc = mfma16(d.w[2 * c + j][k], fh[i][k], acc, T{});
-            }
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int t = TERMS - 1; t >= 0; --t)
+                acc = mfma16(d.w[2 * c + j][k], t < HELD ? ft[t < HELD ? t : 0][i][k] : fl[k], acc, T{});
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[4 * j + r] = (T)fmaf(scale, acc[r] * back[i], (float)b[4 * j + r]);
           }
@@ -450,7 +472,7 @@ struct Expand {
 
 // ---------------------------------------------------------------- the adapters' gradients
 // out[c][j] (or out[j][c], J_FIRST) = s_e sum over the adapter's positions p of z[row(p)][c] f[p][j].
-// A workgroup takes 128 columns of one adapter and a part of its rows, 64 at a time: z's rows and f's two
+// A workgroup takes 128 columns of one adapter and a part of its rows, 64 at a time: z's rows and f's
 // terms go to LDS and both operands are read transposed; the next 64 rows are on their way meanwhile.  Each
 // wave has 32 columns.
 struct LoraGradArgs {
@@ -466,7 +488,9 @@ struct LoraGradArgs {
 template <typename T, int JT, bool J_FIRST>
 struct LoraGrad {
   static constexpr int COLS = 128, FROW = JT * 32;   // bytes a row of f's terms
-  static size_t smem_bytes() { return 64 * COLS * 2 + 2 * 64 * FROW + 64; }
+  static constexpr int TERMS = kTerms<T>;
+  // LDS: z's rows, f's terms one after the other, the waves' largest values
+  static size_t smem_bytes() { return 64 * COLS * 2 + TERMS * 64 * FROW + 64; }
 
   static __device__ __forceinline__ void run(const LoraGradArgs& s, int block, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -478,8 +502,8 @@ struct LoraGrad {
     const int each = ((hi - lo + s.splits - 1) / s.splits + 63) / 64 * 64;
     const int p0 = min(hi, lo + split * each), p1 = min(hi, p0 + each);
     const int rank = s.rank;
-    uint8_t *zt = smem, *fh = smem + 64 * COLS * 2, *fl = fh + 64 * FROW;
-    uint32_t* tops = reinterpret_cast<uint32_t*>(fl + 64 * FROW);
+    uint8_t *zt = smem, *ft = smem + 64 * COLS * 2;
+    uint32_t* tops = reinterpret_cast<uint32_t*>(ft + TERMS * 64 * FROW);
     auto turn = [](int row) { return 2 * ((row & 3) + 4 * ((row >> 3) & 1)); };   // of a row's 16 pieces
 
     i16x8_t zv[4];
@@ -544,11 +568,12 @@ struct LoraGrad {
 #pragma unroll
       for (int i = 0; i < JT; ++i) {
         const int at = (i * 256 + tid) / (JT * 4), j = ((i * 256 + tid) % (JT * 4)) * 4;
-        T h4[4], l4[4];
+        T terms[TERMS][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) two_terms(fv[i][r] * up, h4[r], l4[r]);
-        *reinterpret_cast<i16x4_t*>(fh + at * FROW + j * 2) = *reinterpret_cast<i16x4_t*>(h4);
-        *reinterpret_cast<i16x4_t*>(fl + at * FROW + j * 2) = *reinterpret_cast<i16x4_t*>(l4);
+        for (int r = 0; r < 4; ++r) split_terms<T>(fv[i][r] * up, [&](int t, T v) { terms[t][r] = v; });
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+          *reinterpret_cast<i16x4_t*>(ft + (t * 64 + at) * FROW + j * 2) = *reinterpret_cast<i16x4_t*>(terms[t]);
       }
       if (p + 64 < p1) load(p + 64);
       __syncthreads();
@@ -567,17 +592,14 @@ struct LoraGrad {
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           const int at = row * FROW + j * 32 + (l16 & 3) * 8;
-          const i16x8_t a = two(fl + at, FROW), b = two(fh + at, FROW);
+          i16x8_t ff[TERMS];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if constexpr (J_FIRST) {
-              acc[c][j] = mfma16(zf[c], a, acc[c][j], T{});
-              acc[c][j] = mfma16(zf[c], b, acc[c][j], T{});
-            } else {
-              acc[c][j] = mfma16(a, zf[c], acc[c][j], T{});
-              acc[c][j] = mfma16(b, zf[c], acc[c][j], T{});
-            }
-          }
+          for (int t = 0; t < TERMS; ++t) ff[t] = two(ft + t * 64 * FROW + at, FROW);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t)
+              acc[c][j] = J_FIRST ? mfma16(zf[c], ff[t], acc[c][j], T{}) : mfma16(ff[t], zf[c], acc[c][j], T{});
         }
       }
       __syncthreads();
