@@ -136,11 +136,11 @@ unsigned gemm16_blocks(const Gemm16Args& g, int shape, int cus) {
   return (unsigned)(((units < room ? units : room) + 7) / 8 * 8);
 }
 
-// The launch's grid and LDS, whose limit is raised for `kernel` (KERNEL's, or one that KERNEL stands for).
-template <typename KERNEL>
-hipError_t gemm16_grid(const Gemm16Args& g, const void* kernel, int shape, unsigned* grid, int* bytes) {
+// The launch's grid and LDS, whose limit is raised for FUNCTION (KERNEL's kernel, or one that KERNEL stands for).
+template <typename KERNEL, auto FUNCTION>
+hipError_t gemm16_grid(const Gemm16Args& g, int shape, unsigned* grid, int* bytes) {
   *bytes = (int)KERNEL::smem_bytes(g.E);
-  hipError_t e = allow_lds<KERNEL>(kernel, kLds);
+  hipError_t e = allow_lds<FUNCTION>(kLds);
   int cus = 0;
   if (e == hipSuccess) e = compute_units(&cus);
   if (e != hipSuccess) return e;
@@ -152,7 +152,7 @@ template <typename KERNEL>
 hipError_t run_gemm16(const Gemm16Args& g, int shape, hipStream_t stream) {
   unsigned grid = 0;
   int bytes = 0;
-  hipError_t e = gemm16_grid<KERNEL>(g, reinterpret_cast<const void*>(&k_gemm16<KERNEL>), shape, &grid, &bytes);
+  hipError_t e = gemm16_grid<KERNEL, &k_gemm16<KERNEL>>(g, shape, &grid, &bytes);
   if (e != hipSuccess) return e;
   if (g.queue) {
     hipLaunchKernelGGL(k_gemm16_queue, dim3(1), dim3(8), 0, stream, g.queue, (int)grid / 8);

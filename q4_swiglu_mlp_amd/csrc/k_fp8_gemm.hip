@@ -39,7 +39,7 @@ hipError_t run_tiles(GemmArgs g, int TM, int splits, hipStream_t stream) {
   g.col_tiles = (g.N + KERNEL::COLS - 1) / KERNEL::COLS;
   g.splits = splits;
   const int bytes = (int)KERNEL::smem_bytes(g.offsets ? g.E : 0);
-  hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_tile<KERNEL>), kLds);
+  hipError_t e = allow_lds<&k_fp8_tile<KERNEL>>(kLds);
   int cus = 0;
   if (e == hipSuccess) e = compute_units(&cus);
   if (e != hipSuccess) return e;
@@ -67,7 +67,7 @@ hipError_t run_stream(StreamArgs s, int cols, hipStream_t stream) {
   const size_t bytes = KERNEL::smem_bytes(s.rows, s.chunk);
   g.row_tiles = (int)max_row_tiles(g.M, g.offsets ? g.E : 0, KERNEL::TM);
   g.col_tiles = (g.N + cols - 1) / cols;
-  const hipError_t e = allow_lds<KERNEL>(reinterpret_cast<const void*>(&k_fp8_stream<KERNEL>), kLds);
+  const hipError_t e = allow_lds<&k_fp8_stream<KERNEL>>(kLds);
   if (e != hipSuccess) return e;
   timing_begin(stream);
   hipLaunchKernelGGL(k_fp8_stream<KERNEL>, dim3((unsigned)((long long)g.row_tiles * g.col_tiles)),

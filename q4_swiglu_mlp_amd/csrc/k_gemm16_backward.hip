@@ -40,9 +40,8 @@ template <typename T, typename OA, typename OW>
 hipError_t run_beside(const Gemm16Args& a, const Gemm16Args& w, hipStream_t stream) {
   using INPUT = Gemm16<kInput, 64, 128, 1, 4, 2, T, OA>;
   using WEIGHT = Gemm16<kWeight, 64, 128, 1, 4, 2, T, OW>;
-  const void* kernel = reinterpret_cast<const void*>(&k_gemm16_beside<INPUT, WEIGHT>);
   int cus = 0;
-  hipError_t e = allow_lds<Both<INPUT, WEIGHT>>(kernel, kLds);
+  hipError_t e = allow_lds<&k_gemm16_beside<INPUT, WEIGHT>>(kLds);
   if (e == hipSuccess) e = compute_units(&cus);
   if (e != hipSuccess) return e;
   const unsigned first = gemm16_blocks<INPUT>(a, 3, cus), behind = gemm16_blocks<WEIGHT>(w, 3, cus);
@@ -69,10 +68,9 @@ template <typename T, typename OA, typename OW>
 hipError_t run_both(const Gemm16Args& a, const Gemm16Args& w, hipStream_t stream) {
   using INPUT = Gemm16<kInput, 256, 256, 2, 4, 2, T, OA>;
   using WEIGHT = Gemm16<kWeight, 256, 256, 2, 4, 2, T, OW>;
-  const void* kernel = reinterpret_cast<const void*>(&k_gemm16_both<INPUT, WEIGHT>);
   unsigned grid = 0;
   int bytes = 0;
-  hipError_t e = gemm16_grid<Both<INPUT, WEIGHT>>(a, kernel, 0, &grid, &bytes);
+  hipError_t e = gemm16_grid<Both<INPUT, WEIGHT>, &k_gemm16_both<INPUT, WEIGHT>>(a, 0, &grid, &bytes);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_gemm16_queue, dim3(1), dim3(16), 0, stream, a.queue, (int)grid / 8);   // both: w's follows
   e = hipGetLastError();

@@ -83,8 +83,8 @@ hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, co
     using DB = LoraGrad<T, JT, false>;
     const size_t first = H::smem_bytes() > DH::smem_bytes() ? H::smem_bytes() : DH::smem_bytes();
     const size_t second = DX::smem_bytes() > DA::smem_bytes() ? DX::smem_bytes() : DA::smem_bytes();
-    hipError_t e = allow_lds<H>(reinterpret_cast<const void*>(&k_lora_firsts<H, DH>), kLds);
-    if (e == hipSuccess) e = allow_lds<DX>(reinterpret_cast<const void*>(&k_lora_seconds<DX, DA, DB>), kLds);
+    hipError_t e = allow_lds<&k_lora_firsts<H, DH>>(kLds);
+    if (e == hipSuccess) e = allow_lds<&k_lora_seconds<DX, DA, DB>>(kLds);
     if (e != hipSuccess) return e;
     const long long h_blocks = M && db ? shrink_blocks(false, h) : 0;
     const long long dh_blocks = M && (dx || da) ? shrink_blocks(false, dh) : 0;

@@ -29,8 +29,8 @@ hipError_t launch_lora(const void* x, const void* a, const void* b, const float*
     constexpr int JT = decltype(jt)::value, R = decltype(r)::value;
     using SHRINK = Shrink<decltype(t), JT, lora_forward_tiles(JT, R), false>;
     using EXPAND = Expand<decltype(t), JT, lora_forward_tiles(JT, R), false>;
-    hipError_t e = allow_lds<SHRINK>(reinterpret_cast<const void*>(&k_lora_shrink<SHRINK>), kLds);
-    if (e == hipSuccess) e = allow_lds<EXPAND>(reinterpret_cast<const void*>(&k_lora_expand<EXPAND>), kLds);
+    hipError_t e = allow_lds<&k_lora_shrink<SHRINK>>(kLds);
+    if (e == hipSuccess) e = allow_lds<&k_lora_expand<EXPAND>>(kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_lora_shrink<SHRINK>, dim3((unsigned)shrink_blocks(true, s)), dim3(256), SHRINK::smem_bytes(),
                        stream, s);

@@ -126,16 +126,16 @@ __device__ __forceinline__ void tile_rows(const ARGS& g, const int32_t* starts, 
   r.rows = __builtin_amdgcn_readfirstlane(min(TM, max(lo, starts[r.expert + 1]) - r.first));
 }
 
-// Raises the kernel's LDS limit, once a device.
-template <typename KERNEL>
-hipError_t allow_lds(const void* kernel, int bytes) {
+// Raises the kernel's LDS limit, once a device.  The kernel itself is the argument, so that no two share a flag.
+template <auto KERNEL>
+hipError_t allow_lds(int bytes) {
   static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (ready.load(std::memory_order_relaxed) & bit) return hipSuccess;
-  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == hipSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
