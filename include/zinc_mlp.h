@@ -496,8 +496,8 @@ int zinc_swiglu_backward(const void* dh, const void* gate, const void* up, int32
  * _backward, from dy [M x N], with dh[m] = B_e^T dy[m]:
  *   dx[m] = base[m] + scales[e] A_e^T dh[m]           base: the projection's own gradient of x
  *   da_e = scales[e] sum_m dh[m] x[m]^T,   db_e = scales[e] sum_m dy[m] (A_e x[m])^T     over the rows of e
- * (zeros for an adapter without rows, also where M is 0).  The gradient of base is dy itself.  dx, da or db
- * may be NULL: it is then not computed.
+ * (zeros for an adapter without rows, whatever its scale, also where M is 0).  The gradient of base is dy itself.
+ * dx, da or db may be NULL: it is then not computed.
  * A x and dh are kept in fp32; where they are operands again they are split in 16-bit terms (three in bf16, which
  * are the value itself, two in fp16, 22 bits of it), sums are fp32 and results are rounded once.  Nothing depends on
  * the order of the GPU's work: equal inputs give equal bits.

@@ -38,12 +38,15 @@ struct JoinArgs {
 };
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_lora_join(JoinArgs a, JoinArgs b, const float* __restrict__ scales) {
+__global__ __launch_bounds__(256) void k_lora_join(JoinArgs a, JoinArgs b, LoraPlan plan,
+                                                    const float* __restrict__ scales) {
   const JoinArgs& g = blockIdx.y ? b : a;
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < g.n; i += (size_t)gridDim.x * 1024) {
     f32x4_t v = *reinterpret_cast<const f32x4_t*>(g.parts + i);
     for (int s = 1; s < g.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(g.parts + s * g.n + i);
-    const float scale = scales ? scales[i / g.each] : 1.0f;
+    int lo, hi;
+    positions_of(plan, (int)(i / g.each), lo, hi);
+    const float scale = grad_scale(scales, (int)(i / g.each), hi > lo);
     typedef T T4 __attribute__((ext_vector_type(4)));
     T4 o;
 #pragma unroll
@@ -107,9 +110,9 @@ hipError_t launch_lora_backward(const void* dy, const void* x, const void* a, co
   if (e != hipSuccess || most == 0) return e;
   const dim3 grid((unsigned)((most + 1023) / 1024 < 1024 ? (most + 1023) / 1024 : 1024), 2);
   if (type == 0)
-    hipLaunchKernelGGL(k_lora_join<_Float16>, grid, dim3(256), 0, stream, ja, jb, scales);
+    hipLaunchKernelGGL(k_lora_join<_Float16>, grid, dim3(256), 0, stream, ja, jb, plan, scales);
   else
-    hipLaunchKernelGGL(k_lora_join<__bf16>, grid, dim3(256), 0, stream, ja, jb, scales);
+    hipLaunchKernelGGL(k_lora_join<__bf16>, grid, dim3(256), 0, stream, ja, jb, plan, scales);
   return hipGetLastError();
 }
 

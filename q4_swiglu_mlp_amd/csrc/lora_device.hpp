@@ -29,6 +29,18 @@ __device__ __forceinline__ int row_at(const LoraPlan& p, int position) {
   return row >= 0 && row < p.M ? row : -1;
 }
 
+// The positions of adapter e: lo up to hi.
+__device__ __forceinline__ void positions_of(const LoraPlan& p, int e, int& lo, int& hi) {
+  lo = min(max(p.offsets[e], 0), p.M);
+  hi = min(max(p.offsets[e + 1], lo), p.M);
+}
+
+// What a gradient of adapter e is multiplied by.  One without rows is zeros, whatever its scale: that of a slot that
+// nobody uses may never have been written.
+__device__ __forceinline__ float grad_scale(const float* scales, int e, bool has_rows) {
+  return scales && has_rows ? scales[e] : 1.0f;
+}
+
 __device__ __forceinline__ i16x8_t load16(const void* p) { return *static_cast<const i16x8_t*>(p); }
 
 // v as the sum of its 16-bit terms, the largest first; what each leaves is exact.  set(term, value).
@@ -498,7 +510,8 @@ struct LoraGrad {
     const int col_tiles = (s.C + COLS - 1) / COLS;
     const int e = block / (col_tiles * s.splits), in = block - e * col_tiles * s.splits;
     const int split = in / col_tiles, c0 = (in - split * col_tiles) * COLS;
-    const int lo = min(max(s.plan.offsets[e], 0), s.plan.M), hi = min(max(s.plan.offsets[e + 1], lo), s.plan.M);
+    int lo, hi;
+    positions_of(s.plan, e, lo, hi);
     const int each = ((hi - lo + s.splits - 1) / s.splits + 63) / 64 * 64;
     const int p0 = min(hi, lo + split * each), p1 = min(hi, p0 + each);
     const int rank = s.rank;
@@ -605,7 +618,7 @@ struct LoraGrad {
       __syncthreads();
     }
     const float back = power(-lifted);
-    const float scale = s.scales ? s.scales[e] : 1.0f;
+    const float scale = grad_scale(s.scales, e, hi > lo);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll

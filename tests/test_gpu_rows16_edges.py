@@ -85,3 +85,25 @@ def test_adapters_keep_every_bit_of_fp32(kind, M, E, rank, K, N):
     want = R.lora_backward(dy, x, a, b, np.ones(E), cpu_plan, np.zeros((M, K)))
     assert torch.equal(dx, to(want[0])) and torch.equal(da, to(want[1]))
     assert M == 1 or (y.any() and db.any() and dx.any() and da.any())
+
+
+# ---------------------------------------------------------------- adapters without rows
+# one part, several parts of the rows, and M = 0
+@pytest.mark.parametrize("kind", HALF)
+@pytest.mark.parametrize("M,E,K,N", [(50, 4, 264, 136), (3000, 3, 264, 136), (0, 2, 16, 24)])
+def test_a_scale_without_rows_is_not_used(kind, M, E, K, N):
+    """Slots of a pool that no row uses, with scales nobody has written: their gradients are zeros."""
+    rng = np.random.default_rng(M)
+    rank = 16
+    ids = (np.arange(M) % (E - 1)).astype(np.int32) + 1          # nobody has adapter 0
+    x, dy = normal(rng, M, K, kind=kind), normal(rng, M, N, kind=kind)
+    a, b = normal(rng, E, rank, K, kind=kind), normal(rng, E, N, rank, kind=kind)
+    plan, ones = plan_of(ids, E), torch.ones(E, device=DEV)
+    clean = Z.zinc_lora(x, a, b, ones, *plan), *Z.zinc_lora_backward(dy, x, a, b, ones, *plan)
+    for bad in (float("nan"), float("inf")):
+        scales = ones.clone()
+        scales[0 if M else slice(None)] = bad
+        got = Z.zinc_lora(x, a, b, scales, *plan), *Z.zinc_lora_backward(dy, x, a, b, scales, *plan)
+        for g, c in zip(got, clean):
+            assert torch.equal(g, c)
+        assert not got[2][0].any() and not got[3][0].any()
