@@ -37,8 +37,12 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(const T* __restrict__ d
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const Sigmoid s = sigmoid(g[r]);
-      const float slope = s.value * fmaf(g[r], s.rest, 1.0f);
-      dg[r] = (d[r] * s.factor * slope) * (u[r] * s.factor);
+      // dh, up and s^2 may each leave what fp32 holds of the others' product: their exponents are added apart.  (0 g
+      // is NaN for an infinite gate, as s g is.)
+      const float slope = fmaf(g[r], 0.0f, s.value * fmaf(g[r], s.rest, 1.0f));
+      const int exponent = __builtin_amdgcn_frexp_expf(d[r]) + __builtin_amdgcn_frexp_expf(u[r]) - 2 * s.half;
+      dg[r] = __builtin_amdgcn_ldexpf(
+          __builtin_amdgcn_frexp_mantf(d[r]) * __builtin_amdgcn_frexp_mantf(u[r]) * slope, exponent);
       du[r] = (d[r] * s.factor) * (g[r] * s.value) * s.factor;
     }
     store8<STREAMED>(dgate + i, dg);

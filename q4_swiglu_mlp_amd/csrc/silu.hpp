@@ -26,12 +26,14 @@ __device__ __forceinline__ float silu_times(float z, float u) {
   return u * f * f * s;
 }
 
-// s = 1 / (1 + e^-z) as value factor^2, and 1 - s, by the same steps.  The factor is a power of two, 1 down to
-// z = -28, and value stays above 2^-42, so that the products behind it lose nothing before the result does.  1 - s
+// s = 1 / (1 + e^-z) as value factor^2, and 1 - s, by the same steps.  The factor is 2^-half, 1 down to
+// z = -28, and value stays above 2^-42, so that z value u factor^2, one factor after u, loses nothing before the result
+// does: u factor is the larger.  (Below 2^-149 the factor is zero, and so is the result.)  1 - s
 // is e^-z s, which has no cancellation (z is cut where e^-z is zero, and not before: a large z times 1 - s has to
 // vanish).
 struct Sigmoid {
   float value, factor, rest;
+  int half;
 };
 __device__ __forceinline__ Sigmoid sigmoid(float z) {
   constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
@@ -42,7 +44,7 @@ __device__ __forceinline__ Sigmoid sigmoid(float z) {
   const float e2 = __builtin_amdgcn_exp2f(fmaf(half, -2.0f, t));
   const float e = fmaf(e2, r * kLn2, e2);
   const float value = __builtin_amdgcn_rcpf(1.0f + e);
-  return {value, __builtin_amdgcn_ldexpf(1.0f, -(int)half), e * value};
+  return {value, __builtin_amdgcn_ldexpf(1.0f, -(int)half), e * value, (int)half};
 }
 
 }  // namespace zinc

@@ -107,3 +107,38 @@ def test_a_scale_without_rows_is_not_used(kind, M, E, K, N):
         for g, c in zip(got, clean):
             assert torch.equal(g, c)
         assert not got[2][0].any() and not got[3][0].any()
+
+
+# ---------------------------------------------------------------- SwiGLU's gradients, factors at both ends of the range
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d,u", [(-70, 60), (-99, 119), (-126, 127), (60, -70), (127, -126), (127, 127), (0, 0), (90, 100)])
+def test_swiglu_gradients_of_factors_at_both_ends(kind, d, u):
+    """dh and up so far apart that a product of some of the factors leaves fp32's range where dgate does not."""
+    rng = np.random.default_rng(5)
+    g = np.concatenate([np.linspace(-340, -20, 1000), np.linspace(-20, 90, 536)]).reshape(12, 128)
+    sign = rng.choice([-1.0, 1.0], (2, 12, 128)) * rng.uniform(1, 2 - 2.0 ** -6, (2, 12, 128))
+    g, dh, up = (dev(v.astype(np.float32)).to(TYPES[kind][0]) for v in (g, np.ldexp(sign[0], d), np.ldexp(sign[1], u)))
+    gh, uh, dhh = host(g), host(up), host(dh)
+    want_g, want_u = R.swiglu_backward(dhh, gh, uh)
+    size = np.abs(dhh) * np.abs(uh) * R.sigmoid(gh) * (1 + np.abs(gh) * R.sigmoid(-gh))
+    dg, du = Z.zinc_swiglu_backward(dh, g, up)
+    # where a result is past the type's largest value it is infinite, and not compared; below fp32's smallest normal
+    # value there are fewer bits: half the smallest step for each of two roundings there
+    most = float(torch.finfo(TYPES[kind][0]).max) * (1 - 2.0 ** -7)
+    for got, want, slack in ((dg, want_g, GLU_GATE * size), (du, want_u, GLU * np.abs(want_u))):
+        fits = np.abs(want) + slack < most
+        assert fits.any() and not np.isnan(host(got)).any()
+        over = np.abs(want) - slack > most * (1 + 2.0 ** -6)
+        assert np.isinf(host(got)[over]).all()
+        close(got.cpu()[torch.from_numpy(fits)], want[fits], slack[fits] + 2.0 ** -149, kind)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_swiglu_gradients_of_infinite_gates(kind):
+    """NaN where the formula has 0 times infinity: dgate of both, dup of minus infinity."""
+    inf = float("inf")
+    g = torch.tensor([[inf, -inf, 0, 1] * 2], device=DEV).to(TYPES[kind][0])
+    one = torch.ones_like(g)
+    dg, du = Z.zinc_swiglu_backward(one, g, one)
+    assert dg.isnan().tolist() == [[True, True, False, False] * 2]
+    assert du.isnan().tolist() == [[False, True, False, False] * 2] and du[0, 0] == inf
