@@ -696,7 +696,7 @@ class _Call:
         return ws.data_ptr(), _nbytes(ws), ws
 
     def run(self, name: str, *args) -> None:
-        if _torch()._C._cuda_getDevice() == self.index:
+        if _torch().cuda.current_device() == self.index:
             status = getattr(lib, name)(*args, self.raw)
         else:
             with _torch().cuda.device(self.index):

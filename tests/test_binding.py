@@ -132,3 +132,34 @@ def test_dequant_and_router_checks():
     with pytest.raises(ValueError, match="expert_ids must be"):
         Z.zinc_moe_route_topk(torch.zeros((4, 8), dtype=torch.float32), 2,
                               expert_ids=torch.zeros((4, 2), dtype=torch.int64))
+
+
+@pytest.mark.parametrize("current,switched", [(1, []), (0, [1])])
+def test_a_call_runs_on_its_tensors_device(monkeypatch, current, switched):
+    """By torch's public functions: the current device is kept, another one's call switches to it and back."""
+    seen = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(self.index)
+
+        def __exit__(self, *_):
+            seen.append("back")
+
+    class Lib:
+        @staticmethod
+        def zinc_swiglu(*args):
+            assert seen == switched
+            seen.append(args)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(Z, "lib", Lib)
+    call = Z._Call.__new__(Z._Call)
+    call.index, call.raw = 1, 7
+    call.run("zinc_swiglu", 2, 3)
+    assert seen == switched + [(2, 3, 7)] + ["back"] * len(switched)
