@@ -15,11 +15,10 @@
 #pragma once
 
 #include "fp8_device.hpp"
+#include "gemm16_plan.hpp"
 #include "tiles.hpp"
 
 namespace zinc {
-
-enum Product { kForward, kInput, kWeight };
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef short i16x8_t __attribute__((ext_vector_type(8)));

@@ -3,8 +3,7 @@
 // rows first, so the last round of the one is work for the same CUs (32768 rows of 64 experts, 768 x 2048, dw in
 // fp32, operands from HBM: 290 us, in two launches 303; 6 % more where every second workgroup begins with dw).
 // Where both are a few units, or bound by memory, the smallest tile's workgroups for da and for dw lie side by side (47
-// rows of 16 experts, 1752 x 696: 28 us, one after the other 43; 1111 of 7, 520 x 1032, fp16: 13 and 22): by the
-// model's times, as if four fifths of the shorter were added to the longer (over 200 drawn sizes 6 % less on average).
+// rows of 16 experts, 1752 x 696: 28 us, one after the other 43; 1111 of 7, 520 x 1032, fp16: 13 and 22).
 #include "gemm16_launch.hpp"
 
 namespace zinc {
@@ -50,18 +49,6 @@ hipError_t run_beside(const Gemm16Args& a, const Gemm16Args& w, hipStream_t stre
                      INPUT::smem_bytes(a.E), stream, a, w, (int)first);
   timing_end(stream);
   return hipGetLastError();
-}
-
-struct BackwardPlan {
-  Gemm16Plan input, weight;
-  bool together, beside;
-};
-BackwardPlan plan_backward(int M, int E, int N, int K) {
-  BackwardPlan p{plan_gemm16(kInput, M, E, N, K), plan_gemm16(kWeight, M, E, N, K), false, false};
-  p.together = p.input.queue && p.weight.queue && p.input.shape == 0 && p.weight.shape == 0;
-  const double a = plan_gemm16(kInput, M, E, N, K, true).us, w = plan_gemm16(kWeight, M, E, N, K, true).us;
-  p.beside = !p.together && (a > w ? a + 0.8 * w : w + 0.8 * a) < p.input.us + p.weight.us;
-  return p;
 }
 
 template <typename T, typename OA, typename OW>
