@@ -13,7 +13,6 @@ namespace {
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxRows = 1 << 24;
 constexpr int kMaxCols = 65536;
-constexpr int kMaxRank = 256;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool cols_ok(int32_t c) { return c > 0 && c % 8 == 0 && c <= kMaxCols; }
@@ -39,7 +38,7 @@ bool gemm_ok(int32_t rows, int32_t E, int32_t N, int32_t K) {
   return rows_ok(rows) && groups_ok(E) && cols_ok(N) && cols_ok(K);
 }
 bool lora_shape_ok(int32_t K, int32_t N, int32_t rank) {
-  return cols_ok(K) && cols_ok(N) && rank > 0 && rank % 8 == 0 && rank <= kMaxRank;
+  return cols_ok(K) && cols_ok(N) && rank > 0 && rank % 8 == 0 && rank <= zinc::kLoraMaxRank;
 }
 
 }  // namespace

@@ -119,6 +119,7 @@ hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* 
                                   void* dup, hipStream_t stream);
 
 // Low-rank adapters beside a projection (k_lora_*.hip).  base may be null or y (dx); dx, da, db may be null.
+constexpr int kLoraMaxRank = 256;   // what the kernels' most tiles of 16 hold
 size_t lora_workspace_bytes(int M, int rank);
 hipError_t launch_lora(const void* x, const void* a, const void* b, const float* scales, const int32_t* offsets,
                        const int32_t* slot_row, const int32_t* row_slot, int E, int M, int K, int N, int rank, int type,

@@ -16,8 +16,6 @@
 
 namespace zinc {
 
-constexpr int kMaxRank = 256;
-
 struct LoraPlan {
   const int32_t *offsets, *slot_row, *row_slot;
   int E, M;

@@ -98,7 +98,9 @@ hipError_t by_rank(int rank, bool few, F f) {
   if (rank <= 32) return by_rows<T, 2>(few, f);
   if (rank <= 64) return by_rows<T, 4>(few, f);
   if (rank <= 128) return by_rows<T, 8>(few, f);
-  return by_rows<T, 16>(few, f);
+  constexpr int kMost = 16;
+  static_assert(kLoraMaxRank == 16 * kMost, "the largest rank fills the most tiles");
+  return by_rows<T, kMost>(few, f);
 }
 template <typename F>
 hipError_t by_kind(int type, int M, int E, int rank, F f) {
