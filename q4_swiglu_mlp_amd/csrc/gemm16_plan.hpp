@@ -51,9 +51,10 @@ inline size_t gemm16_part_bytes(Product f, int M, int E, int N, int K) {
 // The cut with the least time by a model fitted to 4388 timings: 90 products of 1 - 256 experts of uneven sizes, 1 -
 // 30000 rows, each with its gradients, in every tile, in 1 - 16 parts, dealt out or not.  It is off by 17 % on average;
 // what it picks takes 4 % more than the best on average (c 3.5 %, da 2 %, dw 5 %), 48 % in the worst of 360.
-// Examples, us, in the order of the tiles, in one part: 32768 rows of 64 x 768 x 2048 124, 132, 150 and 171, dw in
-// fp32 178, 191, 203 and 250; 2331 of 7 x 520 x 1032 31, 21, 19 and 13; 64 of 64 x 768 x 2048 49, 34, 38 and 32,
-// and 27 in two parts of the last.  For 256 CUs.
+// Examples (bf16, the kernel's us by trace, operands from HBM), in the order of the tiles, in one part, dealt out in
+// turn: 32768 rows of 64 x 768 x 2048 c 126, 137, 158 and 178, da 137, 151, 168 and 202, dw in fp32 205, 229, 232 and
+// 302, and 170 from queues in the largest; 2331 of 7 x 520 x 1032 (fp16, from the caches) 32, 20, 15 and 13; 64 of 64 x
+// 768 x 2048 45, 32, 36 and 26, and 22 + 4 in two parts of the last.  For 256 CUs.
 // small: the smallest tile, in one part, dealt out in turn.
 inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small = false) {
   constexpr int kCus = 256;
@@ -124,7 +125,9 @@ inline Gemm16Plan plan_gemm16(Product f, int M, int E, int N, int K, bool small 
 
 // Both gradients in one launch: one after the other where both are dealt out in the largest tile, or side by side in the
 // smallest, by the model's times as if four fifths of the shorter were added to the longer (over 200 drawn sizes 6 %
-// less on average).
+// less on average).  A call, us, so and in two launches: 1111 rows of 7 x 520 x 1032, fp16 15 and 24; 500 of 64 x 256 x
+// 512 20 and 23; 8 of 256 x 312 x 4152 142 and 153; 64 of 64 x 768 x 2048 119 and 108 (it takes two).  The model
+// misses 47 of 16 x 1752 x 696: 41 in two, which it takes, and 27 side by side.
 struct BackwardPlan {
   Gemm16Plan input, weight;
   bool together, beside;

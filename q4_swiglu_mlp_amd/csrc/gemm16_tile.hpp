@@ -83,9 +83,9 @@ struct Gemm16 {
   // dw 2 %, da gains 1 % with two or three.
   static constexpr bool EAGER = NT == 2;
   static constexpr int BAND = 8;   // row tiles walked per column
-  // Large tiles' outputs are stored past the caches, in whole lines: 32768 rows of 64 experts, 768 x 2048, dw in fp32
-  // 143 us, in lines that the caches hold 180, in half lines 166 and 183 (half as much again is written); da
-  // 118 and 131.
+  // Large tiles' outputs are stored past the caches, in whole lines (in half lines memory writes half as much
+  // again): 32768 rows of 64 experts, 768 x 2048, from queues, by trace, on the same operands again and again dw in fp32
+  // 146 us, in lines that the caches hold 186, da 122 and 128; on operands from HBM dw 174 and 181, da 140 and 141.
   static constexpr bool STREAMED = NT == 4;
   // workgroups a CU holds by registers
   static constexpr int HELD = (MT * NT * 4 <= 32 ? 12 : 8) / WAVES;
@@ -180,7 +180,7 @@ struct Gemm16 {
   }
 
   // Zeros in dw, or in its parts, for the experts without rows, order[reached] and on, 64 KB a workgroup in turn
-  // (5.3 TB/s; 8 rows of 256 experts, 312 x 4152, both gradients 151 us, by products of no steps 312).
+  // (5.3 TB/s; 8 rows of 256 experts, 312 x 4152, both gradients 142 us, by products of no steps 312).
   static __device__ __forceinline__ void clear_absent(const Gemm16Args& g, const int32_t* order, int reached, int block,
                                                       int blocks) {
     constexpr int kChunk = 4096;   // of 16 bytes
@@ -398,8 +398,8 @@ struct Gemm16 {
       if (unit < 0) return;
       const Unit cu = unit_at(g, starts, ends, row_tiles, col_tiles, unit);
       // A wave whose rows all lie behind the tile's last only copies and keeps step; its SIMD's other wave has the
-      // matrix unit to itself (8192 rows of 8 x 11008 x 4096 680 us, without 687; the gradients of 32768 of 64 x 768 x
-      // 2048 292 and 297).
+      // matrix unit to itself (8192 rows of 8 uneven experts x 11008 x 4096, by trace, 709 us, without 734; the gradients
+      // of 32768 of 64 x 768 x 2048 299 and 304).
       const bool idle = WM > 1 && (F == kWeight ? g.N - cu.p0 : cu.rows) <= wm * (TM / WM);
       if (idle) {
         for (int k = 0; k < cu.steps; ++k, buf = after(buf)) {

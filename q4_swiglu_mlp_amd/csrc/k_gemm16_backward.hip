@@ -1,9 +1,10 @@
 // Both gradients of a 16-bit product by expert, in one launch where that is less.  Where both are many units of the
 // largest tile, a workgroup that finds no more units of da goes on with those of dw, the experts with most
 // rows first, so the last round of the one is work for the same CUs (32768 rows of 64 experts, 768 x 2048, dw in
-// fp32, operands from HBM: 290 us, in two launches 303; 6 % more where every second workgroup begins with dw).
-// Where both are a few units, or bound by memory, the smallest tile's workgroups for da and for dw lie side by side (47
-// rows of 16 experts, 1752 x 696: 28 us, one after the other 43; 1111 of 7, 520 x 1032, fp16: 13 and 22).
+// fp32, operands from HBM: a call 300 us, in two launches 311, of which the kernels are 140 - 143 and 174 - 180; where
+// every second workgroup began with dw 6 % more).
+// Where both are a few units, or bound by memory, the smallest tile's workgroups for da and for dw lie side by side
+// (plan_backward).
 #include "gemm16_launch.hpp"
 
 namespace zinc {

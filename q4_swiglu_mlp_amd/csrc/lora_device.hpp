@@ -6,7 +6,7 @@
 //
 // h and dh are kept in fp32 as parts of their sums ([splits][rows][rank], added in order where they are
 // read).  As operands of the second products they are sums of 16-bit terms: three in bf16, which are all of fp32's
-// 24 bits (two, 16 bits, take 18 % less in the gradients of rank 128, 8 % of rank 64, 1 % in the rest of up to 64, but
+// 24 bits (two, 16 bits, take 14 % less in the gradients of rank 128, 8 % of rank 64, 1 % in the rest of up to 64, but
 // sums that cancel show the rest); two in fp16, 22 bits: off by 2^-22 of a value at most, as four of the 2^-24 that
 // each addition of the sum before may be off by, of which there are eight at least.  fp16's range is not fp32's: its
 // terms are taken of h times a power of two, of the row (expand) or of all rows so far (gradients of A and B).
@@ -79,8 +79,8 @@ __device__ __forceinline__ void trade_lines(i16x8_t& first, i16x8_t& second) {
 }
 
 // F pieces of f a thread: the sums of their parts in order; load(part, piece).  The first part and up to four more of
-// every piece are in flight at a time (1626 rows of 16 adapters of rank 128, gradients: the second launch 34 us, piece
-// by piece 50).
+// every piece are in flight at a time (1626 rows of 16 adapters of rank 128, 2048 to 2048, gradients: the second
+// launch 38 us, piece by piece 45).
 template <int F, typename LOAD>
 __device__ __forceinline__ void sum_parts(f32x4_t (&v)[F], int splits, LOAD load) {
   constexpr int G = F <= 2 ? 4 : F <= 4 ? 2 : 1;
@@ -272,8 +272,8 @@ struct Expand {
   static constexpr int COLS = 32 * CP;   // columns of a wave's step
   static constexpr int STRIDE = JT * 16 + 4;   // floats a row of f, in LDS
   static constexpr int STAGE = KT * 32 * COLS * 2;   // bytes
-  // Many rows of base and y pass the caches by, where they move in whole lines: 8192 x 11008, rank 64 92 us
-  // through the caches, 88 with y past them, 84 with both; rank 16 76, 71 and 67.
+  // Many rows of base and y pass the caches by, where they move in whole lines: 8192 x 11008, bf16, rank 64
+  // 93 us through the caches, 93 with y past them, 90 with both; rank 16 82, 77 and 71.
   static constexpr bool STREAMED = CP == 2 && RT > 1;
   static __device__ __forceinline__ i16x8_t load_base(const T* p) {
     if constexpr (STREAMED)

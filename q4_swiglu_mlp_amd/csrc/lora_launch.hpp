@@ -9,11 +9,10 @@ namespace zinc {
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Row tiles of 16 a workgroup takes: one where adapters have few rows, else as many as the registers hold
-// with two workgroups a CU.  8192 rows, eight adapters, 4096 to 11008, us: the second product through the
-// caches of rank 16 74 with two, 80 with four, 75 with one; of rank 32 78 and 81; of rank 64 104 with two, 91 with
-// four, but 101 and 115 where its matrix is turned (dx); the first of rank 16 15 - 17 with any, of rank 64 27 with
-// two, 40 with one.
-// Of the forward call's first product, 23 with four in one workgroup a CU.
+// with two workgroups a CU.  8192 rows, eight adapters, 4096 to 11008, bf16, us by trace, with one, two and four: the
+// forward call's second product of rank 16 76, 71 and 78, of rank 32 84, 74 and 79, of rank 64 123, 96 and 90, its first
+// of rank 16 22, 20 and 17, of rank 64 41, 28 and 23; all of the gradients of rank 16 147, 142 and 168, of rank 64 244,
+// 235 and 445 (registers spill).
 inline int lora_row_tiles(int M, int E, int rank, bool forward) {
   if (M / E <= 24 || rank > 128) return 1;
   return forward && rank > 32 && rank <= 64 ? 4 : 2;
@@ -22,7 +21,7 @@ inline int lora_row_tiles(int M, int E, int rank, bool forward) {
 // Rows times splits of the first products' parts, at most, wherever there is more than one.
 constexpr int kPartRows = 16384;
 
-// Parts of the columns in a first product: enough for two workgroups a CU, of 512 columns or more.
+// Parts of the columns in a first product: as many as leave at most two workgroups a CU, of 512 columns or more.
 inline int shrink_splits(int M, int E, int rank, int C, bool forward) {
   if (M == 0) return 1;
   const long long tiles = max_row_tiles(M, E, 16 * lora_row_tiles(M, E, rank, forward));
@@ -43,8 +42,9 @@ inline long long shrink_blocks(bool forward, const ShrinkArgs& s) {
   return max_row_tiles(s.plan.M, s.plan.E, 16 * lora_row_tiles(s.plan.M, s.plan.E, s.rank, forward)) * s.splits;
 }
 
-// Spans of the columns in a second product: 1024 columns (8192 x 11008, rank 64 84 us, 512 columns 88, 768 92,
-// 2816 92), down to 256 where there are fewer than two workgroups a CU.
+// Spans of the columns in a second product: 1024 columns (8192 x 11008, bf16, 512, 768, 1024 and 2816 columns: rank 16
+// 71, 69, 71 and 75 us, rank 32 74, 74, 74 and 77, rank 64 95, 96, 90 and 85), down to 256 where there are fewer than two
+// workgroups a CU.
 inline ExpandArgs expand_of(bool forward, const ShrinkArgs& f, const void* w, int N, const float* scales,
                             const void* base, void* y) {
   ExpandArgs s{f.plan, f.parts, f.splits, f.rank, N, w, scales, base, y, 0, 0, 0, 0};
@@ -62,7 +62,10 @@ inline long long expand_blocks(const ExpandArgs& s) {
 }
 
 // Parts of an adapter's rows in the gradients of A and B: as many as make two workgroups a CU at least, of 128 rows
-// or more if the rows are even (4060 rows of 8, 5784 columns: the second launch 55 us with two parts, 74 with one).
+// or more if the rows are even.  They pay for their sum where the rows are uneven or the adapters few: a call on uneven
+// rows, bf16, us, in 1, 2, 4 and 8 parts: 4096 rows of 4, rank 16, 4096 to 4096 72, 57, 55 (the rule's) and 59; 2000 of
+// 2, rank 16, 2048 to 2048 57, 37, 27 and 26 (seven: 26); 4060 of 8, rank 64, 5784 to 1032 106, 101 (the rule's), 110 and
+// 130, but 5784 to 5784 127, 144 (the rule's), 163 and 200.
 inline int grad_splits(int M, int E, int C) {
   const long long tiles = (long long)E * ceil_div(C, 128);
   long long s = ceil_div(512, tiles);

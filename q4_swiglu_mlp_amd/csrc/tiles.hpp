@@ -21,15 +21,15 @@ __device__ __forceinline__ Buffer tile_buffer(const uint8_t* p, int bytes) {
 __device__ __forceinline__ void to_lds(Buffer b, int off, uint8_t* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
 }
-// The same out of the compiler's sight, which would wait for all copies before every transposing read: whoever
-// reads the tile waits for them by count.  (m0 is for such copies alone on gfx950; a kernel has them of one kind.)
-// The bounded buffer as its four words (the same for the wave).
+// A bounded buffer as its four words (the same for the wave).
 __device__ __forceinline__ i32x4_t buffer_words(const uint8_t* p, int bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(p);
   return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
                  __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
                  __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
+// to_lds out of the compiler's sight, which would wait for all copies before every transposing read: whoever
+// reads the tile waits for them by count.  (m0 is for such copies alone on gfx950; a kernel has them of one kind.)
 __device__ __forceinline__ void copy_to_lds(i32x4_t b, int off, const uint8_t* dst) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)dst;
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
