@@ -111,7 +111,8 @@ def test_a_scale_without_rows_is_not_used(kind, M, E, K, N):
 
 # ---------------------------------------------------------------- SwiGLU's gradients, factors at both ends of the range
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("d,u", [(-70, 60), (-99, 119), (-126, 127), (60, -70), (127, -126), (127, 127), (0, 0), (90, 100)])
+@pytest.mark.parametrize("d,u", [(-70, 60), (-99, 119), (-126, 127), (60, -70), (127, -126), (127, 127), (0, 0), (90, 100), (-132, 127),
+                                 (127, -132)])
 def test_swiglu_gradients_of_factors_at_both_ends(kind, d, u):
     """dh and up so far apart that a product of some of the factors leaves fp32's range where dgate does not."""
     rng = np.random.default_rng(5)
