@@ -499,8 +499,9 @@ int zinc_swiglu_backward(const void* dh, const void* gate, const void* up, int32
  * (zeros for an adapter without rows, whatever its scale, also where M is 0).  The gradient of base is dy itself.
  * dx, da or db may be NULL: it is then not computed.
  * A x and dh are kept in fp32; where they are operands again they are split in 16-bit terms (three in bf16, which
- * are the value itself, two in fp16, 22 bits of it), sums are fp32 and results are rounded once.  Nothing depends on
- * the order of the GPU's work: equal inputs give equal bits.
+ * are the value itself, two in fp16, 22 bits of it), sums are fp32 and results are rounded once.  An infinity that
+ * meets such an operand (b's in y, a's in dx, x's in da, dy's in db) may give NaN where the formula gives an infinity.
+ * Nothing depends on the order of the GPU's work: equal inputs give equal bits.
  * K and N: multiples of 8 up to 65536, rank a multiple of 8 up to 256 (else ZINC_ERR_SHAPE); M <= 2^24,
  * n_adapters <= 1024 (else ZINC_ERR_ARG).  Matrices and the workspace are 16-byte aligned, scales and the
  * plan 4.  The workspace sizes are non-decreasing in M.
