@@ -10,10 +10,10 @@ reciprocal) = 6, silu(z) u by 6 + 2 products = 8 (powers of two are exact) and d
 off by 3 + 6 + 1 = 10, so 1 + z (1 - s) by 10 + 1 of the sum of its terms' magnitudes, and dgate by 6 + 11 + 3
 products = 20 of that.
 
-Adapters: A x and dh are sums as above; two 16-bit terms of them are off by (half a step)^2: 2^-16 of a
+Adapters: A x and dh are sums as above; as operands they are two 16-bit terms, off by (half a step)^2: 2^-16 of a
 value in bf16, 2^-22 in fp16 and there, where the lower term is subnormal, 2^-38 of the largest value beside it.
-The second sum has two terms for each of its products.  (In bf16 there is a third term, which makes the operand exact:
-test_gpu_rows16_edges.py.)
+The second sum has two terms for each of its products.
+(In bf16 there is a third term now, which makes the operand exact: test_gpu_rows16_edges.py.)
 """
 from __future__ import annotations
 
